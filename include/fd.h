@@ -70,7 +70,8 @@ typedef enum fd_status {
     FD_ERR_WORKSPACE_TOO_SMALL = 3,  /* workspace_bytes below the *_workspace_size() value */
     FD_ERR_BAD_PAGE_TABLE = 4,       /* (device status) a page id outside [0, num_pages) */
     FD_ERR_CUDA = 5,                 /* a CUDA launch or query failed */
-    FD_ERR_DEVICE_TIMEOUT = 6        /* (device status) a pipeline wait hit its time limit */
+    FD_ERR_DEVICE_TIMEOUT = 6,       /* (device status) a pipeline wait hit its time limit */
+    FD_ERR_OUT_OF_PAGES = 7          /* (device status) fd_assign_pages ran past the free pages */
 } fd_status;
 
 typedef enum fd_out_dtype {
@@ -371,6 +372,139 @@ FD_API int fd_decode_paged_fp4(const void* q, const uint8_t* k_pages, const uint
                                void* out, int out_dtype, float* lse,
                                void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Prompts.  Attention of many query tokens per sequence, packed one sequence
+ * behind the other: query token i of a sequence with Lq queries and Lk keys
+ * sees the keys [0, Lk - Lq + i] (causal != 0: the last query at the last
+ * key) or [0, Lk).  With s_j = scale * <q, k_j> over the visible keys,
+ * out = sum_j e^(s_j) v_j / sum_j e^(s_j) and lse = ln sum_j e^(s_j); a query
+ * that sees no key gets out = 0, lse = -inf.  scale must be finite and > 0.
+ * Scores, maxima, sums and outputs are binary32; the weights e^(s - m) enter
+ * the product with V as bf16 (relative rounding at most 2^-8), so out carries up to
+ * 2^-8 of the weighted mean of |v| in error even as float32; lse does not (its sum takes the
+ * weights before that rounding).
+ *   q            [total_q, Hq, d] bf16, tokens q_stride elements apart (a
+ *                multiple of 8, at least Hq * d: a slice of a fused projection
+ *                works); k_stride, v_stride likewise for k, v
+ *   cu_seqlens_q [B + 1] int32, ascending: sequence b owns the query tokens
+ *                cu_seqlens_q[b] .. cu_seqlens_q[b + 1] - 1.  Offsets outside
+ *                [0, total_q] or descending are clamped and recorded in the
+ *                device status (FD_ERR_INVALID_ARG).
+ *   out          [total_q, Hq, d] in out_dtype; lse [total_q, Hq] float32 or
+ *                NULL.  Rows that belong to no sequence are left as they are.
+ *   num_splits   0 = planner; > 0: the keys are cut into that many chunks of
+ *                ceil(max_k / num_splits) rounded up to 128, merged at the end
+ *   workspace    fd_prefill_workspace_size(...) bytes, may be NULL when 0
+ * max_k is total_k for fd_prefill_packed and max_pages * 64 for
+ * fd_prefill_paged. */
+FD_API int fd_prefill_num_splits(int B, int total_q, int Hq, int Hkv, int max_k, int d, int num_splits);
+FD_API size_t fd_prefill_workspace_size(int B, int total_q, int Hq, int Hkv, int max_k, int d, int num_splits);
+
+/* Whole prompts: keys and values packed like the queries.
+ *   k, v         [total_k, Hkv, d] bf16
+ *   cu_seqlens_k [B + 1] int32 (pass cu_seqlens_q for self-attention).
+ * Keys of other sequences, and rows past cu_seqlens_k[B], never influence a
+ * result, whatever they hold.  Keys hidden from a query by the causal mask
+ * have to be finite (a weight of 0 times infinity is NaN). */
+FD_API int fd_prefill_packed(const void* q, const void* k, const void* v,
+                             long long q_stride, long long k_stride, long long v_stride,
+                             const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,
+                             int B, int total_q, int total_k, int Hq, int Hkv, int d,
+                             float scale, int causal, int num_splits,
+                             void* out, int out_dtype, float* lse,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/* Prompt tails over a paged cache that already holds their keys and values
+ * (fd_append_kv_paged): sequence b has seq_lens[b] keys, its queries are the
+ * last ones.  k_pages, v_pages, page_table, seq_lens and page_size as in
+ * fd_decode_paged; a bad page's tokens are skipped and reported the same way.
+ * One query token per sequence gives fd_decode_paged's result. */
+FD_API int fd_prefill_paged(const void* q, const void* k_pages, const void* v_pages, long long q_stride,
+                            const int32_t* page_table, int max_pages, int num_pages,
+                            const int32_t* cu_seqlens_q, const int32_t* seq_lens, int page_size,
+                            int B, int total_q, int Hq, int Hkv, int d,
+                            float scale, int causal, int num_splits,
+                            void* out, int out_dtype, float* lse,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* Decode of one token per sequence for a batch whose sequences start with the
+ * same tokens: the shared keys and values are read once for the whole batch
+ * (every query of the batch against them as one matrix product), each
+ * sequence's own tokens by the split-KV pass, and all partial results are
+ * joined exactly.  The result is that of fd_decode_paged / fd_decode_dense
+ * over the whole sequences; weights of the shared part are bf16 (see the
+ * prompts above).  scale must be finite and > 0.
+ *   num_splits  chunks of the shared tokens, 0 = planner
+ *   workspace   fd_shared_prefix_workspace_size(B, Hq, Hkv, prefix_len, L_own,
+ *               d, num_splits) bytes (never 0): prefix_len = prefix_pages * 64
+ *               and L_own = (max_pages - prefix_pages) * 64 when paged. */
+FD_API size_t fd_shared_prefix_workspace_size(int B, int Hq, int Hkv, int prefix_len, int L_own, int d,
+                                              int num_splits);
+
+/* Paged: token t < prefix_pages * 64 of every sequence is row t % 64 of page
+ * prefix_table[t / 64]; later tokens follow page_table [B, max_pages] as in
+ * fd_decode_paged (whose first prefix_pages entries are not read).  seq_lens
+ * counts all tokens of a sequence, shared ones included; a sequence shorter
+ * than the prefix attends its first seq_lens[b] tokens. */
+FD_API int fd_decode_paged_shared_prefix(const void* q, const void* k_pages, const void* v_pages,
+                                         const int32_t* prefix_table, int prefix_pages,
+                                         const int32_t* page_table, int max_pages, int num_pages,
+                                         const int32_t* seq_lens, int page_size,
+                                         int B, int Hq, int Hkv, int d, float scale, int num_splits,
+                                         void* out, int out_dtype, float* lse,
+                                         void* workspace, size_t workspace_bytes, void* stream);
+
+/* Contiguous: k_prefix, v_prefix [Hkv, prefix_len, d] bf16 come first, then
+ * every sequence's own tokens k, v [B, Hkv, L_max, d] with seq_lens [B] own
+ * tokens (or NULL: L_max), as in fd_decode_dense. */
+FD_API int fd_decode_dense_shared_prefix(const void* q, const void* k_prefix, const void* v_prefix, int prefix_len,
+                                         const void* k, const void* v, const int32_t* seq_lens,
+                                         int B, int Hq, int Hkv, int L_max, int d, float scale, int num_splits,
+                                         void* out, int out_dtype, float* lse,
+                                         void* workspace, size_t workspace_bytes, void* stream);
+
+/* Pages and slots for the new tokens of a batch, without the host knowing the
+ * lengths.  Sequence b has cached_lens[b] tokens in its pages and gets
+ * new_lens[b] more; with before = ceil(cached / 64) and after =
+ * ceil((cached + new) / 64), in the order of (sequence, page):
+ *   page_table[b, before .. after - 1] = the next entries of free_pages, from
+ *                   entry free_head[0] on (free_head NULL: from 0); the other
+ *                   entries of the table are left as they are
+ *   seq_lens[b]     = cached_lens[b] + new_lens[b]   (may be cached_lens itself)
+ *   cu_seqlens      [B + 1]: offsets of the sequences' new tokens
+ *   slots[t]        = page_table[b, pos / 64] * 64 + pos % 64 for the new token
+ *                   t = cu_seqlens[b] + i of sequence b, pos = cached_lens[b] + i;
+ *                   -1 behind the last new token, up to total_new (a padded batch)
+ *   free_head_out[0] = entries of free_pages used up (may be free_head itself)
+ * slots [total_new] must be 16-byte aligned.  Where free_pages [num_free] runs
+ * out, table entries and slots become -1 and the device status records
+ * FD_ERR_OUT_OF_PAGES; lengths below 0, beyond max_pages * 64, or adding up to
+ * more than total_new are cut (slots -1, or not written) and recorded as
+ * FD_ERR_INVALID_ARG. */
+FD_API int fd_assign_pages(const int32_t* cached_lens, const int32_t* new_lens, int B,
+                           int32_t* page_table, int max_pages, int page_size,
+                           const int32_t* free_pages, int num_free, const int32_t* free_head, int total_new,
+                           int32_t* seq_lens, int32_t* cu_seqlens, int64_t* slots, int32_t* free_head_out,
+                           void* stream);
+
+/* New key and value rows into a paged cache: row h of token t goes to row
+ * slots[t] % 64 of page slots[t] / 64, head h.
+ *   k, v     [T, Hkv, d] bf16, tokens k_stride / v_stride elements apart
+ *   slots    [T] int64 (fd_assign_pages); a negative slot is skipped; one
+ *            outside the pool is skipped and recorded (FD_ERR_BAD_PAGE_TABLE).
+ *            Slots of one call must differ from each other.
+ *   k_pages, v_pages [num_pages, Hkv, 64, d] bf16 */
+FD_API int fd_append_kv_paged(const void* k, const void* v, long long k_stride, long long v_stride,
+                              const int64_t* slots, int T, int Hkv, int d,
+                              void* k_pages, void* v_pages, int num_pages, int page_size, void* stream);
+
+/* The same into the paged fp8 cache of fd_decode_paged_fp8, each row encoded
+ * as by fd_quantize_kv_fp8 (the same bytes). */
+FD_API int fd_append_kv_paged_fp8(const void* k, const void* v, long long k_stride, long long v_stride,
+                                  const int64_t* slots, int T, int Hkv, int d,
+                                  uint8_t* k_pages, float* k_page_scales, uint8_t* v_pages, float* v_page_scales,
+                                  int num_pages, int page_size, void* stream);
+
 /* Size of the fixed device scratch array used by fd_decode_dense_noalloc. */
 #define FD_NOALLOC_SCRATCH_BYTES (4u << 20)
 
@@ -415,9 +549,9 @@ FD_API int fd_decode_dense_noalloc(const void* q, const void* k, const void* v,
 FD_API int fd_debug_inject_wait_timeout(unsigned long long wait_limit_ns, int withhold_tile);
 
 /* Synchronises `stream`, then reports the device status word of the current
- * device: FD_ERR_DEVICE_TIMEOUT, FD_ERR_BAD_PAGE_TABLE, FD_ERR_INVALID_ARG (a
- * seq_lens entry outside [0, L_max]; the kernels clamped it) or FD_OK, in
- * that order of precedence (FD_ERR_CUDA if the synchronisation itself
+ * device: FD_ERR_DEVICE_TIMEOUT, FD_ERR_BAD_PAGE_TABLE, FD_ERR_OUT_OF_PAGES,
+ * FD_ERR_INVALID_ARG (a seq_lens entry outside [0, L_max], or an offset or
+ * length of the prompt calls; the kernels clamped it) or FD_OK, in that order of precedence (FD_ERR_CUDA if the synchronisation itself
  * failed).  clear != 0 resets the word afterwards. */
 FD_API int fd_device_status(int clear, void* stream);
 

@@ -25,8 +25,11 @@ __all__ = [
     "fd_decode_paged_fp8", "fd_quantize_kv_fp4", "fd_num_splits_fp4", "fd_decode_fp4_workspace_size",
     "fd_decode_dense_fp4", "fd_decode_paged_fp4", "fd_decode_dense_unified", "fd_decode_paged_unified",
     "fd_decode_topdelta_group_union", "fd_debug_inject_wait_timeout", "fd_quantize_v_fp4",
+    "fd_prefill_num_splits", "fd_prefill_workspace_size", "fd_prefill_packed", "fd_prefill_paged",
+    "fd_shared_prefix_workspace_size", "fd_decode_paged_shared_prefix", "fd_decode_dense_shared_prefix",
+    "fd_assign_pages", "fd_append_kv_paged", "fd_append_kv_paged_fp8",
     "FD_OK", "FD_ERR_INVALID_ARG", "FD_ERR_UNSUPPORTED", "FD_ERR_WORKSPACE_TOO_SMALL",
-    "FD_ERR_BAD_PAGE_TABLE", "FD_ERR_CUDA", "FD_ERR_DEVICE_TIMEOUT", "FD_OUT_F32", "FD_OUT_BF16",
+    "FD_ERR_BAD_PAGE_TABLE", "FD_ERR_CUDA", "FD_ERR_DEVICE_TIMEOUT", "FD_ERR_OUT_OF_PAGES", "FD_OUT_F32", "FD_OUT_BF16",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -40,6 +43,7 @@ FD_ERR_WORKSPACE_TOO_SMALL = 3
 FD_ERR_BAD_PAGE_TABLE = 4
 FD_ERR_CUDA = 5
 FD_ERR_DEVICE_TIMEOUT = 6
+FD_ERR_OUT_OF_PAGES = 7
 FD_OUT_F32 = 0
 FD_OUT_BF16 = 1
 
@@ -68,6 +72,7 @@ def open_library(path: str):
         raise ImportError(f"libfd.so not built at {path}; run long_context_decode_split_gb300._build.build()")
     lib = ctypes.CDLL(path)
     P, I, F, S = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+    N = ctypes.c_longlong
     sig = {
         "fd_abi_version": (I, []),
         "fd_status_string": (ctypes.c_char_p, [I]),
@@ -96,6 +101,16 @@ def open_library(path: str):
         "fd_decode_fp4_workspace_size": (S, [I, I, I, I, I, I, I]),
         "fd_decode_dense_fp4": (I, [P, P, P, P, P, P, I, I, I, I, I, F, I, P, I, P, P, S, P]),
         "fd_decode_paged_fp4": (I, [P, P, P, P, P, P, I, I, P, I, I, I, I, I, F, I, P, I, P, P, S, P]),
+        "fd_prefill_num_splits": (I, [I, I, I, I, I, I, I]),
+        "fd_prefill_workspace_size": (S, [I, I, I, I, I, I, I]),
+        "fd_prefill_packed": (I, [P, P, P, N, N, N, P, P, I, I, I, I, I, I, F, I, I, P, I, P, P, S, P]),
+        "fd_prefill_paged": (I, [P, P, P, N, P, I, I, P, P, I, I, I, I, I, I, F, I, I, P, I, P, P, S, P]),
+        "fd_shared_prefix_workspace_size": (S, [I, I, I, I, I, I, I]),
+        "fd_decode_paged_shared_prefix": (I, [P, P, P, P, I, P, I, I, P, I, I, I, I, I, F, I, P, I, P, P, S, P]),
+        "fd_decode_dense_shared_prefix": (I, [P, P, P, I, P, P, P, I, I, I, I, I, F, I, P, I, P, P, S, P]),
+        "fd_assign_pages": (I, [P, P, I, P, I, I, P, I, P, I, P, P, P, P, P]),
+        "fd_append_kv_paged": (I, [P, P, N, N, P, I, I, I, P, P, I, I, P]),
+        "fd_append_kv_paged_fp8": (I, [P, P, N, N, P, I, I, I, P, P, P, P, I, I, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -599,6 +614,263 @@ def fd_decode_paged_fp4(q, k_pages, k_page_scales, v_pages, v_page_scales, page_
     [P,Hkv,64,d/32] uint8."""
     return _decode_paged_q("fp4", q, k_pages, k_page_scales, v_pages, v_page_scales, page_table, num_pages,
                            seq_lens, scale, num_splits, out, lse, out_dtype, want_lse, workspace, stream)
+
+
+def _check_tokens(t, name, H=None, d=None):
+    """[T, H, d] bf16 whose tokens may lie further apart than H * d elements (a
+    slice of a fused projection); returns the token stride in elements."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    dev = torch.cuda.current_device()
+    if t.device.index != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev} (the first tensor's device)")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 3 or (H is not None and t.shape[1] != H) or (d is not None and t.shape[2] != d):
+        raise ValueError(f"{name} must be [tokens, {'heads' if H is None else H}, {'d' if d is None else d}], "
+                         f"got {tuple(t.shape)}")
+    T, H, d = t.shape
+    row = H * d
+    if t.numel() and ((d > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != d)):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    stride = t.stride(0) if T > 1 else row
+    if stride < row:
+        raise ValueError(f"{name}: tokens must not overlap")
+    return stride
+
+
+def _check_offsets(t, name, B=None):
+    _check_cuda(t, name, torch.int32, None if B is None else (B + 1,))
+    _need(t.dim() == 1 and t.numel() >= 1, f"{name} must be [B + 1]")
+
+
+def fd_prefill_num_splits(B, total_q, Hq, Hkv, max_k, d, num_splits=0) -> int:
+    r = int(load().fd_prefill_num_splits(B, total_q, Hq, Hkv, max_k, d, num_splits))
+    if r < 0:
+        raise FdError(-r, "fd_prefill_num_splits")
+    return r
+
+
+def fd_prefill_workspace_size(B, total_q, Hq, Hkv, max_k, d, num_splits=0) -> int:
+    return int(load().fd_prefill_workspace_size(B, total_q, Hq, Hkv, max_k, d, num_splits))
+
+
+@_on_device_of_first_tensor
+def fd_prefill_packed(q, k, v, cu_seqlens_q, cu_seqlens_k=None, scale=None, causal=True, num_splits=0, out=None,
+                      lse=None, out_dtype="bf16", want_lse=True, workspace=None, stream=None):
+    """Attention of whole prompts packed one behind the other.  q [Tq,Hq,d],
+    k, v [Tk,Hkv,d] bf16 (tokens may be strided), cu_seqlens_q [B+1] int32,
+    cu_seqlens_k [B+1] or None (= cu_seqlens_q).  Returns (out [Tq,Hq,d],
+    lse [Tq,Hq] or None); rows of no sequence are not written."""
+    lib = load()
+    qs = _check_tokens(q, "q")
+    Tq, Hq, d = q.shape
+    ks = _check_tokens(k, "k", None, d)
+    Tk, Hkv, _ = k.shape
+    vs = _check_tokens(v, "v", Hkv, d)
+    _need(v.shape[0] == Tk, "k and v must have the same number of tokens")
+    _check_offsets(cu_seqlens_q, "cu_seqlens_q")
+    B = cu_seqlens_q.numel() - 1
+    if cu_seqlens_k is None:
+        cu_seqlens_k = cu_seqlens_q
+    _check_offsets(cu_seqlens_k, "cu_seqlens_k", B)
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    code, out, lse = _outputs(Tq, Hq, d, q.device, out, lse, out_dtype, want_lse)
+    ws = _workspace(fd_prefill_workspace_size(B, Tq, Hq, Hkv, Tk, d, num_splits), q.device, workspace)
+    st = lib.fd_prefill_packed(_p(q), _p(k), _p(v), qs, ks, vs, _p(cu_seqlens_q), _p(cu_seqlens_k), B, Tq, Tk, Hq, Hkv,
+                               d, scale, int(bool(causal)), int(num_splits), _p(out), code, _p(lse), _p(ws),
+                               0 if ws is None else ws.numel() * ws.element_size(), _stream(stream))
+    _raise(st, "fd_prefill_packed")
+    return out, lse
+
+
+def _check_pool(k_pages, v_pages, d):
+    _check_cuda(k_pages, "k_pages", torch.bfloat16)
+    _need(k_pages.dim() == 4 and k_pages.shape[3] == d, "k_pages must be [P, Hkv, page, d]")
+    _check_cuda(v_pages, "v_pages", torch.bfloat16, k_pages.shape)
+    return k_pages.shape[1], k_pages.shape[2]
+
+
+@_on_device_of_first_tensor
+def fd_prefill_paged(q, k_pages, v_pages, page_table, num_pages, cu_seqlens_q, seq_lens, scale=None, causal=True,
+                     num_splits=0, out=None, lse=None, out_dtype="bf16", want_lse=True, workspace=None, stream=None):
+    """Attention of prompt tails over a paged cache that holds their keys and
+    values.  q [Tq,Hq,d] bf16 (tokens may be strided), k_pages/v_pages
+    [P,Hkv,64,d] bf16, page_table [B,max_pages] int32, cu_seqlens_q [B+1]
+    int32, seq_lens [B] int32 (all keys; the queries are the last ones)."""
+    lib = load()
+    qs = _check_tokens(q, "q")
+    Tq, Hq, d = q.shape
+    Hkv, page_size = _check_pool(k_pages, v_pages, d)
+    _check_offsets(cu_seqlens_q, "cu_seqlens_q")
+    B = cu_seqlens_q.numel() - 1
+    _check_cuda(page_table, "page_table", torch.int32)
+    _need(page_table.dim() == 2 and page_table.shape[0] == B, "page_table must be [B, max_pages]")
+    max_pages = page_table.shape[1]
+    _check_cuda(seq_lens, "seq_lens", torch.int32, (B,))
+    _need(0 <= int(num_pages) <= k_pages.shape[0], "num_pages must be within the pool")
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    code, out, lse = _outputs(Tq, Hq, d, q.device, out, lse, out_dtype, want_lse)
+    ws = _workspace(fd_prefill_workspace_size(B, Tq, Hq, Hkv, max_pages * page_size, d, num_splits), q.device,
+                    workspace)
+    st = lib.fd_prefill_paged(_p(q), _p(k_pages), _p(v_pages), qs, _p(page_table), max_pages, int(num_pages),
+                              _p(cu_seqlens_q), _p(seq_lens), page_size, B, Tq, Hq, Hkv, d, scale, int(bool(causal)),
+                              int(num_splits), _p(out), code, _p(lse), _p(ws),
+                              0 if ws is None else ws.numel() * ws.element_size(), _stream(stream))
+    _raise(st, "fd_prefill_paged")
+    return out, lse
+
+
+def fd_shared_prefix_workspace_size(B, Hq, Hkv, prefix_len, L_own, d, num_splits=0) -> int:
+    return int(load().fd_shared_prefix_workspace_size(B, Hq, Hkv, prefix_len, L_own, d, num_splits))
+
+
+@_on_device_of_first_tensor
+def fd_decode_paged_shared_prefix(q, k_pages, v_pages, prefix_table, page_table, num_pages, seq_lens, scale=None,
+                                  num_splits=0, out=None, lse=None, out_dtype="bf16", want_lse=True, workspace=None,
+                                  stream=None):
+    """fd_decode_paged for a batch whose sequences share their first
+    64 * len(prefix_table) tokens, read once for the whole batch.
+    prefix_table [n] int32 page ids (the first n entries of every page_table
+    row are not read); seq_lens [B] int32 counts all tokens."""
+    lib = load()
+    _check_cuda(q, "q", torch.bfloat16)
+    _need(q.dim() == 3, "q must be [B, Hq, d]")
+    B, Hq, d = q.shape
+    Hkv, page_size = _check_pool(k_pages, v_pages, d)
+    _check_cuda(prefix_table, "prefix_table", torch.int32)
+    _need(prefix_table.dim() == 1, "prefix_table must be [prefix_pages]")
+    _check_cuda(page_table, "page_table", torch.int32)
+    _need(page_table.dim() == 2 and page_table.shape[0] == B, "page_table must be [B, max_pages]")
+    max_pages, n = page_table.shape[1], prefix_table.numel()
+    _need(n <= max_pages, "prefix_table must be no longer than a row of page_table")
+    _check_cuda(seq_lens, "seq_lens", torch.int32, (B,))
+    _need(0 <= int(num_pages) <= k_pages.shape[0], "num_pages must be within the pool")
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    code, out, lse = _outputs(B, Hq, d, q.device, out, lse, out_dtype, want_lse)
+    ws = _workspace(fd_shared_prefix_workspace_size(B, Hq, Hkv, n * page_size, (max_pages - n) * page_size, d,
+                                                    num_splits), q.device, workspace)
+    st = lib.fd_decode_paged_shared_prefix(_p(q), _p(k_pages), _p(v_pages), _p(prefix_table), n, _p(page_table),
+                                           max_pages, int(num_pages), _p(seq_lens), page_size, B, Hq, Hkv, d, scale,
+                                           int(num_splits), _p(out), code, _p(lse), _p(ws),
+                                           0 if ws is None else ws.numel() * ws.element_size(), _stream(stream))
+    _raise(st, "fd_decode_paged_shared_prefix")
+    return out, lse
+
+
+@_on_device_of_first_tensor
+def fd_decode_dense_shared_prefix(q, k_prefix, v_prefix, k, v, seq_lens=None, scale=None, num_splits=0, out=None,
+                                  lse=None, out_dtype="bf16", want_lse=True, workspace=None, stream=None):
+    """fd_decode_dense for a batch whose sequences start with the same tokens:
+    k_prefix, v_prefix [Hkv,P,d] bf16 (read once for the whole batch), then
+    every sequence's own k, v [B,Hkv,L_max,d] with seq_lens [B] int32 own
+    tokens (or None)."""
+    lib = load()
+    _check_cuda(q, "q", torch.bfloat16)
+    _need(q.dim() == 3, "q must be [B, Hq, d]")
+    B, Hq, d = q.shape
+    _check_cuda(k_prefix, "k_prefix", torch.bfloat16)
+    _need(k_prefix.dim() == 3 and k_prefix.shape[2] == d, "k_prefix must be [Hkv, P, d]")
+    Hkv, P, _ = k_prefix.shape
+    _check_cuda(v_prefix, "v_prefix", torch.bfloat16, k_prefix.shape)
+    _check_cuda(k, "k", torch.bfloat16)
+    _need(k.dim() == 4 and k.shape[0] == B and k.shape[1] == Hkv and k.shape[3] == d, "k must be [B, Hkv, L_max, d]")
+    L_max = k.shape[2]
+    _check_cuda(v, "v", torch.bfloat16, k.shape)
+    if seq_lens is not None:
+        _check_cuda(seq_lens, "seq_lens", torch.int32, (B,))
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    code, out, lse = _outputs(B, Hq, d, q.device, out, lse, out_dtype, want_lse)
+    ws = _workspace(fd_shared_prefix_workspace_size(B, Hq, Hkv, P, L_max, d, num_splits), q.device, workspace)
+    st = lib.fd_decode_dense_shared_prefix(_p(q), _p(k_prefix), _p(v_prefix), P, _p(k), _p(v), _p(seq_lens), B, Hq, Hkv,
+                                           L_max, d, scale, int(num_splits), _p(out), code, _p(lse), _p(ws),
+                                           0 if ws is None else ws.numel() * ws.element_size(), _stream(stream))
+    _raise(st, "fd_decode_dense_shared_prefix")
+    return out, lse
+
+
+def _int32_out(t, name, shape, device):
+    if t is None:
+        return torch.empty(shape, dtype=torch.int32, device=device)
+    _check_cuda(t, name, torch.int32, shape)
+    return t
+
+
+@_on_device_of_first_tensor
+def fd_assign_pages(page_table, cached_lens, new_lens, free_pages, total_new, free_head=None, page_size=64,
+                    seq_lens=None, cu_seqlens=None, slots=None, free_head_out=None, stream=None):
+    """Pages and slots for the new tokens of a batch.  page_table [B,max_pages]
+    int32 (its new entries are filled in), cached_lens, new_lens [B] int32,
+    free_pages [F] int32 used in order from entry free_head[0] ([1] int32, or
+    None = 0), total_new the number of slots.  Returns (seq_lens [B],
+    cu_seqlens [B+1], slots [total_new] int64, free_head_out [1]); seq_lens may
+    be cached_lens and free_head_out may be free_head (updated in place)."""
+    lib = load()
+    _check_cuda(page_table, "page_table", torch.int32)
+    _need(page_table.dim() == 2, "page_table must be [B, max_pages]")
+    B, max_pages = page_table.shape
+    _check_cuda(cached_lens, "cached_lens", torch.int32, (B,))
+    _check_cuda(new_lens, "new_lens", torch.int32, (B,))
+    _check_cuda(free_pages, "free_pages", torch.int32)
+    _need(free_pages.dim() == 1, "free_pages must be [F]")
+    if free_head is not None:
+        _check_cuda(free_head, "free_head", torch.int32, (1,))
+    total_new = int(total_new)
+    _need(total_new >= 0, "total_new must be >= 0")
+    dev = page_table.device
+    seq_lens = _int32_out(seq_lens, "seq_lens", (B,), dev)
+    cu_seqlens = _int32_out(cu_seqlens, "cu_seqlens", (B + 1,), dev)
+    free_head_out = _int32_out(free_head_out, "free_head_out", (1,), dev)
+    if slots is None:
+        slots = torch.empty(total_new, dtype=torch.int64, device=dev)
+    _check_cuda(slots, "slots", torch.int64, (total_new,))
+    st = lib.fd_assign_pages(_p(cached_lens), _p(new_lens), B, _p(page_table), max_pages, int(page_size),
+                             _p(free_pages), free_pages.numel(), _p(free_head), total_new, _p(seq_lens),
+                             _p(cu_seqlens), _p(slots), _p(free_head_out), _stream(stream))
+    _raise(st, "fd_assign_pages")
+    return seq_lens, cu_seqlens, slots, free_head_out
+
+
+@_on_device_of_first_tensor
+def fd_append_kv_paged(k, v, slots, k_pages, v_pages, stream=None):
+    """Store new rows k, v [T,Hkv,d] bf16 (tokens may be strided) at slots [T]
+    int64 of the pools k_pages, v_pages [P,Hkv,64,d] bf16 (negative slots are
+    skipped).  Returns (k_pages, v_pages)."""
+    lib = load()
+    ks = _check_tokens(k, "k")
+    T, Hkv, d = k.shape
+    vs = _check_tokens(v, "v", Hkv, d)
+    _need(v.shape[0] == T, "k and v must have the same number of tokens")
+    _check_cuda(slots, "slots", torch.int64, (T,))
+    heads, page_size = _check_pool(k_pages, v_pages, d)
+    _need(heads == Hkv, "k_pages must have the heads of k")
+    st = lib.fd_append_kv_paged(_p(k), _p(v), ks, vs, _p(slots), T, Hkv, d, _p(k_pages), _p(v_pages),
+                                k_pages.shape[0], page_size, _stream(stream))
+    _raise(st, "fd_append_kv_paged")
+    return k_pages, v_pages
+
+
+@_on_device_of_first_tensor
+def fd_append_kv_paged_fp8(k, v, slots, k_pages, k_page_scales, v_pages, v_page_scales, stream=None):
+    """fd_append_kv_paged into the paged fp8 cache: k_pages, v_pages [P,Hkv,64,d]
+    uint8 codes, k_page_scales, v_page_scales [P,Hkv,64] float32; rows are
+    encoded as by fd_quantize_kv_fp8."""
+    lib = load()
+    ks = _check_tokens(k, "k")
+    T, Hkv, d = k.shape
+    vs = _check_tokens(v, "v", Hkv, d)
+    _need(v.shape[0] == T, "k and v must have the same number of tokens")
+    _check_cuda(slots, "slots", torch.int64, (T,))
+    _check_cuda(k_pages, "k_pages", torch.uint8)
+    _need(k_pages.dim() == 4 and k_pages.shape[1] == Hkv and k_pages.shape[3] == d, "k_pages must be [P, Hkv, page, d]")
+    P, _, page_size, _ = k_pages.shape
+    _check_cuda(v_pages, "v_pages", torch.uint8, k_pages.shape)
+    _check_cuda(k_page_scales, "k_page_scales", torch.float32, (P, Hkv, page_size))
+    _check_cuda(v_page_scales, "v_page_scales", torch.float32, (P, Hkv, page_size))
+    st = lib.fd_append_kv_paged_fp8(_p(k), _p(v), ks, vs, _p(slots), T, Hkv, d, _p(k_pages), _p(k_page_scales),
+                                    _p(v_pages), _p(v_page_scales), P, page_size, _stream(stream))
+    _raise(st, "fd_append_kv_paged_fp8")
+    return k_pages, k_page_scales, v_pages, v_page_scales
 
 
 def fd_debug_inject_wait_timeout(wait_limit_ns=0, withhold_tile=-1) -> int:

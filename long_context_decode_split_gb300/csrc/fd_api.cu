@@ -326,9 +326,389 @@ int paged_entry(Cache cache, const void* q, const void* k_pages, const void* v_p
     return decode_common(a, num_splits, true, out_dtype, workspace, workspace_bytes, stream, cache);
 }
 
+// ---------------------------------------------------------------------------
+// Attention of packed query rows (prompts, prompt tails) and the decode of a
+// batch with a shared prefix.
+
+// Chunks of the keys for `ctas` CTAs per chunk: one while those fill the SMs
+// twice, else enough chunks for about four CTAs per SM (sequences are ragged
+// and the causal triangle halves the work of a whole prompt), each of at least
+// 512 keys.
+struct RowsPlan {
+    int splits, chunk;
+};
+
+RowsPlan rows_plan(long long ctas, int max_k, int requested) {
+    const int sms = requested > 0 ? 0 : current_sm_count();
+    long long want = requested;
+    if (requested <= 0) {
+        want = 1;
+        if (sms > 0 && ctas > 0 && ctas < 2LL * sms) want = (4LL * sms + ctas - 1) / ctas;
+        const long long most = max_k / 512;
+        if (want > most) want = most;
+        if (want < 1) want = 1;
+    }
+    long long chunk = (max_k + want - 1) / want;
+    chunk = (chunk + 127) / 128 * 128;
+    if (chunk < 128) chunk = 128;
+    RowsPlan pl;
+    pl.chunk = (int)chunk;
+    pl.splits = requested > 0 ? requested : (int)((max_k + chunk - 1) / chunk);
+    if (pl.splits < 1) pl.splits = 1;
+    return pl;
+}
+
+int check_rows(int B, int total_q, int Hq, int Hkv, int max_k, int d, int num_splits) {
+    const int st = check_shape(B, Hq, Hkv, max_k, d);
+    if (st != FD_OK) return st;
+    if (total_q < 0 || total_q > (1 << 30) || num_splits < 0 || num_splits > 65535) return FD_ERR_INVALID_ARG;
+    // grid x and the row indices of the tile copies are 32-bit
+    if (fd::rows_tiles(B, total_q, Hq / Hkv) * Hkv > 0x7fffffffLL) return FD_ERR_UNSUPPORTED;
+    return FD_OK;
+}
+
+RowsPlan prefill_plan(int B, int total_q, int Hq, int Hkv, int max_k, int num_splits) {
+    return rows_plan(fd::rows_tiles(B, total_q, Hq / Hkv) * Hkv, max_k, num_splits);
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// A token stride covers the token's heads and keeps 16-byte rows.
+bool stride_ok(long long s, int H, int d) { return s >= (long long)H * d && s % 8 == 0 && s <= (1LL << 32); }
+
+int prefill_entry(fd::RowsArgs& a, int num_splits, int out_dtype, void* workspace, size_t workspace_bytes,
+                  void* stream) {
+    const int st = check_rows(a.B, a.total_q, a.Hq, a.Hkv, a.max_k, a.D, num_splits);
+    if (st != FD_OK) return st;
+    if (out_dtype != FD_OUT_F32 && out_dtype != FD_OUT_BF16) return FD_ERR_INVALID_ARG;
+    if (!(a.scale > 0.f) || !std::isfinite(a.scale)) return FD_ERR_INVALID_ARG;
+    if (!stride_ok(a.q_stride, a.Hq, a.D)) return FD_ERR_INVALID_ARG;
+    const bool some = a.B > 0 && a.total_q > 0;
+    if (some && (!a.q || !a.out || !a.cu_q)) return FD_ERR_INVALID_ARG;
+    if (!aligned16(a.q) || !aligned16(a.k) || !aligned16(a.v) || !aligned16(a.out)) return FD_ERR_INVALID_ARG;
+    if (!aligned4(a.lse) || !aligned4(a.cu_q) || !aligned4(a.cu_k) || !aligned4(a.seq_lens) ||
+        !aligned4(a.page_table))
+        return FD_ERR_INVALID_ARG;
+    const RowsPlan pl = prefill_plan(a.B, a.total_q, a.Hq, a.Hkv, a.max_k, num_splits);
+    const size_t need = fd::decode_workspace_bytes(a.total_q, a.Hq, a.D, pl.splits);
+    if (need > 0) {
+        if (!workspace || workspace_bytes < need) return FD_ERR_WORKSPACE_TOO_SMALL;
+        if (!aligned16(workspace)) return FD_ERR_INVALID_ARG;
+        if ((long long)a.total_q * a.Hq > 0x7fffffffLL) return FD_ERR_UNSUPPORTED;  // the merge's grid
+    }
+    if (!some) return FD_OK;
+    a.splits = pl.splits;
+    a.chunk = pl.chunk;
+    a.out_bf16 = out_dtype == FD_OUT_BF16;
+    a.direct = pl.splits == 1;
+    a.rec0 = 0;
+    a.rec_stride = pl.splits;
+    a.part_o = static_cast<float*>(workspace);
+    a.part_ml = need ? a.part_o + (size_t)a.total_q * a.Hq * pl.splits * a.D : nullptr;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = fd::launch_rows(a, s);
+    if (e != cudaSuccess || a.direct) return to_status(e);
+    // every record of a row is written: a merge over `splits` chunks of a full row
+    return to_status(fd::launch_merge(a.part_o, a.part_ml, nullptr, a.total_q, a.Hq, pl.splits * kTile, a.D,
+                                      pl.splits, kTile, a.out, a.out_bf16, a.lse, s));
+}
+
+// The two parts of a shared-prefix decode: chunks of the shared tokens, then
+// chunks of every sequence's own tokens, in one list of partials.
+struct SharedPlan {
+    RowsPlan shared;
+    Plan own;
+    int list;  // records per (sequence, query head)
+};
+
+SharedPlan shared_plan(int B, int Hq, int Hkv, int prefix_len, int L_own, int d, int num_splits) {
+    SharedPlan s;
+    s.shared = rows_plan(fd::rows_tiles(1, B, Hq / Hkv) * Hkv, prefix_len, num_splits);
+    s.own = decode_plan(B, Hq, Hkv, L_own, d, 0, true);
+    s.list = s.shared.splits + (L_own > 0 ? s.own.splits : 0);
+    return s;
+}
+
+int check_shared(int B, int Hq, int Hkv, int prefix_len, int L_own, int d, int num_splits) {
+    if (prefix_len < 0 || prefix_len > (1 << 30) || L_own < 0 || L_own > (1 << 30)) return FD_ERR_INVALID_ARG;
+    const int st = check_shape(B, Hq, Hkv, L_own, d);
+    return st != FD_OK ? st : check_rows(1, B, Hq, Hkv, prefix_len, d, num_splits);
+}
+
+// r: the shared part (keys, layout); o: the decode of every sequence's own tokens.
+int shared_entry(fd::RowsArgs& r, fd::DecodeArgs& o, int prefix_len, int L_own, int num_splits, int out_dtype,
+                 void* workspace, size_t workspace_bytes, void* stream) {
+    if (out_dtype != FD_OUT_F32 && out_dtype != FD_OUT_BF16) return FD_ERR_INVALID_ARG;
+    if (!(o.scale > 0.f) || !std::isfinite(o.scale)) return FD_ERR_INVALID_ARG;
+    if (o.B > 0 && (!o.q || !o.out)) return FD_ERR_INVALID_ARG;
+    if (o.B > 0 && prefix_len > 0 && (!r.k || !r.v)) return FD_ERR_INVALID_ARG;
+    if (o.B > 0 && L_own > 0 && (!o.k || !o.v)) return FD_ERR_INVALID_ARG;
+    if (!aligned16(o.q) || !aligned16(o.k) || !aligned16(o.v) || !aligned16(o.out) || !aligned16(r.k) ||
+        !aligned16(r.v))
+        return FD_ERR_INVALID_ARG;
+    if (!aligned4(o.lse) || !aligned4(o.seq_lens) || !aligned4(o.page_table) || !aligned4(r.page_table))
+        return FD_ERR_INVALID_ARG;
+    // tile copies address cache rows with 32-bit coordinates
+    const long long own_rows = o.page_table ? (long long)o.num_pages * o.Hkv * kTile : (long long)o.B * o.Hkv * L_own;
+    if (own_rows > 0x7fffffffLL) return FD_ERR_UNSUPPORTED;
+    const SharedPlan pl = shared_plan(o.B, o.Hq, o.Hkv, prefix_len, L_own, o.D, num_splits);
+    const size_t need = fd::decode_workspace_bytes(o.B, o.Hq, o.D, pl.list < 2 ? 2 : pl.list);
+    if (!workspace || workspace_bytes < need) return FD_ERR_WORKSPACE_TOO_SMALL;
+    if (!aligned16(workspace)) return FD_ERR_INVALID_ARG;
+    if (o.B == 0) return FD_OK;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    float* ws = static_cast<float*>(workspace);
+    float* ml = ws + (size_t)o.B * o.Hq * pl.list * o.D;
+    const int out_bf16 = out_dtype == FD_OUT_BF16;
+    r.q = o.q;
+    r.q_stride = (long long)o.Hq * o.D;
+    r.B = 1;
+    r.total_q = o.B;
+    r.Hq = o.Hq;
+    r.Hkv = o.Hkv;
+    r.D = o.D;
+    r.max_k = prefix_len;
+    r.total_k = prefix_len;
+    r.scale = o.scale;
+    r.splits = pl.shared.splits;
+    r.chunk = pl.shared.chunk;
+    r.part_o = ws;
+    r.part_ml = ml;
+    r.rec0 = 0;
+    r.rec_stride = pl.list;
+    cudaError_t e = fd::launch_rows(r, s);
+    if (e != cudaSuccess) return to_status(e);
+    if (L_own > 0) {
+        o.splits = pl.own.splits;
+        o.chunk_fixed = pl.own.chunk_fixed;
+        o.out_bf16 = out_bf16;
+        o.part_o = ws;
+        o.part_ml = ml;
+        o.list_splits = pl.list;
+        o.rec0 = pl.shared.splits;
+        e = fd::launch_decode(o, s);
+        if (e != cudaSuccess) return to_status(e);
+    }
+    return to_status(fd::launch_merge(ws, ml, nullptr, o.B, o.Hq, pl.list * kTile, o.D, pl.list, kTile, o.out,
+                                      out_bf16, o.lse, s));
+}
+
 }  // namespace
 
 extern "C" {
+
+int fd_prefill_num_splits(int B, int total_q, int Hq, int Hkv, int max_k, int d, int num_splits) {
+    const int st = check_rows(B, total_q, Hq, Hkv, max_k, d, num_splits);
+    if (st != FD_OK) return -st;
+    return prefill_plan(B, total_q, Hq, Hkv, max_k, num_splits).splits;
+}
+
+size_t fd_prefill_workspace_size(int B, int total_q, int Hq, int Hkv, int max_k, int d, int num_splits) {
+    if (check_rows(B, total_q, Hq, Hkv, max_k, d, num_splits) != FD_OK) return 0;
+    return fd::decode_workspace_bytes(total_q, Hq, d, prefill_plan(B, total_q, Hq, Hkv, max_k, num_splits).splits);
+}
+
+int fd_prefill_packed(const void* q, const void* k, const void* v, long long q_stride, long long k_stride,
+                      long long v_stride, const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int B,
+                      int total_q, int total_k, int Hq, int Hkv, int d, float scale, int causal, int num_splits,
+                      void* out, int out_dtype, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+    if (total_k < 0) return FD_ERR_INVALID_ARG;
+    const int st = check_shape(B, Hq, Hkv, total_k, d);
+    if (st != FD_OK) return st;
+    if (!stride_ok(k_stride, Hkv, d) || !stride_ok(v_stride, Hkv, d)) return FD_ERR_INVALID_ARG;
+    if (B > 0 && total_q > 0 && (!cu_seqlens_k || (total_k > 0 && (!k || !v)))) return FD_ERR_INVALID_ARG;
+    fd::RowsArgs a = {};
+    a.q = q;
+    a.q_stride = q_stride;
+    a.k = k;
+    a.v = v;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.k_head_stride = a.v_head_stride = d;
+    a.cu_q = cu_seqlens_q;
+    a.cu_k = cu_seqlens_k;
+    a.B = B;
+    a.total_q = total_q;
+    a.total_k = total_k;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.D = d;
+    a.max_k = total_k;
+    a.scale = scale;
+    a.causal = causal != 0;
+    a.out = out;
+    a.lse = lse;
+    return prefill_entry(a, num_splits, out_dtype, workspace, workspace_bytes, stream);
+}
+
+int fd_prefill_paged(const void* q, const void* k_pages, const void* v_pages, long long q_stride,
+                     const int32_t* page_table, int max_pages, int num_pages, const int32_t* cu_seqlens_q,
+                     const int32_t* seq_lens, int page_size, int B, int total_q, int Hq, int Hkv, int d, float scale,
+                     int causal, int num_splits, void* out, int out_dtype, float* lse, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+    if (page_size != kTile) return page_size > 0 ? FD_ERR_UNSUPPORTED : FD_ERR_INVALID_ARG;
+    if (max_pages <= 0 || num_pages < 0 || max_pages > (1 << 24)) return FD_ERR_INVALID_ARG;
+    const int st = check_shape(B, Hq, Hkv, max_pages * kTile, d);
+    if (st != FD_OK) return st;
+    if (B > 0 && total_q > 0 && (!page_table || !seq_lens || (num_pages > 0 && (!k_pages || !v_pages))))
+        return FD_ERR_INVALID_ARG;
+    if ((long long)num_pages * Hkv * kTile > 0x7fffffffLL) return FD_ERR_UNSUPPORTED;
+    fd::RowsArgs a = {};
+    a.q = q;
+    a.q_stride = q_stride;
+    a.k = k_pages;
+    a.v = v_pages;
+    a.cu_q = cu_seqlens_q;
+    a.seq_lens = seq_lens;
+    a.page_table = page_table;
+    a.table_stride = max_pages;
+    a.max_pages = max_pages;
+    a.num_pages = num_pages;
+    a.B = B;
+    a.total_q = total_q;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.D = d;
+    a.max_k = max_pages * kTile;
+    a.scale = scale;
+    a.causal = causal != 0;
+    a.out = out;
+    a.lse = lse;
+    return prefill_entry(a, num_splits, out_dtype, workspace, workspace_bytes, stream);
+}
+
+size_t fd_shared_prefix_workspace_size(int B, int Hq, int Hkv, int prefix_len, int L_own, int d, int num_splits) {
+    if (check_shared(B, Hq, Hkv, prefix_len, L_own, d, num_splits) != FD_OK) return 0;
+    const int list = shared_plan(B, Hq, Hkv, prefix_len, L_own, d, num_splits).list;
+    return fd::decode_workspace_bytes(B, Hq, d, list < 2 ? 2 : list);
+}
+
+int fd_decode_dense_shared_prefix(const void* q, const void* k_prefix, const void* v_prefix, int prefix_len,
+                                  const void* k, const void* v, const int32_t* seq_lens, int B, int Hq, int Hkv,
+                                  int L_max, int d, float scale, int num_splits, void* out, int out_dtype, float* lse,
+                                  void* workspace, size_t workspace_bytes, void* stream) {
+    const int st = check_shared(B, Hq, Hkv, prefix_len, L_max, d, num_splits);
+    if (st != FD_OK) return st;
+    fd::RowsArgs r = {};
+    fd::DecodeArgs o = {};
+    r.k = k_prefix;
+    r.v = v_prefix;
+    r.k_stride = r.v_stride = d;
+    r.k_head_stride = r.v_head_stride = (long long)prefix_len * d;
+    o.q = q;
+    o.k = k;
+    o.v = v;
+    o.seq_lens = seq_lens;
+    o.B = B;
+    o.Hq = Hq;
+    o.Hkv = Hkv;
+    o.L_max = L_max;
+    o.D = d;
+    o.scale = scale;
+    o.out = out;
+    o.lse = lse;
+    return shared_entry(r, o, prefix_len, L_max, num_splits, out_dtype, workspace, workspace_bytes, stream);
+}
+
+int fd_decode_paged_shared_prefix(const void* q, const void* k_pages, const void* v_pages,
+                                  const int32_t* prefix_table, int prefix_pages, const int32_t* page_table,
+                                  int max_pages, int num_pages, const int32_t* seq_lens, int page_size, int B, int Hq,
+                                  int Hkv, int d, float scale, int num_splits, void* out, int out_dtype, float* lse,
+                                  void* workspace, size_t workspace_bytes, void* stream) {
+    if (page_size != kTile) return page_size > 0 ? FD_ERR_UNSUPPORTED : FD_ERR_INVALID_ARG;
+    if (max_pages <= 0 || num_pages < 0 || max_pages > (1 << 24)) return FD_ERR_INVALID_ARG;
+    if (prefix_pages < 0 || prefix_pages > max_pages) return FD_ERR_INVALID_ARG;
+    const int prefix_len = prefix_pages * kTile, L_own = (max_pages - prefix_pages) * kTile;
+    const int st = check_shared(B, Hq, Hkv, prefix_len, L_own, d, num_splits);
+    if (st != FD_OK) return st;
+    if (B > 0 && (!page_table || !seq_lens || (prefix_pages > 0 && !prefix_table))) return FD_ERR_INVALID_ARG;
+    if ((long long)num_pages * Hkv * kTile > 0x7fffffffLL) return FD_ERR_UNSUPPORTED;
+    fd::RowsArgs r = {};
+    fd::DecodeArgs o = {};
+    r.k = k_pages;
+    r.v = v_pages;
+    r.page_table = prefix_table ? prefix_table : page_table;  // no shared page: never read
+    r.table_stride = prefix_pages;
+    r.max_pages = prefix_pages;
+    r.num_pages = num_pages;
+    r.row_lens = seq_lens;
+    o.q = q;
+    o.k = k_pages;
+    o.v = v_pages;
+    o.seq_lens = seq_lens;
+    o.page_table = page_table + prefix_pages;
+    o.max_pages = max_pages;
+    o.num_pages = num_pages;
+    o.B = B;
+    o.Hq = Hq;
+    o.Hkv = Hkv;
+    o.L_max = max_pages * kTile;
+    o.D = d;
+    o.scale = scale;
+    o.skip_tokens = prefix_len;
+    o.out = out;
+    o.lse = lse;
+    return shared_entry(r, o, prefix_len, L_own, num_splits, out_dtype, workspace, workspace_bytes, stream);
+}
+
+// ---------------------------------------------------------------------------
+// Page assignment and cache append.
+
+int fd_assign_pages(const int32_t* cached_lens, const int32_t* new_lens, int B, int32_t* page_table, int max_pages,
+                    int page_size, const int32_t* free_pages, int num_free, const int32_t* free_head, int total_new,
+                    int32_t* seq_lens, int32_t* cu_seqlens, int64_t* slots, int32_t* free_head_out, void* stream) {
+    if (page_size != kTile) return page_size > 0 ? FD_ERR_UNSUPPORTED : FD_ERR_INVALID_ARG;
+    if (B < 0 || max_pages <= 0 || max_pages > (1 << 24) || num_free < 0 || total_new < 0) return FD_ERR_INVALID_ARG;
+    if (B > 0 && (!cached_lens || !new_lens || !page_table || !seq_lens)) return FD_ERR_INVALID_ARG;
+    if (!cu_seqlens || !free_head_out || (num_free > 0 && !free_pages) || (total_new > 0 && !slots))
+        return FD_ERR_INVALID_ARG;
+    if (!aligned4(cached_lens) || !aligned4(new_lens) || !aligned4(page_table) || !aligned4(free_pages) ||
+        !aligned4(free_head) || !aligned4(seq_lens) || !aligned4(cu_seqlens) || !aligned16(slots) ||
+        !aligned4(free_head_out))
+        return FD_ERR_INVALID_ARG;
+    fd::AssignArgs a = {cached_lens, new_lens, B, page_table, max_pages, free_pages, num_free, free_head, total_new,
+                        seq_lens, cu_seqlens, slots, free_head_out};
+    return to_status(fd::launch_assign(a, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
+
+namespace {
+
+int append_entry(fd::AppendArgs& a, int page_size, bool fp8, void* stream) {
+    if (page_size != kTile) return page_size > 0 ? FD_ERR_UNSUPPORTED : FD_ERR_INVALID_ARG;
+    if (a.T < 0 || a.num_pages < 0) return FD_ERR_INVALID_ARG;
+    const int st = check_shape(0, a.Hkv, a.Hkv, 0, a.D);
+    if (st != FD_OK) return st;
+    if (!stride_ok(a.k_stride, a.Hkv, a.D) || !stride_ok(a.v_stride, a.Hkv, a.D)) return FD_ERR_INVALID_ARG;
+    if (a.T > 0 && (!a.k || !a.v || !a.slots)) return FD_ERR_INVALID_ARG;
+    if (a.T > 0 && a.num_pages > 0 && (!a.k_pages || !a.v_pages || (fp8 && (!a.k_scales || !a.v_scales))))
+        return FD_ERR_INVALID_ARG;
+    if (!aligned16(a.k) || !aligned16(a.v) || !aligned16(a.k_pages) || !aligned16(a.v_pages) ||
+        !aligned4(a.k_scales) || !aligned4(a.v_scales) || (reinterpret_cast<uintptr_t>(a.slots) & 7u))
+        return FD_ERR_INVALID_ARG;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return to_status(fp8 ? fd::launch_append_fp8(a, s) : fd::launch_append(a, s));
+}
+
+}  // namespace
+
+extern "C" {
+
+int fd_append_kv_paged(const void* k, const void* v, long long k_stride, long long v_stride, const int64_t* slots,
+                       int T, int Hkv, int d, void* k_pages, void* v_pages, int num_pages, int page_size,
+                       void* stream) {
+    fd::AppendArgs a = {k, v, k_stride, v_stride, slots, T, Hkv, d, num_pages, k_pages, v_pages, nullptr, nullptr};
+    return append_entry(a, page_size, false, stream);
+}
+
+int fd_append_kv_paged_fp8(const void* k, const void* v, long long k_stride, long long v_stride,
+                           const int64_t* slots, int T, int Hkv, int d, uint8_t* k_pages, float* k_page_scales,
+                           uint8_t* v_pages, float* v_page_scales, int num_pages, int page_size, void* stream) {
+    fd::AppendArgs a = {k, v, k_stride, v_stride, slots, T, Hkv, d, num_pages, k_pages, v_pages, k_page_scales,
+                        v_page_scales};
+    return append_entry(a, page_size, true, stream);
+}
 
 int fd_abi_version(void) { return FD_ABI_VERSION; }
 
@@ -341,6 +721,7 @@ const char* fd_status_string(int status) {
         case FD_ERR_BAD_PAGE_TABLE: return "FD_ERR_BAD_PAGE_TABLE: a page id was outside the page pool";
         case FD_ERR_CUDA: return "FD_ERR_CUDA: a CUDA call failed";
         case FD_ERR_DEVICE_TIMEOUT: return "FD_ERR_DEVICE_TIMEOUT: a kernel pipeline wait hit its time limit";
+        case FD_ERR_OUT_OF_PAGES: return "FD_ERR_OUT_OF_PAGES: the list of free pages was used up";
         default: return "unknown fd_status";
     }
 }
@@ -588,14 +969,17 @@ int fd_debug_inject_wait_timeout(unsigned long long wait_limit_ns, int withhold_
 
 int fd_device_status(int clear, void* stream) {
     if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return FD_ERR_CUDA;
-    unsigned a = 0, b = 0, c = 0, e = 0;
+    unsigned a = 0, b = 0, c = 0, e = 0, r = 0, g = 0;
     if (fd::decode_status_read(&a, clear != 0) != cudaSuccess) return FD_ERR_CUDA;
     if (fd::topdelta_status_read(&b, clear != 0) != cudaSuccess) return FD_ERR_CUDA;
     if (fd::fp8_status_read(&c, clear != 0) != cudaSuccess) return FD_ERR_CUDA;
     if (fd::fp4_status_read(&e, clear != 0) != cudaSuccess) return FD_ERR_CUDA;
-    const unsigned bits = a | b | c | e;
+    if (fd::rows_status_read(&r, clear != 0) != cudaSuccess) return FD_ERR_CUDA;
+    if (fd::pages_status_read(&g, clear != 0) != cudaSuccess) return FD_ERR_CUDA;
+    const unsigned bits = a | b | c | e | r | g;
     if (bits & 2u) return FD_ERR_DEVICE_TIMEOUT;
     if (bits & 1u) return FD_ERR_BAD_PAGE_TABLE;
+    if (bits & 8u) return FD_ERR_OUT_OF_PAGES;
     if (bits & 4u) return FD_ERR_INVALID_ARG;
     return FD_OK;
 }

@@ -64,6 +64,7 @@ struct PartialParams {
     int Hq, Hkv, L_max, G;
     float scale_log2;
     int splits, chunk_fixed;
+    int skip_tokens;  // leading tokens of every sequence that another pass attends (page_table starts after them)
     float phi2, lo2;  // unified-max variant: phi and phi - kUnifiedRange, log2 units
     unsigned long long wait_limit_ns;  // time limit of every pipeline wait
     int withhold_tile;                 // >= 0: fault injection, that tile of each chunk is never copied
@@ -156,7 +157,7 @@ partial_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
     const int split = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_wait_primary();  // the previous kernel in the stream may still be running
-    const int L = clamped_len(p.seq_lens, b, p.L_max, &g_status_decode);
+    const int L = max(clamped_len(p.seq_lens, b, p.L_max, &g_status_decode) - p.skip_tokens, 0);
     const int chunk = chunk_len(L, p.splits, p.chunk_fixed);
     const int t0 = split * chunk;
     const int t1 = min(L, t0 + chunk);
@@ -173,6 +174,11 @@ partial_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
                 else static_cast<float*>(p.st.out)[o] = 0.f;
             }
             if (p.st.lse && threadIdx.x < p.G) p.st.lse[b * p.Hq + hq0 + threadIdx.x] = -INFINITY;
+        }
+        if (p.st.mark_empty && threadIdx.x < p.G) {
+            const size_t pi = (size_t)(b * p.Hq + hq0 + threadIdx.x) * p.st.splits + p.st.rec0 + split;
+            p.st.part_ml[2 * pi + 0] = -INFINITY;
+            p.st.part_ml[2 * pi + 1] = 0.f;
         }
         return;
     }
@@ -649,8 +655,12 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream) {
     pp.st.out = a.out;
     pp.st.out_bf16 = a.out_bf16;
     pp.st.lse = a.lse;
-    pp.st.direct = a.splits == 1 ? 1 : 0;
-    pp.st.splits = a.splits;
+    const bool listed = a.list_splits > 0;
+    pp.skip_tokens = a.skip_tokens;
+    pp.st.direct = !listed && a.splits == 1 ? 1 : 0;
+    pp.st.splits = listed ? a.list_splits : a.splits;
+    pp.st.rec0 = a.rec0;
+    pp.st.mark_empty = listed ? 1 : 0;
     const dim3 grid((unsigned)a.splits, (unsigned)a.Hkv, (unsigned)a.B);
     cudaError_t e;
     const bool u = a.unified != 0;
@@ -658,7 +668,7 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream) {
                               : launch_dispatch<128, false>(pp.G, u, tk, tv, pp, grid, stream);
     else e = paged ? launch_dispatch<64, true>(pp.G, u, tk, tv, pp, grid, stream)
                    : launch_dispatch<64, false>(pp.G, u, tk, tv, pp, grid, stream);
-    if (e != cudaSuccess || a.splits == 1) return e;
+    if (e != cudaSuccess || listed || a.splits == 1) return e;
     return launch_merge(a.part_o, a.part_ml, a.seq_lens, a.B, a.Hq, a.L_max, a.D, a.splits, a.chunk_fixed,
                         a.out, a.out_bf16, a.lse, stream);
 }

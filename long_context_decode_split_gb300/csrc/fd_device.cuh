@@ -17,6 +17,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr unsigned kStatusBadPage = 1u;
 constexpr unsigned kStatusTimeout = 2u;
 constexpr unsigned kStatusBadSeqLen = 4u;
+constexpr unsigned kStatusOutOfPages = 8u;
 
 // Sequence length as the kernels use it: seq_lens[b] clamped to [0, L_max]
 // (an out-of-range entry is recorded in `status`).
@@ -495,6 +496,8 @@ struct StoreTarget {
     float* part_ml;  // [rows, splits, 2]: (m_i in log2 units, l_i)
     int direct;
     int splits;
+    int rec0 = 0;        // record of chunk 0
+    int mark_empty = 0;  // empty chunks write m = -inf to their record (all D columns of O unwritten)
 };
 
 // Final step of both combines: red_o/red_m/red_l hold every consumer warp's
@@ -528,7 +531,7 @@ __device__ __forceinline__ void store_combined(unsigned char* smem, int tid, int
             else static_cast<float*>(st.out)[oi] = val;
             if (dim == 0 && st.lse) st.lse[row] = lsum > 0.f ? (M + __log2f(lsum)) * kLn2 : -INFINITY;
         } else {
-            const size_t pi = (size_t)row * st.splits + split;
+            const size_t pi = (size_t)row * st.splits + st.rec0 + split;
             st.part_o[pi * D + dim] = val;
             if (dim == 0) {
                 st.part_ml[2 * pi + 0] = lsum > 0.f ? M : -INFINITY;

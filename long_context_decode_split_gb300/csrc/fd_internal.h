@@ -47,6 +47,12 @@ struct DecodeArgs {
     float* part_ml;           // workspace: [B, Hq, splits, 2]
     int unified;              // bf16 cache only: unified-max variant with fixed max value `phi`
     float phi;                // (natural-log units of the scaled score)
+    // bf16 cache only: chunks written as part of a longer list of partials
+    // (the shared-prefix decode).  list_splits > 0: no merge follows; chunk i
+    // goes to record rec0 + i of list_splits, empty chunks are marked, and the
+    // first skip_tokens tokens of every sequence belong to someone else
+    // (page_table then points at the first own page of row 0).
+    int list_splits, rec0, skip_tokens;
 };
 
 // Workspace bytes for `splits` chunks (0 when splits == 1).
@@ -127,6 +133,74 @@ cudaError_t launch_quantize_fp4(const Fp4QuantArgs& a, cudaStream_t stream);
 int fp4_ctas_per_sm(int D, bool paged);
 cudaError_t launch_decode_fp4(const DecodeArgs& a, cudaStream_t stream);
 cudaError_t fp4_status_read(unsigned* bits, bool clear);
+
+// Attention of packed query rows (fd_rows.cu): prompts, prompt tails, and the
+// shared part of a shared-prefix decode.  Sequence s owns the query tokens
+// cu_q[s] .. cu_q[s + 1] - 1 (cu_q null: one sequence of total_q tokens) and
+// Lk keys; its query i sees keys [0, Lk - Lq + i] (causal) or [0, Lk).
+struct RowsArgs {
+    const void* q;            // [total_q, Hq, D] bf16, tokens q_stride elements apart
+    long long q_stride;
+    const void* k;            // contiguous: token t of head h at t * k_stride + h * k_head_stride;
+    const void* v;            // or pools [num_pages, Hkv, 64, D]
+    long long k_stride, v_stride, k_head_stride, v_head_stride;
+    const int32_t* cu_q;      // [B + 1] or null
+    const int32_t* cu_k;      // contiguous keys: [B + 1] or null (sequence 0 has all total_k)
+    const int32_t* seq_lens;  // pages: [B] keys of each sequence or null (max_pages * 64)
+    const int32_t* row_lens;  // [total_q] or null: a further limit on the keys of a query
+    const int32_t* page_table;// [B, table_stride] when paged, else null
+    int max_pages, num_pages; // entries of a row that may be read; pages in the pool
+    long long table_stride;
+    int B, total_q, total_k, Hq, Hkv, D;
+    int max_k;                // bound on Lk
+    float scale;
+    int causal;
+    int splits, chunk;        // chunks of `chunk` keys (a multiple of 128); splits == 1: all keys
+    void* out;                // splits == 1: [total_q, Hq, D] and lse [total_q, Hq] or null
+    int out_bf16;
+    float* lse;
+    float* part_o;            // else record rec0 + chunk of rec_stride: [total_q, Hq, rec_stride, D]
+    float* part_ml;           // and [total_q, Hq, rec_stride, 2]
+    int rec0, rec_stride;     // (every record of a query row is written, empty ones with m = -inf)
+    int direct;               // write out/lse instead of records
+};
+// CTAs of one chunk and KV head that `total_q` tokens in B sequences take at most.
+long long rows_tiles(int B, int total_q, int G);
+cudaError_t launch_rows(const RowsArgs& a, cudaStream_t stream);
+cudaError_t rows_status_read(unsigned* bits, bool clear);
+
+// Page assignment and cache append (fd_pages.cu).
+struct AssignArgs {
+    const int32_t* cached_lens;
+    const int32_t* new_lens;
+    int B;
+    int32_t* page_table;
+    int max_pages;
+    const int32_t* free_pages;
+    int num_free;
+    const int32_t* free_head;  // [1] or null (0)
+    int total_new;
+    int32_t* seq_lens;
+    int32_t* cu_new;
+    int64_t* slots;
+    int32_t* free_head_out;
+};
+cudaError_t launch_assign(const AssignArgs& a, cudaStream_t stream);
+
+struct AppendArgs {
+    const void* k;            // [T, Hkv, D] bf16, tokens k_stride elements apart
+    const void* v;
+    long long k_stride, v_stride;
+    const int64_t* slots;     // [T]
+    int T, Hkv, D, num_pages;
+    void* k_pages;            // bf16, or e4m3 codes with the row scales below
+    void* v_pages;
+    float* k_scales;
+    float* v_scales;
+};
+cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream);
+cudaError_t launch_append_fp8(const AppendArgs& a, cudaStream_t stream);
+cudaError_t pages_status_read(unsigned* bits, bool clear);
 
 // Launch with programmatic stream serialization: the grid may be scheduled
 // while the previous kernel in the stream is still running, so the kernel
