@@ -13,6 +13,7 @@
 
 #include "fd_device.cuh"
 #include "fd_internal.h"
+#include "fd_tma.h"
 
 namespace fd {
 
@@ -21,10 +22,6 @@ __device__ unsigned int g_status_rows;
 namespace {
 
 struct RowsParams {
-    const uint16_t* q;
-    const uint16_t* k;
-    const uint16_t* v;
-    long long q_stride, k_stride, v_stride, k_head_stride, v_head_stride;
     const int32_t* cu_q;
     const int32_t* cu_k;
     const int32_t* seq_lens;
@@ -43,6 +40,7 @@ struct RowsParams {
     float* part_o;
     float* part_ml;
     int rec0, rec_stride, direct;
+    int zero_row;  // a row past the page pool: a tile copied from there is zeros
 };
 
 // One tile's place: the sequence, its query tokens and its keys.
@@ -108,184 +106,582 @@ __device__ __forceinline__ int visible_keys(const RowsParams& p, const RowsItem&
     return max(n, 0);
 }
 
-// Four warps, 16 rows each; keys in tiles of 64.
-template <int D, bool PAGED>
-__global__ void __launch_bounds__(128) rows_kernel(const RowsParams p) {
-    constexpr int C = D / 8;  // 16-byte chunks of a row
-    __shared__ __align__(1024) unsigned char smem[2 * 64 * D * 2];
-    unsigned char* sk = smem;
-    unsigned char* sv = smem + 64 * D * 2;
-    pdl_wait_primary();
-    pdl_launch_dependents();
+constexpr int kRows = 128;    // rows of a tile: the lanes of an accumulator in tensor memory
+constexpr int kBlock = 128;   // keys per step
+constexpr int kThreads = 384; // two softmax warpgroups, then the copy warp, the MMA warp and two idle ones
+constexpr int kCopyWarp = 8, kMmaWarp = 9;
+// Registers per thread after the split: 168 x 384 at launch = 216 x 256 + 72 x 128.
+constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
+
+// A running maximum is replaced only when a row exceeds it by more than this
+// (log2 units): the weights then stay below 2^8, far inside binary32 and bf16
+// range, and O is rescaled a few times per sequence instead of at every block.
+constexpr float kRescaleAt = 8.f;
+
+template <int D, bool DUAL>
+struct RowsGeo {
+    static constexpr int BOX = 128 * 128;           // 128 rows x 64 bf16 channels
+    static constexpr int BOXES = D / 64;
+    static constexpr int TILE = BOXES * BOX;        // 128 rows of D channels
+    static constexpr int TILES = DUAL ? 2 : 1;      // of query rows
+    static constexpr int STAGES = D == 128 ? (DUAL ? 5 : 6) : 8;
+    static constexpr int SMEM = 1024 + (TILES + STAGES) * TILE + (2 * STAGES + 6) * 8 + 16 + 2 * 128 * 4;
+    static_assert(SMEM <= 232448, "shared memory of a CTA");
+};
+
+// ---- tensor memory and tcgen05 ------------------------------------------------
+
+__device__ __forceinline__ void tmem_alloc(uint32_t* where, uint32_t cols) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(where)), "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+}
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// 32 columns of the warp's 32 lanes (one row per thread); tmem_wait_ld ties the
+// registers to the wait, so nothing reads them before it.
+__device__ __forceinline__ void tmem_ld32(uint32_t (&r)[32], uint32_t addr) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+}
+__device__ __forceinline__ void tie32(uint32_t (&r)[32]) {
+    asm volatile(""
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                   "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                   "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Shared-memory operand descriptor, 128-byte swizzle: address and both byte
+// offsets in units of 16 bytes, descriptor version 1, layout 2.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+    return (uint64_t)((addr & 0x3ffffu) >> 4) | (uint64_t)(lbo >> 4) << 16 | (uint64_t)(sbo >> 4) << 32 |
+           1ull << 46 | 2ull << 61;
+}
+// Channels contiguous (Q and K): 8-row groups 1024 bytes apart.
+__device__ __forceinline__ uint64_t desc_rows(uint32_t addr) { return smem_desc(addr, 16, 1024); }
+// Tokens as the contraction, channels contiguous (V): 64-channel boxes one BOX
+// apart, groups of 8 tokens 1024 bytes apart.
+__device__ __forceinline__ uint64_t desc_cols(uint32_t addr) { return smem_desc(addr, 128 * 128, 1024); }
+
+// Instruction descriptor: bf16 x bf16 -> fp32, M = 128, N columns; bit 16: B
+// with its N index contiguous.
+__host__ __device__ constexpr uint32_t mma_desc(int n, bool b_cols) {
+    return 1u << 4 | 1u << 7 | 1u << 10 | (b_cols ? 1u << 16 : 0u) | (uint32_t)(n / 8) << 17 | 8u << 24;
+}
+// One thread: D[tmem] (+)= A[smem] B[smem]^T, 16 deep.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// The same with A in tensor memory (bf16 pairs, one 32-bit column per pair).
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// `bar` gets one arrival when every MMA this thread issued so far is done.
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+
+__device__ __forceinline__ void tma_load_2d(void* dst, const void* tmap, int x, int y, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+        ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, int x, int y, int z, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// ---- the pass -------------------------------------------------------------------
+//
+// S = Q K^T and O += P V run on tcgen05 with S, P and O in tensor memory.  Two
+// pipelines (i = 0, 1) alternate on the tensor cores: while the softmax
+// warpgroup of one turns its S into P, the MMA warp runs the other's products.
+//   DUAL    the two pipelines hold two tiles of query rows and share every
+//           block of keys and values
+//   single  both hold the same tile and take the even and the odd blocks; their
+//           (m, l, O) are joined at the end
+// A thread of a softmax warpgroup owns one row: 128 scores in registers, no
+// shuffles.  P (bf16) overwrites the first half of S; the products of a
+// pipeline run in the order they are issued, so S of block j + 1 is computed
+// after P of block j was read.  Tensor memory columns: S0 S1 | O0 O1.
+// Keys and values pass through one ring of 128-row tiles (K0 V0 K1 V1 ..).
+template <int D, bool PAGED, bool DUAL>
+__global__ void __launch_bounds__(kThreads, 1)
+rows_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+            const __grid_constant__ CUtensorMap tmv, const RowsParams p) {
+    using Geo = RowsGeo<D, DUAL>;
+    constexpr int TILES = Geo::TILES, STAGES = Geo::STAGES, BOXES = Geo::BOXES, BOX = Geo::BOX, TILE = Geo::TILE;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    unsigned char* sq = smem;
+    unsigned char* ring = smem + TILES * TILE;
+    uint64_t* full = reinterpret_cast<uint64_t*>(ring + STAGES * TILE);
+    uint64_t* empty = full + STAGES;
+    uint64_t* q_full = empty + STAGES;
+    uint64_t* s_full = q_full + 1;  // [2] S of the next block (at the end: O) is complete
+    uint64_t* p_full = s_full + 2;  // [2] P is in place, and O is rescaled
+    uint64_t* drained = p_full + 2;
+    uint32_t* tmem_at = reinterpret_cast<uint32_t*>(drained + 1);
+    float* join = reinterpret_cast<float*>(tmem_at + 4);  // [2][128] m and l of pipeline 1 (single)
+
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int gid = lane >> 2, tig = lane & 3, mi = lane >> 3;
+    pdl_wait_primary();
     const int h = blockIdx.x % p.Hkv, split = blockIdx.y;
-    const RowsItem it = find_item(p, (int)(gridDim.x / p.Hkv - 1 - blockIdx.x / p.Hkv), p.tok);
+    const RowsItem it = find_item(p, (int)(gridDim.x / p.Hkv - 1 - blockIdx.x / p.Hkv), TILES * p.tok);
     if (it.t0 < 0 || it.t0 >= it.Lq) return;
-    const int ntok = min(p.tok, it.Lq - it.t0);
 
-    int lim[2], token[2], head[2];
-    bool live[2];
-    uint32_t qa[D / 16][4];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int r = warp * 16 + gid + 8 * i;
-        token[i] = r / p.G;
-        head[i] = h * p.G + r % p.G;
-        live[i] = r < p.tok * p.G && token[i] < ntok;
-        lim[i] = live[i] ? visible_keys(p, it, it.t0 + token[i]) : 0;
-        token[i] += it.q0 + it.t0;
-        const uint32_t* qr = reinterpret_cast<const uint32_t*>(p.q + (size_t)token[i] * p.q_stride + (size_t)head[i] * D);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-            qa[kk][i] = live[i] ? qr[8 * kk + tig] : 0u;
-            qa[kk][2 + i] = live[i] ? qr[8 * kk + 4 + tig] : 0u;
-        }
-    }
+    // blocks of keys of each pipeline
     const int c0 = split * p.chunk;
-    int most = it.Lk;
-    if (p.causal) most = min(most, it.Lk - it.Lq + it.t0 + ntok);
-    const int c1 = min(most, c0 + p.chunk);
-
-    float o[D / 8][4];
-#pragma unroll
-    for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-
-    for (int t = c0; t < c1; t += 64) {
-        const int rows = min(64, c1 - t);
-        bool ok = true;
-        size_t krow = 0, vrow = 0;
-        long long ks = p.k_stride, vs = p.v_stride;
-        if (PAGED) {
-            const int pg = p.page_table[(size_t)it.seq * p.table_stride + t / kTile];
-            ok = pg >= 0 && pg < p.num_pages;
-            if (!ok && threadIdx.x == 0) atomicOr(&g_status_rows, kStatusBadPage);
-            krow = vrow = ((size_t)pg * p.Hkv + h) * kTile * D;
-            ks = vs = D;
-        } else {
-            krow = (size_t)(it.k0 + t) * p.k_stride + (size_t)h * p.k_head_stride;
-            vrow = (size_t)(it.k0 + t) * p.v_stride + (size_t)h * p.v_head_stride;
-        }
-        if (!ok) continue;
-        __syncthreads();
-        for (int i = threadIdx.x; i < 64 * C; i += 128) {
-            const int r = i / C, c = i % C;
-            uint4 kk = make_uint4(0u, 0u, 0u, 0u), vv = kk;
-            if (r < rows) {
-                kk = *reinterpret_cast<const uint4*>(p.k + krow + (size_t)r * ks + c * 8);
-                vv = *reinterpret_cast<const uint4*>(p.v + vrow + (size_t)r * vs + c * 8);
-            }
-            *reinterpret_cast<uint4*>(sk + swz(r, c)) = kk;
-            *reinterpret_cast<uint4*>(sv + swz(r, c)) = vv;
-        }
-        __syncthreads();
-        float s[8][4];
-#pragma unroll
-        for (int n = 0; n < 8; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-#pragma unroll
-            for (int n = 0; n < 8; n += 2) {
-                uint32_t b0, b1, b2, b3;
-                ldsm_x4(smem_u32(sk) + swz(8 * n + 8 * (mi >> 1) + (lane & 7), 2 * kk + (mi & 1)), b0, b1, b2, b3);
-                mma_bf16(s[n], qa[kk][0], qa[kk][1], qa[kk][2], qa[kk][3], b0, b1);
-                mma_bf16(s[n + 1], qa[kk][0], qa[kk][1], qa[kk][2], qa[kk][3], b2, b3);
-            }
-        float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-        for (int n = 0; n < 8; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int col = t + 8 * n + 2 * tig + (e & 1);
-                s[n][e] = col < min(lim[e >> 1], c1) ? s[n][e] * p.scale_log2 : -INFINITY;
-                mx[e >> 1] = fmaxf(mx[e >> 1], s[n][e]);
-            }
-        float a[2], base[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
-            mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
-            const float mn = fmaxf(m[i], mx[i]);
-            base[i] = mn == -INFINITY ? 0.f : mn;
-            a[i] = exp2_approx(m[i] - base[i]);
-            m[i] = mn;
-            l[i] *= a[i];
-        }
-#pragma unroll
-        for (int n = 0; n < 8; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                s[n][e] = exp2_approx(s[n][e] - base[e >> 1]);
-                l[e >> 1] += s[n][e];
-            }
-#pragma unroll
-        for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[n][e] *= a[e >> 1];
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-            const uint32_t a0 = pack_bf16(s[2 * kk][0], s[2 * kk][1]), a1 = pack_bf16(s[2 * kk][2], s[2 * kk][3]);
-            const uint32_t a2 = pack_bf16(s[2 * kk + 1][0], s[2 * kk + 1][1]);
-            const uint32_t a3 = pack_bf16(s[2 * kk + 1][2], s[2 * kk + 1][3]);
-#pragma unroll
-            for (int n = 0; n < D / 8; n += 2) {
-                uint32_t b0, b1, b2, b3;
-                ldsm_x4_t(smem_u32(sv) + swz(16 * kk + 8 * (mi & 1) + (lane & 7), n + (mi >> 1)), b0, b1, b2, b3);
-                mma_bf16(o[n], a0, a1, a2, a3, b0, b1);
-                mma_bf16(o[n + 1], a0, a1, a2, a3, b2, b3);
-            }
-        }
-    }
+    int nb[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-        if (!live[i]) continue;
-        const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
-        const size_t row = (size_t)token[i] * p.Hq + head[i];
-        const size_t rec = row * p.rec_stride + p.rec0 + split;
-#pragma unroll
-        for (int n = 0; n < D / 8; ++n) {
-            const float x = o[n][2 * i] * inv, y = o[n][2 * i + 1] * inv;
-            const int dim = 8 * n + 2 * tig;
-            if (!p.direct) *reinterpret_cast<float2*>(p.part_o + rec * D + dim) = make_float2(x, y);
-            else if (p.out_bf16)
-                *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + row * D + dim) = pack_bf16(x, y);
-            else *reinterpret_cast<float2*>(static_cast<float*>(p.out) + row * D + dim) = make_float2(x, y);
+        const int first = it.t0 + (DUAL ? i : 0) * p.tok;
+        const int ntok = min(p.tok, it.Lq - first);
+        int most = it.Lk;
+        if (p.causal) most = min(most, it.Lk - it.Lq + first + ntok);
+        most = min(most, c0 + p.chunk) - c0;
+        nb[i] = ntok > 0 && most > 0 ? (most + kBlock - 1) / kBlock : 0;
+    }
+    const int blocks = max(nb[0], nb[1]);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
         }
-        if (tig == 0) {
-            if (!p.direct) {
-                p.part_ml[2 * rec] = l[i] > 0.f ? m[i] : -INFINITY;
-                p.part_ml[2 * rec + 1] = l[i];
-            } else if (p.lse) {
-                p.lse[row] = l[i] > 0.f ? (m[i] + __log2f(l[i])) * kLn2 : -INFINITY;
+        mbar_init(q_full, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 4);
+        }
+        mbar_init(drained, 1);
+        fence_barrier_init();
+    }
+    if (warp == kMmaWarp) tmem_alloc(tmem_at, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_at;
+
+    if (warp >= kCopyWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp == kCopyWarp && lane == 0 && blocks > 0) {
+            // ---------------- copies ----------------
+            const uint32_t qbytes = (uint32_t)(p.tok * p.G * D * 2);
+            const int qtiles = DUAL && nb[1] > 0 ? 2 : 1;
+            mbar_arrive_expect_tx(q_full, qbytes * qtiles);
+            for (int i = 0; i < qtiles; ++i)
+                for (int bx = 0; bx < BOXES; ++bx)
+                    tma_load_3d(sq + i * TILE + bx * BOX, &tmq, 64 * bx, h * p.G, it.q0 + it.t0 + i * p.tok, q_full);
+            int n = 0;  // ring position
+            bool ok = true;
+            // block j of the keys (which = 0) or values (1) into the next stage
+            auto load = [&](int j, int which) {
+                const int s = n % STAGES;
+                ok = ok && mbar_wait(&empty[s], ((uint32_t)(n / STAGES) & 1u) ^ 1u);
+                if (!ok) return;
+                const void* map = which ? static_cast<const void*>(&tmv) : static_cast<const void*>(&tmk);
+                unsigned char* dst = ring + s * TILE;
+                const int at = c0 + j * kBlock;
+                mbar_arrive_expect_tx(&full[s], TILE);
+                if (PAGED) {
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const int pi = at / kTile + half;
+                        int y = p.zero_row;  // past the pool: zeros
+                        if (pi * kTile < it.Lk && pi < p.max_pages) {
+                            const int pg = p.page_table[(size_t)it.seq * p.table_stride + pi];
+                            if (pg >= 0 && pg < p.num_pages) y = (pg * p.Hkv + h) * kTile;
+                            else atomicOr(&g_status_rows, kStatusBadPage);
+                        }
+#pragma unroll
+                        for (int bx = 0; bx < BOXES; ++bx)
+                            tma_load_2d(dst + bx * BOX + half * (BOX / 2), map, 64 * bx, y, &full[s]);
+                    }
+                } else {
+#pragma unroll
+                    for (int bx = 0; bx < BOXES; ++bx)
+                        tma_load_3d(dst + bx * BOX, map, 64 * bx, h, it.k0 + at, &full[s]);
+                }
+                ++n;
+            };
+            constexpr int AHEAD = DUAL ? 1 : 2;  // blocks by which the keys run ahead of the values
+            for (int j = 0; j < AHEAD && j < blocks; ++j) load(j, 0);
+            for (int j = 0; j < blocks; ++j) {
+                load(j, 1);
+                if (j + AHEAD < blocks) load(j + AHEAD, 0);
+            }
+            if (!ok) {
+                // the others stopped early: let the copies in flight land before the CTA ends
+                atomicOr(&g_status_rows, kStatusTimeout);
+                mbar_wait(q_full, 0);
+                for (int u = max(0, n - STAGES); u < n; ++u) mbar_wait(&full[u % STAGES], (uint32_t)(u / STAGES) & 1u);
+            }
+        } else if (warp == kMmaWarp && blocks > 0) {
+            // ---------------- products ----------------
+            constexpr uint32_t IQK = mma_desc(kBlock, false), IPV = mma_desc(D, true);
+            const uint32_t q_at = smem_u32(sq), ring_at = smem_u32(ring);
+            bool ok = warp_wait(q_full, 0);
+            int n = 0;  // ring position
+            auto arrive = [&](int& stage) {  // the next tile of the ring
+                stage = n % STAGES;
+                ok = ok && warp_wait(&full[stage], (uint32_t)(n / STAGES) & 1u);
+                ++n;
+            };
+            auto qk = [&](int i, int stage) {  // S_i = Q_i K^T
+                if (lane == 0) {
+                    const uint32_t qa = q_at + (DUAL ? i : 0) * TILE, ka = ring_at + stage * TILE;
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = (kk / 4) * BOX + (kk % 4) * 32;
+                        mma_ss(tmem + i * 128, desc_rows(qa + off), desc_rows(ka + off), IQK, kk > 0);
+                    }
+                }
+            };
+            auto pv = [&](int i, int stage, bool first) {  // O_i += P_i V
+                if (lane == 0) {
+                    const uint32_t va = ring_at + stage * TILE;
+#pragma unroll
+                    for (int kk = 0; kk < kBlock / 16; ++kk)
+                        mma_ts(tmem + 256 + i * D, tmem + i * 128 + kk * 8, desc_cols(va + kk * 16 * 128), IPV,
+                               !first || kk > 0);
+                }
+            };
+            auto commit = [&](uint64_t* bar) {
+                if (lane == 0) mma_commit(bar);
+            };
+            // Value rows past the sequence may hold anything; their weight is 0, but 0 * NaN is NaN.
+            auto clear_tail = [&](int j, int stage) {
+                const int rows = it.Lk - (c0 + j * kBlock);
+                if (rows >= kBlock) return;
+                unsigned char* v = ring + stage * TILE;
+                for (int i = lane; i < (kBlock - rows) * 8; i += 32)
+#pragma unroll
+                    for (int bx = 0; bx < BOXES; ++bx)
+                        *reinterpret_cast<uint4*>(v + bx * BOX + rows * 128 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+            };
+            auto weights = [&](int i, int round) {
+                ok = ok && warp_wait(&p_full[i], (uint32_t)round & 1u);
+                tc_fence_after();
+            };
+            int sk = 0, sv = 0;
+            if (DUAL) {
+                arrive(sk);
+                if (ok) {
+                    for (int i = 0; i < 2; ++i)
+                        if (nb[i] > 0) {
+                            qk(i, sk);
+                            commit(&s_full[i]);
+                        }
+                    commit(&empty[sk]);
+                }
+                for (int j = 0; ok && j < blocks; ++j) {
+                    arrive(sv);
+                    if (!ok) break;
+                    clear_tail(j, sv);
+                    const bool more = j + 1 < blocks;
+                    if (more) arrive(sk);
+                    if (!ok) break;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        if (j < nb[i]) {
+                            weights(i, j);
+                            if (!ok) break;
+                            pv(i, sv, j == 0);
+                            if (j + 1 < nb[i]) qk(i, sk);
+                            commit(&s_full[i]);
+                        }
+                    }
+                    if (!ok) break;
+                    commit(&empty[sv]);
+                    if (more) commit(&empty[sk]);
+                }
+            } else {
+                for (int j = 0; ok && j < 2 && j < blocks; ++j) {
+                    arrive(sk);
+                    if (!ok) break;
+                    qk(j, sk);
+                    commit(&s_full[j]);
+                    commit(&empty[sk]);
+                }
+                for (int j = 0; ok && j < blocks; ++j) {
+                    const int i = j & 1;
+                    arrive(sv);
+                    if (!ok) break;
+                    clear_tail(j, sv);
+                    if (j + 2 < blocks) arrive(sk);
+                    weights(i, j >> 1);
+                    if (!ok) break;
+                    pv(i, sv, j < 2);
+                    if (j + 2 < blocks) qk(i, sk);
+                    commit(&s_full[i]);
+                    commit(&empty[sv]);
+                    if (j + 2 < blocks) commit(&empty[sk]);
+                }
+            }
+            if (!ok) {
+                if (lane == 0) atomicOr(&g_status_rows, kStatusTimeout);
+                commit(drained);
+                warp_wait(drained, 0);
             }
         }
+    } else {
+        // ---------------- softmax, one row per thread ----------------
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        const int i = warp >> 2;  // pipeline
+        const int r = threadIdx.x & 127;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // 32 lanes per warp, lane in the upper half
+        const uint32_t s_at = tmem + lanes + i * 128, o_at = tmem + lanes + 256 + i * D;
+        const int first = it.t0 + (DUAL ? i : 0) * p.tok;
+        const int tk = r / p.G;
+        const bool live = tk < p.tok && first + tk < it.Lq;
+        const int lim = live ? min(visible_keys(p, it, first + tk), c0 + p.chunk) - c0 : 0;
+        const int rounds = DUAL ? nb[i] : (nb[0] + 1 - i) / 2;
+        float m = -INFINITY;
+        float2 l2 = make_float2(0.f, 0.f);
+        bool ok = true;
+        for (int round = 0; round < rounds; ++round) {
+            const int j = DUAL ? round : 2 * round + i;
+            const int left = lim - j * kBlock;  // visible keys from this block on
+            bool bad[2] = {false, false};
+            if (PAGED) {
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int pi = (c0 + j * kBlock) / kTile + half;
+                    if (pi * kTile < it.Lk && pi < p.max_pages) {
+                        const int pg = p.page_table[(size_t)it.seq * p.table_stride + pi];
+                        bad[half] = pg < 0 || pg >= p.num_pages;
+                    }
+                }
+            }
+            if (!warp_wait(&s_full[i], (uint32_t)round & 1u)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            uint32_t s[4][32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32(s[c], s_at + 32 * c);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tie32(s[c]);
+            if (__any_sync(0xffffffffu, left < kBlock || bad[0] || bad[1])) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (32 * c + e >= left || bad[c >> 1]) s[c][e] = 0xff800000u;  // -inf
+            }
+            float mx[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                mx[c] = __uint_as_float(s[c][0]);
+#pragma unroll
+                for (int e = 1; e < 32; ++e) mx[c] = fmaxf(mx[c], __uint_as_float(s[c][e]));
+            }
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+            if (__any_sync(0xffffffffu, top > m + kRescaleAt)) {
+                const float mn = fmaxf(m, top);
+                const float a = mn == -INFINITY ? 1.f : exp2_approx(m - mn);
+                m = mn;
+                l2 = f2mul(l2, make_float2(a, a));
+                if (round > 0) {
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t o[32];
+                        tmem_ld32(o, o_at + 32 * c);
+                        tmem_wait_ld();
+                        tie32(o);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+                        tmem_st32(o_at + 32 * c, o);
+                    }
+                }
+            }
+            const float base = m == -INFINITY ? 0.f : m;
+            const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nb2 = make_float2(-base, -base);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                uint32_t w[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    const int c = 2 * half + e / 16, x = 2 * (e % 16);
+                    float2 f = f2fma(make_float2(__uint_as_float(s[c][x]), __uint_as_float(s[c][x + 1])), sc2, nb2);
+                    f = make_float2(exp2_approx(f.x), exp2_approx(f.y));
+                    l2 = __fadd2_rn(l2, f);
+                    w[e] = pack_bf16(f.x, f.y);
+                }
+                tmem_st32(s_at + 32 * half, w);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_full[i]);
+        }
+        if (ok && rounds > 0) ok = warp_wait(&s_full[i], (uint32_t)rounds & 1u);
+        if (!ok && lane == 0) atomicOr(&g_status_rows, kStatusTimeout);
+        tc_fence_after();
+        pdl_launch_dependents();
+        float l = ok ? l2.x + l2.y : 0.f;
+        if (!ok) m = -INFINITY;
+        float own = 1.f, other = 0.f;  // factors of this pipeline's and the other's O
+        float* o1 = reinterpret_cast<float*>(ring);  // [D][128]: O of pipeline 1
+        if (!DUAL) {
+            named_barrier(1, 256);  // both pipelines are done with the ring
+            if (i == 1) {
+                join[r] = m;
+                join[128 + r] = l;
+                if (rounds > 0) {
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t o[32];
+                        tmem_ld32(o, o_at + 32 * c);
+                        tmem_wait_ld();
+                        tie32(o);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o1[(32 * c + e) * 128 + r] = __uint_as_float(o[e]);
+                    }
+                }
+            }
+            named_barrier(1, 256);
+            if (i == 0) {
+                const float m1 = join[r], l1 = join[128 + r];
+                const float M = fmaxf(m, m1);
+                own = m == -INFINITY ? 0.f : exp2_approx(m - M);
+                other = m1 == -INFINITY ? 0.f : exp2_approx(m1 - M);
+                l = own * l + other * l1;
+                m = M;
+            }
+        }
+        const int head = h * p.G + r - tk * p.G;
+        const size_t row = (size_t)(it.q0 + first + tk) * p.Hq + head;
+        const size_t rec = row * p.rec_stride + p.rec0 + split;
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        own *= inv;
+        other *= inv;
+        if (DUAL || i == 0) {
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                if (rounds > 0) {
+                    tmem_ld32(o, o_at + 32 * c);
+                    tmem_wait_ld();
+                    tie32(o);
+                }
+                float f[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    f[e] = own != 0.f ? __uint_as_float(o[e]) * own : 0.f;
+                    if (!DUAL && other != 0.f) f[e] += o1[(32 * c + e) * 128 + r] * other;
+                }
+                if (!live) continue;
+                if (!p.direct || !p.out_bf16) {
+                    float4* dst = reinterpret_cast<float4*>(
+                        (p.direct ? static_cast<float*>(p.out) + row * D : p.part_o + rec * D) + 32 * c);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) dst[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+                } else {
+                    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * D + 32 * c);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        dst[e] = make_uint4(pack_bf16(f[8 * e], f[8 * e + 1]), pack_bf16(f[8 * e + 2], f[8 * e + 3]),
+                                            pack_bf16(f[8 * e + 4], f[8 * e + 5]), pack_bf16(f[8 * e + 6], f[8 * e + 7]));
+                }
+            }
+            if (live) {
+                if (!p.direct) {
+                    p.part_ml[2 * rec] = l > 0.f ? m : -INFINITY;
+                    p.part_ml[2 * rec + 1] = l;
+                } else if (p.lse) {
+                    p.lse[row] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
+                }
+            }
+        }
+        tc_fence_before();
+    }
+    __syncwarp();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_free(tmem, 512);
     }
 }
 
-int rows_tok(int G) { return 64 / G; }
+int rows_tok(int G) { return kRows / G; }
+
+// Two tiles per CTA when the sequences fill more than one on average.
+bool rows_dual(int B, int total_q, int G) { return B > 0 && total_q / B > rows_tok(G); }
+
+template <int D, bool PAGED, bool DUAL>
+cudaError_t launch_kernel(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const RowsParams& p,
+                          dim3 grid, cudaStream_t stream) {
+    constexpr auto kernel = rows_kernel<D, PAGED, DUAL>;
+    constexpr int SMEM = RowsGeo<D, DUAL>::SMEM;
+    static bool done[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || !done[dev]) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+        if (e != cudaSuccess) return e;
+        // the warpgroups' register shares are cut from what the block is launched with
+        cudaFuncAttributes attr;
+        e = cudaFuncGetAttributes(&attr, kernel);
+        if (e != cudaSuccess) return e;
+        if (attr.numRegs * kThreads < 256 * kSoftmaxRegs + 128 * kOtherRegs) return cudaErrorInvalidConfiguration;
+        if (dev < 64) done[dev] = true;
+    }
+    return launch_pdl(kernel, grid, dim3(kThreads), SMEM, stream, q, k, v, p);
+}
 
 }  // namespace
 
-long long rows_tiles(int B, int total_q, int G) { return (long long)total_q / rows_tok(G) + B; }
+long long rows_tiles(int B, int total_q, int G) {
+    return (long long)total_q / (rows_tok(G) * (rows_dual(B, total_q, G) ? 2 : 1)) + B;
+}
 
 cudaError_t launch_rows(const RowsArgs& a, cudaStream_t stream) {
     if (a.total_q == 0 || a.B == 0) return cudaSuccess;
     RowsParams p;
-    p.q = static_cast<const uint16_t*>(a.q);
-    p.k = static_cast<const uint16_t*>(a.k);
-    p.v = static_cast<const uint16_t*>(a.v);
-    p.q_stride = a.q_stride;
-    p.k_stride = a.k_stride;
-    p.v_stride = a.v_stride;
-    p.k_head_stride = a.k_head_stride;
-    p.v_head_stride = a.v_head_stride;
     p.cu_q = a.cu_q;
     p.cu_k = a.cu_k;
     p.seq_lens = a.seq_lens;
@@ -313,14 +709,37 @@ cudaError_t launch_rows(const RowsArgs& a, cudaStream_t stream) {
     p.rec0 = a.rec0;
     p.rec_stride = a.rec_stride;
     p.direct = a.direct;
+    const bool paged = a.page_table != nullptr;
+    const uint64_t pool_rows = paged ? (uint64_t)a.num_pages * a.Hkv * kTile : 0;
+    p.zero_row = (int)(pool_rows > 0 ? pool_rows : 1);
+    CUtensorMap tq, tk, tv;
+    if (!make_token_map(&tq, a.q, a.D, a.Hq, a.total_q, a.D, a.q_stride, p.G, p.tok)) return cudaErrorInvalidValue;
+    bool ok;
+    if (paged && pool_rows > 0) {
+        ok = make_row_map(&tk, a.k, pool_rows, (uint32_t)a.D * 2) && make_row_map(&tv, a.v, pool_rows, (uint32_t)a.D * 2);
+    } else if (paged) {  // an empty pool: nothing is read, any well-formed map will do
+        ok = make_row_map(&tk, a.q, 1, (uint32_t)a.D * 2) && make_row_map(&tv, a.q, 1, (uint32_t)a.D * 2);
+    } else if (a.total_k > 0) {
+        ok = make_token_map(&tk, a.k, a.D, a.Hkv, a.total_k, a.k_head_stride, a.k_stride, 1, kBlock) &&
+             make_token_map(&tv, a.v, a.D, a.Hkv, a.total_k, a.v_head_stride, a.v_stride, 1, kBlock);
+    } else {
+        tk = tv = tq;
+        ok = true;
+    }
+    if (!ok) return cudaErrorInvalidValue;
     const long long tiles = rows_tiles(a.B, a.total_q, p.G);
     const dim3 grid((unsigned)(tiles * a.Hkv), (unsigned)a.splits);
-    const bool paged = a.page_table != nullptr;
-    if (a.D == 128)
-        return paged ? launch_pdl(rows_kernel<128, true>, grid, dim3(128), 0, stream, p)
-                     : launch_pdl(rows_kernel<128, false>, grid, dim3(128), 0, stream, p);
-    return paged ? launch_pdl(rows_kernel<64, true>, grid, dim3(128), 0, stream, p)
-                 : launch_pdl(rows_kernel<64, false>, grid, dim3(128), 0, stream, p);
+    const bool dual = rows_dual(a.B, a.total_q, p.G);
+    if (a.D == 128) {
+        if (paged) return dual ? launch_kernel<128, true, true>(tq, tk, tv, p, grid, stream)
+                               : launch_kernel<128, true, false>(tq, tk, tv, p, grid, stream);
+        return dual ? launch_kernel<128, false, true>(tq, tk, tv, p, grid, stream)
+                    : launch_kernel<128, false, false>(tq, tk, tv, p, grid, stream);
+    }
+    if (paged) return dual ? launch_kernel<64, true, true>(tq, tk, tv, p, grid, stream)
+                           : launch_kernel<64, true, false>(tq, tk, tv, p, grid, stream);
+    return dual ? launch_kernel<64, false, true>(tq, tk, tv, p, grid, stream)
+                : launch_kernel<64, false, false>(tq, tk, tv, p, grid, stream);
 }
 
 cudaError_t rows_status_read(unsigned* bits, bool clear) {

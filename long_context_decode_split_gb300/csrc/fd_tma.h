@@ -57,6 +57,24 @@ inline bool make_row_map(CUtensorMap* map, const void* base, uint64_t rows, uint
     return r == CUDA_SUCCESS;
 }
 
+// Tensor map over packed tokens [tokens, heads, channels] bf16 with the given
+// strides (elements, multiples of 8), read as boxes of 64 channels x box_heads
+// x box_tokens rows of 128 bytes (128-byte swizzle, the head index running
+// faster); tokens past the end read as zero.
+inline bool make_token_map(CUtensorMap* map, const void* base, int channels, int heads, int tokens,
+                           long long head_stride, long long token_stride, int box_heads, int box_tokens) {
+    EncodeTiledFn enc = tensor_map_encoder();
+    if (!enc || tokens <= 0) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)channels, (cuuint64_t)heads, (cuuint64_t)tokens};
+    const cuuint64_t strides[2] = {(cuuint64_t)head_stride * 2, (cuuint64_t)token_stride * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_tokens};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 // Tensor map over a plain vector of `n` elements of `elem_bytes` (4 or 2)
 // bytes, read as boxes of `box` elements (box * elem_bytes a multiple of 16,
 // box <= 256) without swizzle.  A copy must start at an index whose byte
