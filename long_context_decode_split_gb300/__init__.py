@@ -131,12 +131,16 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
+def _nbytes(t):
+    return 0 if t is None else t.numel() * t.element_size()
+
+
 def _stream(stream):
     """The stream handle for a call on the current device: `stream`, which must
     belong to that device, or the device's current torch stream."""
+    dev = torch._C._cuda_getDevice()
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
-    dev = torch.cuda.current_device()
+        return torch._C._cuda_getCurrentRawStream(dev)
     if stream.device.index != dev:
         raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{dev}")
     return stream.cuda_stream
@@ -150,7 +154,7 @@ def _on_device_of_first_tensor(fn):
     def wrapper(t, *args, **kwargs):
         if not (isinstance(t, torch.Tensor) and t.is_cuda):
             raise ValueError(f"{fn.__name__}: the first argument must be a CUDA tensor")
-        if t.device.index == torch.cuda.current_device():
+        if t.get_device() == torch._C._cuda_getDevice():
             return fn(t, *args, **kwargs)
         with torch.cuda.device(t.device):
             return fn(t, *args, **kwargs)
@@ -166,14 +170,14 @@ def _check_cuda(t, name, dtype=None, shape=None):
     # messages are built only on failure: this runs several times per call
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    dev = torch.cuda.current_device()
-    if t.device.index != dev:
+    dev = torch._C._cuda_getDevice()
+    if t.get_device() != dev:
         raise ValueError(f"{name} is on {t.device}, expected cuda:{dev} (the first tensor's device)")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
@@ -208,15 +212,18 @@ def fd_num_splits(B, Hq, Hkv, L_max, d, num_splits=0, ragged=False) -> int:
 _WS_SIZES = {}
 
 
-def fd_decode_workspace_size(B, Hq, Hkv, L_max, d, num_splits=0, ragged=False) -> int:
+def _remembered_size(name, *args):
     # the plan depends on the shape and the current device only: remembered per both
-    key = (torch.cuda.current_device() if torch.cuda.is_available() else -1, B, Hq, Hkv, L_max, d, num_splits,
-           bool(ragged))
+    key = (name, torch.cuda.current_device() if torch.cuda.is_available() else -1, *args)
     n = _WS_SIZES.get(key)
     if n is None:
-        n = int(load().fd_decode_workspace_size(B, Hq, Hkv, L_max, d, num_splits, int(bool(ragged))))
+        n = int(getattr(load(), name)(*args))
         _WS_SIZES[key] = n
     return n
+
+
+def fd_decode_workspace_size(B, Hq, Hkv, L_max, d, num_splits=0, ragged=False) -> int:
+    return _remembered_size("fd_decode_workspace_size", B, Hq, Hkv, L_max, d, num_splits, int(bool(ragged)))
 
 
 def fd_topdelta_workspace_size(B, Hq, Hkv, L_max, d, num_splits=0) -> int:
@@ -396,7 +403,7 @@ def fd_decode_topdelta(q, codes, mn_scale, res, res_scale, v, seq_lens=None, sca
     st = getattr(lib, name)(_p(q), _p(codes), _p(mn_scale), _p(res), _p(res_scale), _p(v), _p(seq_lens),
                             B, Hq, Hkv, L_max, d, scale, delta, int(n_sink), int(window), int(num_splits),
                             _p(out), code, _p(lse), _p(sel_mask), _p(sel_count), _p(ws),
-                            0 if ws is None else ws.numel() * ws.element_size(), _stream(stream))
+                            _nbytes(ws), _stream(stream))
     _raise(st, name)
     return out, lse, sel_mask, sel_count
 
@@ -502,7 +509,7 @@ def _decode_dense_q(kind, q, k_codes, k_scales, v_codes, v_scales, seq_lens, sca
     ws = _workspace(need, q.device, workspace)
     st = getattr(lib, name)(_p(q), _p(k_codes), _p(k_scales), _p(v_codes), _p(v_scales), _p(seq_lens),
                             B, Hq, Hkv, L_max, d, scale, int(num_splits), _p(out), code, _p(lse), _p(ws),
-                            0 if ws is None else ws.numel() * ws.element_size(), _stream(stream))
+                            _nbytes(ws), _stream(stream))
     _raise(st, name)
     return out, lse
 
@@ -532,7 +539,7 @@ def _decode_paged_q(kind, q, k_pages, k_page_scales, v_pages, v_page_scales, pag
     st = getattr(lib, name)(_p(q), _p(k_pages), _p(k_page_scales), _p(v_pages), _p(v_page_scales),
                             _p(page_table), max_pages, int(num_pages), _p(seq_lens), page_size, B, Hq, Hkv,
                             d, scale, int(num_splits), _p(out), code, _p(lse), _p(ws),
-                            0 if ws is None else ws.numel() * ws.element_size(), _stream(stream))
+                            _nbytes(ws), _stream(stream))
     _raise(st, name)
     return out, lse
 
@@ -621,8 +628,8 @@ def _check_tokens(t, name, H=None, d=None):
     slice of a fused projection); returns the token stride in elements."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    dev = torch.cuda.current_device()
-    if t.device.index != dev:
+    dev = torch._C._cuda_getDevice()
+    if t.get_device() != dev:
         raise ValueError(f"{name} is on {t.device}, expected cuda:{dev} (the first tensor's device)")
     if t.dtype != torch.bfloat16:
         raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
@@ -631,6 +638,8 @@ def _check_tokens(t, name, H=None, d=None):
                          f"got {tuple(t.shape)}")
     T, H, d = t.shape
     row = H * d
+    if t.is_contiguous():
+        return row
     if t.numel() and ((d > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != d)):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
     stride = t.stride(0) if T > 1 else row
@@ -652,7 +661,9 @@ def fd_prefill_num_splits(B, total_q, Hq, Hkv, max_k, d, num_splits=0) -> int:
 
 
 def fd_prefill_workspace_size(B, total_q, Hq, Hkv, max_k, d, num_splits=0) -> int:
-    return int(load().fd_prefill_workspace_size(B, total_q, Hq, Hkv, max_k, d, num_splits))
+    if len(_WS_SIZES) > 4096:  # prompt batches differ at every call
+        _WS_SIZES.clear()
+    return _remembered_size("fd_prefill_workspace_size", B, total_q, Hq, Hkv, max_k, d, num_splits)
 
 
 @_on_device_of_first_tensor
@@ -679,7 +690,7 @@ def fd_prefill_packed(q, k, v, cu_seqlens_q, cu_seqlens_k=None, scale=None, caus
     ws = _workspace(fd_prefill_workspace_size(B, Tq, Hq, Hkv, Tk, d, num_splits), q.device, workspace)
     st = lib.fd_prefill_packed(_p(q), _p(k), _p(v), qs, ks, vs, _p(cu_seqlens_q), _p(cu_seqlens_k), B, Tq, Tk, Hq, Hkv,
                                d, scale, int(bool(causal)), int(num_splits), _p(out), code, _p(lse), _p(ws),
-                               0 if ws is None else ws.numel() * ws.element_size(), _stream(stream))
+                               _nbytes(ws), _stream(stream))
     _raise(st, "fd_prefill_packed")
     return out, lse
 
@@ -716,13 +727,13 @@ def fd_prefill_paged(q, k_pages, v_pages, page_table, num_pages, cu_seqlens_q, s
     st = lib.fd_prefill_paged(_p(q), _p(k_pages), _p(v_pages), qs, _p(page_table), max_pages, int(num_pages),
                               _p(cu_seqlens_q), _p(seq_lens), page_size, B, Tq, Hq, Hkv, d, scale, int(bool(causal)),
                               int(num_splits), _p(out), code, _p(lse), _p(ws),
-                              0 if ws is None else ws.numel() * ws.element_size(), _stream(stream))
+                              _nbytes(ws), _stream(stream))
     _raise(st, "fd_prefill_paged")
     return out, lse
 
 
 def fd_shared_prefix_workspace_size(B, Hq, Hkv, prefix_len, L_own, d, num_splits=0) -> int:
-    return int(load().fd_shared_prefix_workspace_size(B, Hq, Hkv, prefix_len, L_own, d, num_splits))
+    return _remembered_size("fd_shared_prefix_workspace_size", B, Hq, Hkv, prefix_len, L_own, d, num_splits)
 
 
 @_on_device_of_first_tensor
@@ -753,7 +764,7 @@ def fd_decode_paged_shared_prefix(q, k_pages, v_pages, prefix_table, page_table,
     st = lib.fd_decode_paged_shared_prefix(_p(q), _p(k_pages), _p(v_pages), _p(prefix_table), n, _p(page_table),
                                            max_pages, int(num_pages), _p(seq_lens), page_size, B, Hq, Hkv, d, scale,
                                            int(num_splits), _p(out), code, _p(lse), _p(ws),
-                                           0 if ws is None else ws.numel() * ws.element_size(), _stream(stream))
+                                           _nbytes(ws), _stream(stream))
     _raise(st, "fd_decode_paged_shared_prefix")
     return out, lse
 
@@ -784,7 +795,7 @@ def fd_decode_dense_shared_prefix(q, k_prefix, v_prefix, k, v, seq_lens=None, sc
     ws = _workspace(fd_shared_prefix_workspace_size(B, Hq, Hkv, P, L_max, d, num_splits), q.device, workspace)
     st = lib.fd_decode_dense_shared_prefix(_p(q), _p(k_prefix), _p(v_prefix), P, _p(k), _p(v), _p(seq_lens), B, Hq, Hkv,
                                            L_max, d, scale, int(num_splits), _p(out), code, _p(lse), _p(ws),
-                                           0 if ws is None else ws.numel() * ws.element_size(), _stream(stream))
+                                           _nbytes(ws), _stream(stream))
     _raise(st, "fd_decode_dense_shared_prefix")
     return out, lse
 

@@ -666,6 +666,10 @@ int fd_assign_pages(const int32_t* cached_lens, const int32_t* new_lens, int B, 
         !aligned4(free_head) || !aligned4(seq_lens) || !aligned4(cu_seqlens) || !aligned16(slots) ||
         !aligned4(free_head_out))
         return FD_ERR_INVALID_ARG;
+    // the new lengths may replace the old ones, but not shifted against them
+    const uintptr_t in = reinterpret_cast<uintptr_t>(cached_lens), to = reinterpret_cast<uintptr_t>(seq_lens);
+    const uintptr_t bytes = (uintptr_t)B * sizeof(int32_t);
+    if (in != to && in < to + bytes && to < in + bytes) return FD_ERR_INVALID_ARG;
     fd::AssignArgs a = {cached_lens, new_lens, B, page_table, max_pages, free_pages, num_free, free_head, total_new,
                         seq_lens, cu_seqlens, slots, free_head_out};
     return to_status(fd::launch_assign(a, static_cast<cudaStream_t>(stream)));
@@ -678,6 +682,7 @@ namespace {
 int append_entry(fd::AppendArgs& a, int page_size, bool fp8, void* stream) {
     if (page_size != kTile) return page_size > 0 ? FD_ERR_UNSUPPORTED : FD_ERR_INVALID_ARG;
     if (a.T < 0 || a.num_pages < 0) return FD_ERR_INVALID_ARG;
+    if (a.Hkv > 0 && (long long)a.T * a.Hkv > 0x7fffffffLL) return FD_ERR_UNSUPPORTED;
     const int st = check_shape(0, a.Hkv, a.Hkv, 0, a.D);
     if (st != FD_OK) return st;
     if (!stride_ok(a.k_stride, a.Hkv, a.D) || !stride_ok(a.v_stride, a.Hkv, a.D)) return FD_ERR_INVALID_ARG;

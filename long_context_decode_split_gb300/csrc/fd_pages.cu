@@ -69,97 +69,191 @@ struct AssignParams {
     int32_t* cu_new;
     int64_t* slots;
     int32_t* free_head_out;
+    int slots_here;  // assign_kernel writes the slots too
+    int lens_here;   // and seq_lens
 };
 
-// One block: sequences in groups of 1024, one per thread, with running sums of
-// their new tokens and pages.  Inputs of a group are in registers before its
-// outputs are written, so outputs may be the inputs' own buffers.
+// What a sequence brings: lengths that the table cannot hold are cut, and
+// reported; the tokens cut off keep their place among the slots.
+struct Lengths {
+    int cached, fresh, end;
+    bool bad;
+};
+__device__ __forceinline__ Lengths lengths_of(const AssignParams& p, int b) {
+    const long long cap = (long long)p.max_pages * kTile;
+    const int cached = p.cached_lens[b], fresh = p.new_lens[b];
+    Lengths l;
+    l.bad = cached < 0 || cached > cap || fresh < 0 || fresh > cap - cached;
+    l.cached = (int)min(max((long long)cached, 0LL), cap);
+    l.fresh = max(fresh, 0);
+    l.end = l.cached + (int)min((long long)l.fresh, cap - l.cached);
+    return l;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
+// One cluster; sequences in groups of 1024, one per thread, with running sums
+// of their new tokens and pages.  Every CTA of the cluster computes the same
+// sums; the table entries (and slots) of a group are shared out among them, CTA
+// 0 writes the rest.  All CTAs have read a group's inputs before its lengths
+// are written (and the head of the free list before anything is), so outputs
+// may be the inputs' own buffers.
 __global__ void __launch_bounds__(kAssignThreads) assign_kernel(const AssignParams p) {
     __shared__ long long red[64];
     __shared__ int cu_s[kAssignThreads + 1];
     __shared__ int cached_s[kAssignThreads];
     __shared__ int end_s[kAssignThreads];
-    __shared__ long long base_s[kAssignThreads];
+    __shared__ long long first_s[kAssignThreads];  // pages taken by the group's sequences before this one
     pdl_wait_primary();
     pdl_launch_dependents();
     const int tid = threadIdx.x;
+    const int part = blockIdx.x, parts = gridDim.x;
     long long head = p.free_head ? p.free_head[0] : 0;
     bool bad = false, out_of_pages = false;
     if (head < 0) {
         head = 0;
         bad = true;
     }
-    const long long cap = (long long)p.max_pages * kTile;
     long long tokens = 0, pages = 0;  // before this group
     for (int b0 = 0; b0 < p.B; b0 += kAssignThreads) {
-        const int b = b0 + tid;
-        int cached = 0, fresh = 0, end = 0;
-        if (b < p.B) {
-            cached = p.cached_lens[b];
-            fresh = p.new_lens[b];
-            // a length that the table cannot hold is cut, and reported; the
-            // tokens cut off keep their place among the slots
-            if (cached < 0 || cached > cap || fresh < 0 || fresh > cap - cached) bad = true;
-            cached = (int)min(max((long long)cached, 0LL), cap);
-            fresh = max(fresh, 0);
-            end = cached + (int)min((long long)fresh, cap - cached);
-        }
-        const int before = pages_of(cached), need = pages_of(end) - before;
-        long long tok = fresh, pg = need, ttok, tpg;
+        const int b = b0 + tid, n = min(p.B - b0, kAssignThreads);
+        Lengths l = {0, 0, 0, false};
+        if (tid < n) l = lengths_of(p, b);
+        bad |= l.bad;
+        long long tok = l.fresh, pg = pages_of(l.end) - pages_of(l.cached), ttok, tpg;
         block_scan2(tok, pg, ttok, tpg, red);
-        tok += tokens;
-        pg += pages;
-        cu_s[tid] = (int)min(tok, (long long)p.total_new);
-        cached_s[tid] = cached;
-        end_s[tid] = end;
-        base_s[tid] = pg;
-        if (tid == 0) cu_s[min(p.B - b0, kAssignThreads)] = (int)min(tokens + ttok, (long long)p.total_new);
-        if (b < p.B) {
+        cu_s[tid] = (int)min(tokens + tok, (long long)p.total_new);
+        cached_s[tid] = l.cached;
+        end_s[tid] = l.end;
+        first_s[tid] = pg;
+        if (tid == 0) cu_s[n] = (int)min(tokens + ttok, (long long)p.total_new);
+        if (parts > 1) cluster_sync();
+        else __syncthreads();
+        if (part == 0 && tid < n) {
             p.cu_new[b] = cu_s[tid];
-            p.seq_lens[b] = end;
-            for (int i = 0; i < need; ++i) {
-                const long long at = head + pg + i;
-                if (at >= p.num_free) out_of_pages = true;
-                p.page_table[(size_t)b * p.max_pages + before + i] = at < p.num_free ? p.free_pages[at] : -1;
-            }
+            if (p.lens_here) p.seq_lens[b] = l.end;
         }
-        __syncthreads();
-        const int n = min(p.B - b0, kAssignThreads);
-        const int t0 = cu_s[0], t1 = cu_s[n];
-        for (int t = t0 + tid; t < t1; t += kAssignThreads) {
-            int lo = 0, hi = n;  // the last sequence with cu <= t
+        // the group's new pages, one per thread
+        const long long base = head + pages;
+        for (long long i = (long long)part * kAssignThreads + tid; i < tpg; i += (long long)parts * kAssignThreads) {
+            if (base + i >= p.num_free) out_of_pages = true;
+            int lo = 0, hi = n;  // the last sequence with first <= i
             while (hi - lo > 1) {
                 const int mid = (lo + hi) / 2;
-                if (cu_s[mid] <= t) lo = mid;
+                if (first_s[mid] <= i) lo = mid;
                 else hi = mid;
             }
-            const int c = cached_s[lo];
-            const long long pos = (long long)c + t - cu_s[lo];
-            const int j = (int)(pos / kTile), first = pages_of(c);
-            int page;
-            if (pos >= end_s[lo]) {
-                page = -1;
-            } else if (j < first) {
-                page = p.page_table[(size_t)(b0 + lo) * p.max_pages + j];
-            } else {
-                const long long at = head + base_s[lo] + j - first;
-                page = at < p.num_free ? p.free_pages[at] : -1;
+            p.page_table[(size_t)(b0 + lo) * p.max_pages + pages_of(cached_s[lo]) + (int)(i - first_s[lo])] =
+                base + i < p.num_free ? p.free_pages[base + i] : -1;
+        }
+        if (p.slots_here) {
+            const int t1 = cu_s[n];
+            for (int t = cu_s[0] + part * kAssignThreads + tid; t < t1; t += parts * kAssignThreads) {
+                int lo = 0, hi = n;  // the last sequence with cu <= t
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) / 2;
+                    if (cu_s[mid] <= t) lo = mid;
+                    else hi = mid;
+                }
+                const int c = cached_s[lo];
+                const long long pos = (long long)c + t - cu_s[lo];
+                const int j = (int)(pos / kTile), old = pages_of(c);
+                int page = -1;
+                if (pos < end_s[lo]) {
+                    const long long at = base + first_s[lo] + j - old;
+                    if (j < old) page = p.page_table[(size_t)(b0 + lo) * p.max_pages + j];
+                    else if (at < p.num_free) page = p.free_pages[at];
+                }
+                p.slots[t] = page < 0 ? -1 : (int64_t)page * kTile + (int)(pos % kTile);
             }
-            p.slots[t] = page < 0 ? -1 : (int64_t)page * kTile + (int)(pos % kTile);
         }
         tokens += ttok;
         pages += tpg;
         __syncthreads();
     }
     if (tokens > p.total_new) bad = true;
-    for (long long t = tokens + tid; t < p.total_new; t += kAssignThreads) p.slots[t] = -1;
-    __syncthreads();  // free_head is read (B = 0 passes no barrier above)
-    if (tid == 0) {
+    if (p.slots_here)
+        for (long long t = tokens + part * kAssignThreads + tid; t < p.total_new; t += parts * kAssignThreads)
+            p.slots[t] = -1;
+    if (parts > 1) cluster_sync();  // free_head is read (B = 0 passes no barrier above)
+    else __syncthreads();
+    if (part == 0 && tid == 0) {
         p.cu_new[p.B] = (int)min(tokens, (long long)p.total_new);
         p.free_head_out[0] = (int)min(head + pages, (long long)p.num_free);
     }
     if (bad) atomicOr(&g_status_pages, kStatusBadSeqLen);
     if (out_of_pages) atomicOr(&g_status_pages, kStatusOutOfPages);
+}
+
+// Slots of many tokens from the finished table: a warp takes kSlotRun tokens in
+// a row and finds the sequences of the first and the last by probing 32 places
+// of the offsets at a time; a lane searches between them, two tokens at a time
+// (one 16-byte store).
+constexpr int kSlotRun = 256;
+
+__global__ void __launch_bounds__(256) slots_kernel(const AssignParams p) {
+    pdl_wait_primary();
+    pdl_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const long long run = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * kSlotRun;
+    if (run >= p.total_new) return;
+    // the last sequence in [s, s + n) whose offset is <= t, by the whole warp
+    auto search = [&](int s, int n, long long t) {
+        while (n > 1) {
+            const int step = (n + 31) / 32;
+            const bool below = lane * step < n && p.cu_new[s + lane * step] <= t;
+            const unsigned votes = __ballot_sync(0xffffffffu, below);
+            const int hit = votes ? 31 - __clz(votes) : 0;
+            s += hit * step;
+            n = min(step, n - hit * step);
+        }
+        return s;
+    };
+    int s = search(0, p.B, run);
+    const int last = search(s, p.B - s, min(run + kSlotRun, (long long)p.total_new) - 1);
+    int start = 0, next = 0, cached = 0, end = 0;
+    auto enter = [&](int b) {
+        const Lengths l = lengths_of(p, b);
+        start = p.cu_new[b];
+        next = p.cu_new[b + 1];
+        cached = l.cached;
+        end = l.end;
+    };
+    if (p.B > 0) enter(s);
+    for (int i = 2 * lane; i < kSlotRun; i += 64) {
+        int64_t out[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const long long t = run + i + e;
+            if (t >= next && s < last) {
+                int hi = last + 1;
+                while (hi - s > 1) {
+                    const int mid = (s + hi) / 2;
+                    if (p.cu_new[mid] <= t) s = mid;
+                    else hi = mid;
+                }
+                enter(s);
+            }
+            out[e] = -1;
+            const long long pos = cached + t - start;
+            if (t < next && pos < end) {
+                const int page = p.page_table[(size_t)s * p.max_pages + pos / kTile];
+                if (page >= 0) out[e] = (int64_t)page * kTile + pos % kTile;
+            }
+        }
+        if (run + i + 1 < p.total_new) *reinterpret_cast<longlong2*>(p.slots + run + i) = make_longlong2(out[0], out[1]);
+        else if (run + i < p.total_new) p.slots[run + i] = out[0];
+    }
+}
+
+// seq_lens in place of cached_lens, once the slots no longer need those.
+__global__ void __launch_bounds__(256) lens_kernel(const AssignParams p) {
+    pdl_wait_primary();
+    pdl_launch_dependents();
+    const int b = blockIdx.x * 256 + threadIdx.x;
+    if (b < p.B) p.seq_lens[b] = lengths_of(p, b).end;
 }
 
 struct AppendParams {
@@ -193,7 +287,8 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
     const long long n = (long long)p.T * p.Hkv * C;
     for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
         const int c = (int)(i % C);
-        const int h = (int)(i / C % p.Hkv), t = (int)(i / C / p.Hkv);
+        const unsigned th = (unsigned)(i / C);  // token * Hkv + head
+        const int t = (int)(th / (unsigned)p.Hkv), h = (int)(th - (unsigned)t * p.Hkv);
         const long long row = pool_row(p, t, h);
         if (row < 0) continue;
         const uint4 kk = *reinterpret_cast<const uint4*>(p.k + (size_t)t * p.k_stride + (size_t)h * D + c * 8);
@@ -214,13 +309,38 @@ __device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
     return r;
 }
 
-// The row as fd_quantize_kv_fp8 encodes it: s = max |x| / 448, codes e4m3(x / s)
-// (binary32 divisions, so that both write the same bytes).  The row's D / 8
-// lanes hold 8 channels each.
-template <int D>
-__device__ __forceinline__ void encode_row(const uint16_t* x, uint8_t* codes, float* scale, bool live, int c) {
-    constexpr int C = D / 8;
-    const uint4 w = live ? *reinterpret_cast<const uint4*>(x + c * 8) : make_uint4(0u, 0u, 0u, 0u);
+// e4m3 codes of x / s as the binary32 division gives them.  A quotient by the
+// rounded reciprocal r is within 3 ulp of that (r: 1/2 ulp of 1/s, which is
+// at most 1 ulp of the product, and the product's own rounding), so both round
+// to the same code unless a border between two codes lies among those ulps.
+// Every border is a multiple of 2^-10 with at most 5 significant bits: its
+// lower 19 mantissa bits are 0.  So only a quotient with those bits within 8 of
+// 0 (one in 2^15) is divided again.
+struct Scale {
+    float s, r;
+    bool plain;  // s, 1 / s normal: the argument above holds
+};
+__device__ __forceinline__ Scale make_scale(float amax) {
+    Scale c;
+    c.s = amax / 448.0f;
+    c.r = 1.0f / c.s;
+    c.plain = c.s > 1e-30f && c.s < 1e30f;
+    return c;
+}
+__device__ __forceinline__ bool near_border(float q) { return ((__float_as_uint(q) + 8u) & 0x7ffffu) <= 16u; }
+__device__ __forceinline__ uint32_t e4m3_quotients(const Scale& c, float x, float y) {
+    float u = x * c.r, v = y * c.r;
+    if (!c.plain || near_border(u) || near_border(v)) {
+        u = c.s != 0.f ? x / c.s : 0.f;
+        v = c.s != 0.f ? y / c.s : 0.f;
+    }
+    return e4m3_pair(u, v);
+}
+
+// The row as fd_quantize_kv_fp8 encodes it (the same bytes): s = max |x| / 448,
+// codes e4m3(x / s).  C lanes hold the row, 8 channels each.
+template <int C>
+__device__ __forceinline__ void encode_row(uint4 w, uint8_t* codes, float* scale, bool live, int c) {
     const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
     float2 f[4];
     float amax = 0.f;
@@ -231,16 +351,12 @@ __device__ __forceinline__ void encode_row(const uint16_t* x, uint8_t* codes, fl
     }
 #pragma unroll
     for (int o = C / 2; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    const float s = amax / 448.0f;
-    uint32_t out[2] = {0u, 0u};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const uint32_t pair = s != 0.f ? e4m3_pair(f[e].x / s, f[e].y / s) : 0u;
-        out[e >> 1] |= pair << (16 * (e & 1));
-    }
+    const Scale s = make_scale(amax);
+    const uint32_t lo = e4m3_quotients(s, f[0].x, f[0].y) | e4m3_quotients(s, f[1].x, f[1].y) << 16;
+    const uint32_t hi = e4m3_quotients(s, f[2].x, f[2].y) | e4m3_quotients(s, f[3].x, f[3].y) << 16;
     if (!live) return;
-    *reinterpret_cast<uint2*>(codes + c * 8) = make_uint2(out[0], out[1]);
-    if (c == 0) *scale = s;
+    *reinterpret_cast<uint2*>(codes + c * 8) = make_uint2(lo, hi);
+    if (c == 0) *scale = s.s;
 }
 
 template <int D>
@@ -254,12 +370,16 @@ __global__ void __launch_bounds__(256) append_fp8_kernel(const AppendParams p) {
     for (long long i0 = (long long)blockIdx.x * 256 + (threadIdx.x & ~31); i0 < n; i0 += step) {
         const long long i = i0 + (threadIdx.x & 31);
         const int c = (int)(i % C);
-        const int h = (int)(i / C % p.Hkv), t = (int)(i / C / p.Hkv);
+        const unsigned th = (unsigned)(i / C);  // token * Hkv + head
+        const int t = (int)(th / (unsigned)p.Hkv), h = (int)(th - (unsigned)t * p.Hkv);
         const long long row = i < n ? pool_row(p, t, h) : -1;
-        encode_row<D>(p.k + (size_t)t * p.k_stride + (size_t)h * D, static_cast<uint8_t*>(p.k_pages) + row * D,
-                      p.k_scales + row, row >= 0, c);
-        encode_row<D>(p.v + (size_t)t * p.v_stride + (size_t)h * D, static_cast<uint8_t*>(p.v_pages) + row * D,
-                      p.v_scales + row, row >= 0, c);
+        uint4 k = make_uint4(0u, 0u, 0u, 0u), v = k;
+        if (row >= 0) {
+            k = *reinterpret_cast<const uint4*>(p.k + (size_t)t * p.k_stride + (size_t)h * D + c * 8);
+            v = *reinterpret_cast<const uint4*>(p.v + (size_t)t * p.v_stride + (size_t)h * D + c * 8);
+        }
+        encode_row<C>(k, static_cast<uint8_t*>(p.k_pages) + row * D, p.k_scales + row, row >= 0, c);
+        encode_row<C>(v, static_cast<uint8_t*>(p.v_pages) + row * D, p.v_scales + row, row >= 0, c);
     }
 }
 
@@ -281,10 +401,36 @@ cudaError_t append_grid(long long n, unsigned* grid) {
 
 }  // namespace
 
+// Up to this many new tokens assign_kernel writes the slots itself (a round of
+// its block per 1024); more go to slots_kernel on the whole GPU.
+constexpr int kSlotsHere = 8192;
+// From this bound on the new pages on, a cluster of eight CTAs shares them out.
+constexpr int kPagesAlone = 2048;
+
 cudaError_t launch_assign(const AssignArgs& a, cudaStream_t stream) {
     AssignParams p{a.cached_lens, a.new_lens, a.B, a.page_table, a.max_pages, a.free_pages, a.num_free, a.free_head,
-                   a.total_new, a.seq_lens, a.cu_new, a.slots, a.free_head_out};
-    return launch_pdl(assign_kernel, dim3(1), dim3(kAssignThreads), 0, stream, p);
+                   a.total_new, a.seq_lens, a.cu_new, a.slots, a.free_head_out, 0, 0};
+    p.slots_here = a.total_new <= kSlotsHere;
+    p.lens_here = p.slots_here || a.seq_lens != a.cached_lens;
+    const unsigned parts = (long long)a.total_new / kTile + a.B > kPagesAlone ? 8 : 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(parts);
+    cfg.blockDim = dim3(kAssignThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = parts;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = parts > 1 ? 2 : 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, assign_kernel, p);
+    if (e != cudaSuccess || p.slots_here) return e;
+    const unsigned blocks = (unsigned)(((long long)a.total_new + 8 * kSlotRun - 1) / (8 * kSlotRun));
+    e = launch_pdl(slots_kernel, dim3(blocks), dim3(256), 0, stream, p);
+    if (e != cudaSuccess || p.lens_here || a.B == 0) return e;
+    return launch_pdl(lens_kernel, dim3((a.B + 255) / 256), dim3(256), 0, stream, p);
 }
 
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream) {

@@ -175,37 +175,46 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Shared-memory operand descriptor, 128-byte swizzle: address and both byte
-// offsets in units of 16 bytes, descriptor version 1, layout 2.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-    return (uint64_t)((addr & 0x3ffffu) >> 4) | (uint64_t)(lbo >> 4) << 16 | (uint64_t)(sbo >> 4) << 32 |
-           1ull << 46 | 2ull << 61;
-}
-// Channels contiguous (Q and K): 8-row groups 1024 bytes apart.
-__device__ __forceinline__ uint64_t desc_rows(uint32_t addr) { return smem_desc(addr, 16, 1024); }
-// Tokens as the contraction, channels contiguous (V): 64-channel boxes one BOX
-// apart, groups of 8 tokens 1024 bytes apart.
-__device__ __forceinline__ uint64_t desc_cols(uint32_t addr) { return smem_desc(addr, 128 * 128, 1024); }
+// Shared-memory operand descriptors, 128-byte swizzle: the lower word holds the
+// address and the leading byte offset in units of 16 bytes, the upper one the
+// stride byte offset (1024: groups of 8 rows or tokens), version 1, layout 2.
+constexpr uint32_t kDescHi = 1024u >> 4 | 1u << 14 | 2u << 29;
+// Channels contiguous (Q and K): the leading offset is not used.
+__device__ __forceinline__ uint32_t desc_rows(uint32_t addr) { return (addr & 0x3ffffu) >> 4 | 1u << 16; }
+// Tokens as the contraction, channels contiguous (V): 64-channel boxes 128 * 128 bytes apart.
+__device__ __forceinline__ uint32_t desc_cols(uint32_t addr) { return (addr & 0x3ffffu) >> 4 | (128u * 128u >> 4) << 16; }
 
 // Instruction descriptor: bf16 x bf16 -> fp32, M = 128, N columns; bit 16: B
 // with its N index contiguous.
 __host__ __device__ constexpr uint32_t mma_desc(int n, bool b_cols) {
     return 1u << 4 | 1u << 7 | 1u << 10 | (b_cols ? 1u << 16 : 0u) | (uint32_t)(n / 8) << 17 | 8u << 24;
 }
-// One thread: D[tmem] (+)= A[smem] B[smem]^T, 16 deep.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// One thread of the warp, the same at every call.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
+}
+// A value that all lanes hold, in a form that the compiler knows to be uniform
+// (tcgen05 operands live in uniform registers).
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __reduce_or_sync(0xffffffffu, x); }
+
+// D[tmem] (+)= A[smem] B[smem]^T, 16 deep; a and b are lower descriptor words.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHi)
         : "memory");
 }
 // The same with A in tensor memory (bf16 pairs, one 32-bit column per pair).
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "mov.b64 db, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHi)
         : "memory");
 }
 // `bar` gets one arrival when every MMA this thread issued so far is done.
@@ -279,6 +288,8 @@ rows_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUt
         most = min(most, c0 + p.chunk) - c0;
         nb[i] = ntok > 0 && most > 0 ? (most + kBlock - 1) / kBlock : 0;
     }
+    nb[0] = (int)uniform(nb[0]);
+    nb[1] = (int)uniform(nb[1]);
     const int blocks = max(nb[0], nb[1]);
 
     if (threadIdx.x == 0) {
@@ -365,27 +376,27 @@ rows_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUt
                 ok = ok && warp_wait(&full[stage], (uint32_t)(n / STAGES) & 1u);
                 ++n;
             };
+            const uint32_t tm = uniform(tmem);
             auto qk = [&](int i, int stage) {  // S_i = Q_i K^T
-                if (lane == 0) {
-                    const uint32_t qa = q_at + (DUAL ? i : 0) * TILE, ka = ring_at + stage * TILE;
+                const uint32_t qa = desc_rows(q_at + (DUAL ? i : 0) * TILE), ka = desc_rows(ring_at + stage * TILE);
+                if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t off = (kk / 4) * BOX + (kk % 4) * 32;
-                        mma_ss(tmem + i * 128, desc_rows(qa + off), desc_rows(ka + off), IQK, kk > 0);
+                        const uint32_t off = ((kk / 4) * BOX + (kk % 4) * 32) >> 4;
+                        mma_ss(tm + i * 128, qa + off, ka + off, IQK, kk > 0);
                     }
                 }
             };
             auto pv = [&](int i, int stage, bool first) {  // O_i += P_i V
-                if (lane == 0) {
-                    const uint32_t va = ring_at + stage * TILE;
+                const uint32_t va = desc_cols(ring_at + stage * TILE);
+                if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < kBlock / 16; ++kk)
-                        mma_ts(tmem + 256 + i * D, tmem + i * 128 + kk * 8, desc_cols(va + kk * 16 * 128), IPV,
-                               !first || kk > 0);
+                        mma_ts(tm + 256 + i * D, tm + i * 128 + kk * 8, va + (kk * 16 * 128 >> 4), IPV, !first || kk > 0);
                 }
             };
             auto commit = [&](uint64_t* bar) {
-                if (lane == 0) mma_commit(bar);
+                if (elect_one()) mma_commit(bar);
             };
             // Value rows past the sequence may hold anything; their weight is 0, but 0 * NaN is NaN.
             auto clear_tail = [&](int j, int stage) {
