@@ -330,32 +330,45 @@ int paged_entry(Cache cache, const void* q, const void* k_pages, const void* v_p
 // Attention of packed query rows (prompts, prompt tails) and the decode of a
 // batch with a shared prefix.
 
-// Chunks of the keys for `ctas` CTAs per chunk: one while those fill the SMs
-// twice, else enough chunks for about four CTAs per SM (sequences are ragged
-// and the causal triangle halves the work of a whole prompt), each of at least
-// 512 keys.
+// Chunks of the keys.
 struct RowsPlan {
     int splits, chunk;
 };
 
-RowsPlan rows_plan(long long ctas, int max_k, int requested) {
-    const int sms = requested > 0 ? 0 : current_sm_count();
-    long long want = requested;
-    if (requested <= 0) {
-        want = 1;
-        if (sms > 0 && ctas > 0 && ctas < 2LL * sms) want = (4LL * sms + ctas - 1) / ctas;
-        const long long most = max_k / 512;
-        if (want > most) want = most;
-        if (want < 1) want = 1;
-    }
-    long long chunk = (max_k + want - 1) / want;
+// `splits` chunks of max_k keys, whole 128-key blocks each.
+RowsPlan rows_chunks(int max_k, long long splits, bool exact) {
+    long long chunk = (max_k + splits - 1) / splits;
     chunk = (chunk + 127) / 128 * 128;
     if (chunk < 128) chunk = 128;
     RowsPlan pl;
     pl.chunk = (int)chunk;
-    pl.splits = requested > 0 ? requested : (int)((max_k + chunk - 1) / chunk);
+    pl.splits = exact ? (int)splits : (int)((max_k + chunk - 1) / chunk);
     if (pl.splits < 1) pl.splits = 1;
     return pl;
+}
+
+// The shared part of a shared-prefix decode: `ctas` CTAs per chunk, one per SM
+// at a time, all with the same work.  A wave of chunks of c blocks takes about
+// c + 4 blocks of time (set-up, first copies, last output), every chunk costs
+// merge work, so: the count with the least waves x (c + 4) + chunks / 8.
+RowsPlan shared_rows_plan(long long ctas, int max_k, int requested) {
+    if (requested > 0) return rows_chunks(max_k, requested, true);
+    const int sms = current_sm_count(), blocks = (max_k + 127) / 128;
+    long long best_s = 1;
+    if (sms > 0 && ctas > 0) {
+        double best = 1e300;
+        for (long long S = 1; S <= blocks && (S == 1 || ctas * S <= 8LL * sms); ++S) {
+            const long long c = (blocks + S - 1) / S;
+            if ((blocks + c - 1) / c != S) continue;  // the chunks of a smaller count
+            const long long waves = (ctas * S + sms - 1) / sms;
+            const double cost = (double)waves * (double)(c + 4) + (double)S / 8.0;
+            if (cost < best) {
+                best = cost;
+                best_s = S;
+            }
+        }
+    }
+    return rows_chunks(max_k, best_s, false);
 }
 
 int check_rows(int B, int total_q, int Hq, int Hkv, int max_k, int d, int num_splits) {
@@ -363,12 +376,22 @@ int check_rows(int B, int total_q, int Hq, int Hkv, int max_k, int d, int num_sp
     if (st != FD_OK) return st;
     if (total_q < 0 || total_q > (1 << 30) || num_splits < 0 || num_splits > 65535) return FD_ERR_INVALID_ARG;
     // grid x and the row indices of the tile copies are 32-bit
-    if (fd::rows_tiles(B, total_q, Hq / Hkv) * Hkv > 0x7fffffffLL) return FD_ERR_UNSUPPORTED;
+    if (fd::rows_tiles(B, total_q, Hq / Hkv, true) * Hkv > 0x7fffffffLL) return FD_ERR_UNSUPPORTED;
     return FD_OK;
 }
 
+// Prompts: one chunk while the tiles fill the SMs twice, else enough chunks for
+// about four CTAs per SM (the sequences' lengths are not known here), each of
+// at least 512 keys.
 RowsPlan prefill_plan(int B, int total_q, int Hq, int Hkv, int max_k, int num_splits) {
-    return rows_plan(fd::rows_tiles(B, total_q, Hq / Hkv) * Hkv, max_k, num_splits);
+    if (num_splits > 0) return rows_chunks(max_k, num_splits, true);
+    const int sms = current_sm_count(), per = fd::rows_tokens(B, total_q, Hq / Hkv);
+    const long long mean = B > 0 ? (total_q + B - 1) / B : 0;  // tokens of a sequence
+    const long long ctas = (long long)B * ((mean + per - 1) / per) * Hkv;
+    long long want = 1;
+    if (sms > 0 && ctas > 0 && ctas < 2LL * sms) want = (4LL * sms + ctas - 1) / ctas;
+    if (want > max_k / 512) want = max_k / 512;
+    return rows_chunks(max_k, want < 1 ? 1 : want, false);
 }
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -408,9 +431,8 @@ int prefill_entry(fd::RowsArgs& a, int num_splits, int out_dtype, void* workspac
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const cudaError_t e = fd::launch_rows(a, s);
     if (e != cudaSuccess || a.direct) return to_status(e);
-    // every record of a row is written: a merge over `splits` chunks of a full row
-    return to_status(fd::launch_merge(a.part_o, a.part_ml, nullptr, a.total_q, a.Hq, pl.splits * kTile, a.D,
-                                      pl.splits, kTile, a.out, a.out_bf16, a.lse, s));
+    return to_status(fd::launch_merge_list(a.part_o, a.part_ml, a.cu_q, a.B, a.total_q, a.Hq, a.D, pl.splits, a.out,
+                                           a.out_bf16, a.lse, s));
 }
 
 // The two parts of a shared-prefix decode: chunks of the shared tokens, then
@@ -423,7 +445,7 @@ struct SharedPlan {
 
 SharedPlan shared_plan(int B, int Hq, int Hkv, int prefix_len, int L_own, int d, int num_splits) {
     SharedPlan s;
-    s.shared = rows_plan(fd::rows_tiles(1, B, Hq / Hkv) * Hkv, prefix_len, num_splits);
+    s.shared = shared_rows_plan(fd::rows_tiles(1, B, Hq / Hkv, false) * Hkv, prefix_len, num_splits);
     s.own = decode_plan(B, Hq, Hkv, L_own, d, 0, true);
     s.list = s.shared.splits + (L_own > 0 ? s.own.splits : 0);
     return s;
@@ -489,8 +511,7 @@ int shared_entry(fd::RowsArgs& r, fd::DecodeArgs& o, int prefix_len, int L_own, 
         e = fd::launch_decode(o, s);
         if (e != cudaSuccess) return to_status(e);
     }
-    return to_status(fd::launch_merge(ws, ml, nullptr, o.B, o.Hq, pl.list * kTile, o.D, pl.list, kTile, o.out,
-                                      out_bf16, o.lse, s));
+    return to_status(fd::launch_merge_list(ws, ml, nullptr, 0, o.B, o.Hq, o.D, pl.list, o.out, out_bf16, o.lse, s));
 }
 
 }  // namespace

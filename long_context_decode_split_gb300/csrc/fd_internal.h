@@ -164,10 +164,16 @@ struct RowsArgs {
     int rec0, rec_stride;     // (every record of a query row is written, empty ones with m = -inf)
     int direct;               // write out/lse instead of records
 };
-// CTAs of one chunk and KV head that `total_q` tokens in B sequences take at most.
-long long rows_tiles(int B, int total_q, int G);
+// Tiles of `total_q` tokens: how many tokens one takes, and how many tiles there are at most
+// (B sequences by offsets) or exactly (one sequence).
+int rows_tokens(int B, int total_q, int G);
+long long rows_tiles(int B, int total_q, int G, bool offsets);
 cudaError_t launch_rows(const RowsArgs& a, cudaStream_t stream);
 cudaError_t rows_status_read(unsigned* bits, bool clear);
+// Merge of n records per row, all of them written (m = -inf: nothing attended).
+// cu (or null: all): only the tokens cu[0] .. cu[B] - 1 have records and results.
+cudaError_t launch_merge_list(const float* part_o, const float* part_ml, const int32_t* cu, int B, int tokens, int Hq,
+                              int D, int n, void* out, int out_bf16, float* lse, cudaStream_t stream);
 
 // Page assignment and cache append (fd_pages.cu).
 struct AssignArgs {

@@ -93,6 +93,23 @@ def test_foreign_rows_do_not_leak(fd):
     assert torch.all(out[sum(lens):] == 7.0) and torch.all(lse[sum(lens):] == 7.0)
 
 
+@pytest.mark.parametrize("num_splits", [2, 30])
+def test_rows_of_no_sequence_are_left_alone_by_the_merge(fd, num_splits):
+    g = generator(17)
+    T, d = 900, 128
+    q, k, v = randn(g, T, 4, d), randn(g, T, 2, d), randn(g, T, 2, d)
+    cu = torch.tensor([100, 160, 700], dtype=torch.int32, device="cuda")
+    n = fd.fd_prefill_workspace_size(2, T, 4, 2, T, d, num_splits)
+    ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")  # NaN in every record
+    out = torch.full((T, 4, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((T, 4), 7.0, dtype=torch.float32, device="cuda")
+    fd.fd_prefill_packed(q, k, v, cu, num_splits=num_splits, out=out, lse=lse, workspace=ws)
+    for a, b in ((100, 160), (160, 700)):
+        check_rows(out[a:b], lse[a:b], attend64(q[a:b], k[a:b], v[a:b], limits(b - a, b - a, True), 1 / math.sqrt(d)))
+    for a, b in ((0, 100), (700, 900)):
+        assert torch.all(out[a:b] == 7.0) and torch.all(lse[a:b] == 7.0)
+
+
 def test_scales_and_extreme_scores(fd):
     g = generator(11)
     for std, scale in ((30.0, 1.0), (1e-3, 0.1), (1.0, 1e-6)):
