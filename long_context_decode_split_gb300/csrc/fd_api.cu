@@ -376,7 +376,8 @@ int check_rows(int B, int total_q, int Hq, int Hkv, int max_k, int d, int num_sp
     if (st != FD_OK) return st;
     if (total_q < 0 || total_q > (1 << 30) || num_splits < 0 || num_splits > 65535) return FD_ERR_INVALID_ARG;
     // grid x and the row indices of the tile copies are 32-bit
-    if (fd::rows_tiles(B, total_q, Hq / Hkv, true) * Hkv > 0x7fffffffLL) return FD_ERR_UNSUPPORTED;
+    const long long ctas = fd::rows_tiles(B, total_q, Hq / Hkv, true) * Hkv;
+    if (ctas * (num_splits > 0 ? num_splits : 1) > 0x7fffffffLL) return FD_ERR_UNSUPPORTED;
     return FD_OK;
 }
 

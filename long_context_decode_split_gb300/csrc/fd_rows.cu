@@ -33,7 +33,8 @@ struct RowsParams {
     int max_k;
     float scale_log2;
     int causal;
-    int chunk;
+    int splits, chunk;
+    int tiles;  // slots of every (head, chunk)
     void* out;
     int out_bf16;
     float* lse;
@@ -54,13 +55,13 @@ struct RowsItem {
 __device__ __forceinline__ int checked_offset(const int32_t* cu, int i, int lo, int hi) {
     const int c = cu[i];
     if (c < lo || c > hi) {
-        if (threadIdx.x == 0) atomicOr(&g_status_rows, kStatusBadSeqLen);
+        if ((threadIdx.x & 31) == 0) atomicOr(&g_status_rows, kStatusBadSeqLen);
         return c < lo ? lo : hi;
     }
     return c;
 }
 
-// Tile slots: sequence s owns the slots floor(cu_q[s] / per) + s up to those of
+// All lanes of a warp together.  Tile slots: sequence s owns the slots floor(cu_q[s] / per) + s up to those of
 // s + 1, at least as many as the tiles it has (`per` tokens each), so a slot's
 // sequence is found by a search of cu_q alone.
 __device__ __forceinline__ RowsItem find_item(const RowsParams& p, int slot, int per) {
@@ -88,7 +89,7 @@ __device__ __forceinline__ RowsItem find_item(const RowsParams& p, int slot, int
     }
     it.t0 = (slot - (it.q0 / per + it.seq)) * per;
     if (p.page_table) {
-        it.Lk = clamped_len(p.seq_lens, it.seq, p.max_k, &g_status_rows);
+        it.Lk = p.seq_lens ? checked_offset(p.seq_lens, it.seq, 0, p.max_k) : p.max_k;
     } else if (p.cu_k) {
         it.k0 = checked_offset(p.cu_k, it.seq, 0, p.total_k);
         it.Lk = checked_offset(p.cu_k, it.seq + 1, it.k0, p.total_k) - it.k0;
@@ -125,7 +126,7 @@ struct RowsGeo {
     static constexpr int TILE = BOXES * BOX;        // 128 rows of D channels
     static constexpr int TILES = DUAL ? 2 : 1;      // of query rows
     static constexpr int STAGES = D == 128 ? (DUAL ? 5 : 6) : 8;
-    static constexpr int SMEM = 1024 + (TILES + STAGES) * TILE + (2 * STAGES + 6) * 8 + 16 + 2 * 128 * 4;
+    static constexpr int SMEM = 1024 + (TILES + STAGES) * TILE + (2 * STAGES + 14) * 8 + 16 + 2 * 64 + 16 + 2 * 128 * 4;
     static_assert(SMEM <= 232448, "shared memory of a CTA");
 };
 
@@ -237,6 +238,56 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, int x, 
         : "memory");
 }
 
+// ---- work distribution ------------------------------------------------------------
+
+// The next CTA of the grid that has not started yet is cancelled and its index
+// written to `answer` (16 bytes, counted on `bar`): a running CTA takes its
+// work over, without a counter in memory.
+__device__ __forceinline__ void next_cta_request(void* answer, uint64_t* bar) {
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+            smem_u32(answer)),
+        "r"(smem_u32(bar))
+        : "memory");
+}
+// Index of the cancelled CTA, or -1: none is left (then no further request).
+__device__ __forceinline__ int next_cta(const void* answer) {
+    uint32_t x, ok;
+    asm volatile(
+        "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t.reg .b32 y, z;\n\t"
+        "ld.shared.b128 r, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "selp.u32 %1, 1, 0, p;\n\t"
+        "mov.b32 %0, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, y, z, _}, r;\n\t}"
+        : "=r"(x), "=r"(ok)
+        : "r"(smem_u32(answer))
+        : "memory");
+    // order the read before the next answer's write
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    return ok ? (int)x : -1;
+}
+
+// Named barrier whose threads all learn whether any of them passed `x`.
+__device__ __forceinline__ bool named_barrier_or(int id, int nthreads, bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %3, 0;\n\t"
+        "bar.red.or.pred p, %1, %2, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)
+        : "r"(id), "r"(nthreads), "r"((uint32_t)x)
+        : "memory");
+    return r != 0;
+}
+
+// A piece of work as the copy warp hands it to the others.
+struct Work {
+    int valid;  // 0: there is no more
+    RowsItem it;
+    int h, split;
+    int nb[2];  // blocks of keys of each pipeline
+};
+
 // ---- the pass -------------------------------------------------------------------
 //
 // S = Q K^T and O += P V run on tcgen05 with S, P and O in tensor memory.  Two
@@ -251,6 +302,10 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, int x, 
 // pipeline run in the order they are issued, so S of block j + 1 is computed
 // after P of block j was read.  Tensor memory columns: S0 S1 | O0 O1.
 // Keys and values pass through one ring of 128-row tiles (K0 V0 K1 V1 ..).
+//
+// A CTA goes from one piece of work to the next without a stop: the copy warp
+// is ahead with the next queries and keys, and the first products of the next
+// piece run while the softmax warpgroups write the last one's results.
 template <int D, bool PAGED, bool DUAL>
 __global__ void __launch_bounds__(kThreads, 1)
 rows_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
@@ -264,45 +319,35 @@ rows_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUt
     uint64_t* full = reinterpret_cast<uint64_t*>(ring + STAGES * TILE);
     uint64_t* empty = full + STAGES;
     uint64_t* q_full = empty + STAGES;
-    uint64_t* s_full = q_full + 1;  // [2] S of the next block (at the end: O) is complete
-    uint64_t* p_full = s_full + 2;  // [2] P is in place, and O is rescaled
-    uint64_t* drained = p_full + 2;
-    uint32_t* tmem_at = reinterpret_cast<uint32_t*>(drained + 1);
-    float* join = reinterpret_cast<float*>(tmem_at + 4);  // [2][128] m and l of pipeline 1 (single)
+    uint64_t* q_empty = q_full + 1;
+    uint64_t* s_full = q_empty + 1;     // [2] S of the next block is complete
+    uint64_t* p_full = s_full + 2;      // [2] P is in place, and O is rescaled
+    uint64_t* o_full = p_full + 2;      // [2] O is complete
+    uint64_t* work_full = o_full + 2;   // [2]
+    uint64_t* work_empty = work_full + 2;
+    uint64_t* next_full = work_empty + 2;
+    uint64_t* drained = next_full + 1;
+    unsigned char* answer = reinterpret_cast<unsigned char*>(drained + 1);  // 16 bytes
+    Work* work = reinterpret_cast<Work*>(answer + 16);                      // [2]
+    uint32_t* tmem_at = reinterpret_cast<uint32_t*>(work + 2);
+    float* join = reinterpret_cast<float*>(tmem_at + 4);  // [2][128] what the pipelines tell each other (single)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    pdl_wait_primary();
-    pdl_launch_dependents();
-    const int h = blockIdx.x % p.Hkv, split = blockIdx.y;
-    const RowsItem it = find_item(p, (int)(gridDim.x / p.Hkv - 1 - blockIdx.x / p.Hkv), TILES * p.tok);
-    if (it.t0 < 0 || it.t0 >= it.Lq) return;
-
-    // blocks of keys of each pipeline
-    const int c0 = split * p.chunk;
-    int nb[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int first = it.t0 + (DUAL ? i : 0) * p.tok;
-        const int ntok = min(p.tok, it.Lq - first);
-        int most = it.Lk;
-        if (p.causal) most = min(most, it.Lk - it.Lq + first + ntok);
-        most = min(most, c0 + p.chunk) - c0;
-        nb[i] = ntok > 0 && most > 0 ? (most + kBlock - 1) / kBlock : 0;
-    }
-    nb[0] = (int)uniform(nb[0]);
-    nb[1] = (int)uniform(nb[1]);
-    const int blocks = max(nb[0], nb[1]);
-
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
         mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 4);
+            mbar_init(&o_full[i], 1);
+            mbar_init(&work_full[i], 1);
+            mbar_init(&work_empty[i], 9);
         }
+        mbar_init(next_full, 1);
         mbar_init(drained, 1);
         fence_barrier_init();
     }
@@ -311,73 +356,133 @@ rows_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUt
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_at;
+    pdl_wait_primary();  // the previous kernel in the stream may still be running
+    pdl_launch_dependents();
 
     if (warp >= kCopyWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-        if (warp == kCopyWarp && lane == 0 && blocks > 0) {
-            // ---------------- copies ----------------
-            const uint32_t qbytes = (uint32_t)(p.tok * p.G * D * 2);
-            const int qtiles = DUAL && nb[1] > 0 ? 2 : 1;
-            mbar_arrive_expect_tx(q_full, qbytes * qtiles);
-            for (int i = 0; i < qtiles; ++i)
-                for (int bx = 0; bx < BOXES; ++bx)
-                    tma_load_3d(sq + i * TILE + bx * BOX, &tmq, 64 * bx, h * p.G, it.q0 + it.t0 + i * p.tok, q_full);
-            int n = 0;  // ring position
+        if (warp == kCopyWarp) {
+            // ---------------- work and copies ----------------
             bool ok = true;
-            // block j of the keys (which = 0) or values (1) into the next stage
-            auto load = [&](int j, int which) {
-                const int s = n % STAGES;
-                ok = ok && mbar_wait(&empty[s], ((uint32_t)(n / STAGES) & 1u) ^ 1u);
-                if (!ok) return;
-                const void* map = which ? static_cast<const void*>(&tmv) : static_cast<const void*>(&tmk);
-                unsigned char* dst = ring + s * TILE;
-                const int at = c0 + j * kBlock;
-                mbar_arrive_expect_tx(&full[s], TILE);
-                if (PAGED) {
+            int n = 0, qn = 0, wn = 0;  // tiles through the ring, query loads, pieces of work
+            int id = blockIdx.x;
+            for (int asked = 0; ok; ++asked) {
+                Work w;
+                w.valid = id >= 0;
+                bool some = !w.valid;
+                if (w.valid) {
+                    w.h = id % p.Hkv;
+                    const int rest = id / p.Hkv;
+                    w.split = rest % p.splits;
+                    w.it = find_item(p, p.tiles - 1 - rest / p.splits, TILES * p.tok);
+                    some = w.it.t0 >= 0 && w.it.t0 < w.it.Lq;
+                    const int c0 = w.split * p.chunk;
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const int pi = at / kTile + half;
-                        int y = p.zero_row;  // past the pool: zeros
-                        if (pi * kTile < it.Lk && pi < p.max_pages) {
-                            const int pg = p.page_table[(size_t)it.seq * p.table_stride + pi];
-                            if (pg >= 0 && pg < p.num_pages) y = (pg * p.Hkv + h) * kTile;
-                            else atomicOr(&g_status_rows, kStatusBadPage);
-                        }
-#pragma unroll
-                        for (int bx = 0; bx < BOXES; ++bx)
-                            tma_load_2d(dst + bx * BOX + half * (BOX / 2), map, 64 * bx, y, &full[s]);
+                    for (int i = 0; i < 2; ++i) {
+                        const int first = w.it.t0 + (DUAL ? i : 0) * p.tok;
+                        const int ntok = min(p.tok, w.it.Lq - first);
+                        int most = w.it.Lk;
+                        if (p.causal) most = min(most, w.it.Lk - w.it.Lq + first + ntok);
+                        most = min(most, c0 + p.chunk) - c0;
+                        w.nb[i] = ntok > 0 && most > 0 ? (most + kBlock - 1) / kBlock : 0;
                     }
-                } else {
-#pragma unroll
-                    for (int bx = 0; bx < BOXES; ++bx)
-                        tma_load_3d(dst + bx * BOX, map, 64 * bx, h, it.k0 + at, &full[s]);
                 }
-                ++n;
-            };
-            constexpr int AHEAD = DUAL ? 1 : 2;  // blocks by which the keys run ahead of the values
-            for (int j = 0; j < AHEAD && j < blocks; ++j) load(j, 0);
-            for (int j = 0; j < blocks; ++j) {
-                load(j, 1);
-                if (j + AHEAD < blocks) load(j + AHEAD, 0);
+                if (some) {
+                    // hand it on (or the end)
+                    const int slot = wn & 1;
+                    ok = warp_wait(&work_empty[slot], ((uint32_t)(wn >> 1) & 1u) ^ 1u);
+                    if (!ok) break;
+                    if (lane == 0) {
+                        work[slot] = w;
+                        mbar_arrive(&work_full[slot]);
+                    }
+                    ++wn;
+                    if (!w.valid) break;
+                    const int blocks = max(w.nb[0], w.nb[1]);
+                    if (blocks > 0) {
+                        ok = warp_wait(q_empty, ((uint32_t)qn & 1u) ^ 1u);
+                        if (!ok) break;
+                        ++qn;
+                        if (lane == 0) {
+                            const uint32_t qbytes = (uint32_t)(p.tok * p.G * D * 2);
+                            const int qtiles = DUAL && w.nb[1] > 0 ? 2 : 1;
+                            mbar_arrive_expect_tx(q_full, qbytes * qtiles);
+                            for (int i = 0; i < qtiles; ++i)
+                                for (int bx = 0; bx < BOXES; ++bx)
+                                    tma_load_3d(sq + i * TILE + bx * BOX, &tmq, 64 * bx, w.h * p.G,
+                                                w.it.q0 + w.it.t0 + i * p.tok, q_full);
+                        }
+                        // block j of the keys (which = 0) or values (1) into the next stage
+                        auto load = [&](int j, int which) {
+                            const int s = n % STAGES;
+                            ok = ok && warp_wait(&empty[s], ((uint32_t)(n / STAGES) & 1u) ^ 1u);
+                            if (!ok) return;
+                            if (lane == 0) {
+                                const void* map = which ? static_cast<const void*>(&tmv) : static_cast<const void*>(&tmk);
+                                unsigned char* dst = ring + s * TILE;
+                                const int at = w.split * p.chunk + j * kBlock;
+                                mbar_arrive_expect_tx(&full[s], TILE);
+                                if (PAGED) {
+#pragma unroll
+                                    for (int half = 0; half < 2; ++half) {
+                                        const int pi = at / kTile + half;
+                                        int y = p.zero_row;  // past the pool: zeros
+                                        if (pi * kTile < w.it.Lk && pi < p.max_pages) {
+                                            const int pg = p.page_table[(size_t)w.it.seq * p.table_stride + pi];
+                                            if (pg >= 0 && pg < p.num_pages) y = (pg * p.Hkv + w.h) * kTile;
+                                            else atomicOr(&g_status_rows, kStatusBadPage);
+                                        }
+#pragma unroll
+                                        for (int bx = 0; bx < BOXES; ++bx)
+                                            tma_load_2d(dst + bx * BOX + half * (BOX / 2), map, 64 * bx, y, &full[s]);
+                                    }
+                                } else {
+#pragma unroll
+                                    for (int bx = 0; bx < BOXES; ++bx)
+                                        tma_load_3d(dst + bx * BOX, map, 64 * bx, w.h, w.it.k0 + at, &full[s]);
+                                }
+                            }
+                            ++n;
+                        };
+                        constexpr int AHEAD = DUAL ? 1 : 2;  // blocks by which the keys run ahead of the values
+                        for (int j = 0; j < AHEAD && j < blocks; ++j) load(j, 0);
+                        for (int j = 0; ok && j < blocks; ++j) {
+                            load(j, 1);
+                            if (j + AHEAD < blocks) load(j + AHEAD, 0);
+                        }
+                        if (!ok) break;
+                    }
+                }
+                // all copies of this piece are under way: ask for the next one
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(next_full, 16);
+                    next_cta_request(answer, next_full);
+                }
+                ok = warp_wait(next_full, (uint32_t)asked & 1u);
+                if (ok) id = next_cta(answer);
+                __syncwarp();
             }
             if (!ok) {
                 // the others stopped early: let the copies in flight land before the CTA ends
-                atomicOr(&g_status_rows, kStatusTimeout);
-                mbar_wait(q_full, 0);
+                if (lane == 0) atomicOr(&g_status_rows, kStatusTimeout);
+                if (qn > 0) mbar_wait(q_full, (uint32_t)(qn - 1) & 1u);
                 for (int u = max(0, n - STAGES); u < n; ++u) mbar_wait(&full[u % STAGES], (uint32_t)(u / STAGES) & 1u);
+                mbar_wait(next_full, 0);
+                mbar_wait(next_full, 1);
             }
-        } else if (warp == kMmaWarp && blocks > 0) {
+        } else if (warp == kMmaWarp) {
             // ---------------- products ----------------
             constexpr uint32_t IQK = mma_desc(kBlock, false), IPV = mma_desc(D, true);
             const uint32_t q_at = smem_u32(sq), ring_at = smem_u32(ring);
-            bool ok = warp_wait(q_full, 0);
-            int n = 0;  // ring position
+            const uint32_t tm = uniform(tmem);
+            bool ok = true;
+            int n = 0, qn = 0;           // ring position, pieces of work with keys
+            uint32_t rounds0 = 0, rounds1 = 0;  // blocks of each pipeline so far
             auto arrive = [&](int& stage) {  // the next tile of the ring
                 stage = n % STAGES;
                 ok = ok && warp_wait(&full[stage], (uint32_t)(n / STAGES) & 1u);
                 ++n;
             };
-            const uint32_t tm = uniform(tmem);
             auto qk = [&](int i, int stage) {  // S_i = Q_i K^T
                 const uint32_t qa = desc_rows(q_at + (DUAL ? i : 0) * TILE), ka = desc_rows(ring_at + stage * TILE);
                 if (elect_one()) {
@@ -386,6 +491,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUt
                         const uint32_t off = ((kk / 4) * BOX + (kk % 4) * 32) >> 4;
                         mma_ss(tm + i * 128, qa + off, ka + off, IQK, kk > 0);
                     }
+                    mma_commit(&s_full[i]);
                 }
             };
             auto pv = [&](int i, int stage, bool first) {  // O_i += P_i V
@@ -399,75 +505,97 @@ rows_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUt
             auto commit = [&](uint64_t* bar) {
                 if (elect_one()) mma_commit(bar);
             };
-            // Value rows past the sequence may hold anything; their weight is 0, but 0 * NaN is NaN.
-            auto clear_tail = [&](int j, int stage) {
-                const int rows = it.Lk - (c0 + j * kBlock);
-                if (rows >= kBlock) return;
-                unsigned char* v = ring + stage * TILE;
-                for (int i = lane; i < (kBlock - rows) * 8; i += 32)
-#pragma unroll
-                    for (int bx = 0; bx < BOXES; ++bx)
-                        *reinterpret_cast<uint4*>(v + bx * BOX + rows * 128 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-            };
-            auto weights = [&](int i, int round) {
-                ok = ok && warp_wait(&p_full[i], (uint32_t)round & 1u);
+            auto weights = [&](int i) {
+                uint32_t& rounds = i ? rounds1 : rounds0;
+                ok = ok && warp_wait(&p_full[i], rounds & 1u);
+                ++rounds;
                 tc_fence_after();
             };
-            int sk = 0, sv = 0;
-            if (DUAL) {
-                arrive(sk);
-                if (ok) {
-                    for (int i = 0; i < 2; ++i)
-                        if (nb[i] > 0) {
-                            qk(i, sk);
-                            commit(&s_full[i]);
-                        }
-                    commit(&empty[sk]);
-                }
-                for (int j = 0; ok && j < blocks; ++j) {
-                    arrive(sv);
-                    if (!ok) break;
-                    clear_tail(j, sv);
-                    const bool more = j + 1 < blocks;
-                    if (more) arrive(sk);
-                    if (!ok) break;
+            for (int wn = 0; ok; ++wn) {
+                const int slot = wn & 1;
+                ok = warp_wait(&work_full[slot], (uint32_t)(wn >> 1) & 1u);
+                if (!ok) break;
+                const Work& w = work[slot];
+                const bool valid = uniform(w.valid) != 0;
+                const int nb0 = (int)uniform(w.nb[0]), nb1 = (int)uniform(w.nb[1]);
+                const int left0 = w.it.Lk - w.split * p.chunk;  // keys of the sequence from the chunk on
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&work_empty[slot]);
+                if (!valid) break;
+                const int blocks = max(nb0, nb1);
+                if (blocks == 0) continue;
+                // Value rows past the sequence may hold anything; their weight is 0, but 0 * NaN is NaN.
+                auto clear_tail = [&](int j, int stage) {
+                    const int rows = left0 - j * kBlock;
+                    if (rows >= kBlock) return;
+                    unsigned char* v = ring + stage * TILE;
+                    for (int i = lane; i < (kBlock - rows) * 8; i += 32)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        if (j < nb[i]) {
-                            weights(i, j);
-                            if (!ok) break;
-                            pv(i, sv, j == 0);
-                            if (j + 1 < nb[i]) qk(i, sk);
-                            commit(&s_full[i]);
-                        }
-                    }
-                    if (!ok) break;
-                    commit(&empty[sv]);
-                    if (more) commit(&empty[sk]);
-                }
-            } else {
-                for (int j = 0; ok && j < 2 && j < blocks; ++j) {
+                        for (int bx = 0; bx < BOXES; ++bx)
+                            *reinterpret_cast<uint4*>(v + bx * BOX + rows * 128 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                };
+                ok = warp_wait(q_full, (uint32_t)qn & 1u);
+                ++qn;
+                int sk = 0, sv = 0;
+                if (DUAL) {
                     arrive(sk);
                     if (!ok) break;
-                    qk(j, sk);
-                    commit(&s_full[j]);
+                    if (nb0 > 0) qk(0, sk);
+                    if (nb1 > 0) qk(1, sk);
                     commit(&empty[sk]);
-                }
-                for (int j = 0; ok && j < blocks; ++j) {
-                    const int i = j & 1;
-                    arrive(sv);
-                    if (!ok) break;
-                    clear_tail(j, sv);
-                    if (j + 2 < blocks) arrive(sk);
-                    weights(i, j >> 1);
-                    if (!ok) break;
-                    pv(i, sv, j < 2);
-                    if (j + 2 < blocks) qk(i, sk);
-                    commit(&s_full[i]);
-                    commit(&empty[sv]);
-                    if (j + 2 < blocks) commit(&empty[sk]);
+                    if (blocks == 1) commit(q_empty);
+                    for (int j = 0; j < blocks; ++j) {
+                        arrive(sv);
+                        if (!ok) break;
+                        clear_tail(j, sv);
+                        const bool more = j + 1 < blocks;
+                        if (more) arrive(sk);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int nb = i ? nb1 : nb0;
+                            if (j < nb) {
+                                weights(i);
+                                if (!ok) break;
+                                pv(i, sv, j == 0);
+                                if (j + 1 < nb) qk(i, sk);
+                                else commit(&o_full[i]);
+                            }
+                        }
+                        if (!ok) break;
+                        commit(&empty[sv]);
+                        if (more) commit(&empty[sk]);
+                        if (j + 2 == blocks) commit(q_empty);
+                    }
+                } else {
+                    for (int j = 0; ok && j < 2 && j < blocks; ++j) {
+                        arrive(sk);
+                        if (!ok) break;
+                        if (j) qk(1, sk);
+                        else qk(0, sk);
+                        commit(&empty[sk]);
+                    }
+                    if (ok && blocks <= 2) commit(q_empty);
+                    for (int j = 0; ok && j < blocks; j += 2) {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            if (j + i >= blocks) break;
+                            arrive(sv);
+                            if (!ok) break;
+                            clear_tail(j + i, sv);
+                            const bool more = j + i + 2 < blocks;
+                            if (more) arrive(sk);
+                            weights(i);
+                            if (!ok) break;
+                            pv(i, sv, j == 0);
+                            if (more) qk(i, sk);
+                            else commit(&o_full[i]);
+                            commit(&empty[sv]);
+                            if (more) commit(&empty[sk]);
+                            if (j + i + 3 == blocks) commit(q_empty);
+                        }
+                    }
                 }
             }
             if (!ok) {
@@ -482,147 +610,169 @@ rows_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUt
         const int i = warp >> 2;  // pipeline
         const int r = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // 32 lanes per warp, lane in the upper half
-        const uint32_t s_at = tmem + lanes + i * 128, o_at = tmem + lanes + 256 + i * D;
-        const int first = it.t0 + (DUAL ? i : 0) * p.tok;
+        const uint32_t s_at = tmem + lanes + i * 128, o_at = tmem + lanes + 256;
         const int tk = r / p.G;
-        const bool live = tk < p.tok && first + tk < it.Lq;
-        const int lim = live ? min(visible_keys(p, it, first + tk), c0 + p.chunk) - c0 : 0;
-        const int rounds = DUAL ? nb[i] : (nb[0] + 1 - i) / 2;
-        float m = -INFINITY;
-        float2 l2 = make_float2(0.f, 0.f);
         bool ok = true;
-        for (int round = 0; round < rounds; ++round) {
-            const int j = DUAL ? round : 2 * round + i;
-            const int left = lim - j * kBlock;  // visible keys from this block on
-            bool bad[2] = {false, false};
-            if (PAGED) {
+        uint32_t s_round = 0, o_round = 0;
+        for (int wn = 0; DUAL ? ok : true; ++wn) {
+            const int slot = wn & 1;
+            ok = ok && warp_wait(&work_full[slot], (uint32_t)(wn >> 1) & 1u);
+            // the warpgroups of a single tile meet at barriers: all of them stop, or none
+            if (DUAL ? !ok : named_barrier_or(2, 256, !ok)) break;
+            const Work& wk = work[slot];
+            const bool valid = wk.valid != 0;
+            const RowsItem it = wk.it;
+            const int h = wk.h, split = wk.split;
+            const int nb = i ? wk.nb[1] : wk.nb[0];
+            const int all = wk.nb[0];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&work_empty[slot]);
+            if (!valid) break;
+            const int c0 = split * p.chunk;
+            const int first = it.t0 + (DUAL ? i : 0) * p.tok;
+            const bool live = tk < p.tok && first + tk < it.Lq;
+            const int lim = live ? min(visible_keys(p, it, first + tk), c0 + p.chunk) - c0 : 0;
+            const int rounds = DUAL ? nb : (nb + 1 - i) / 2;
+            float m = -INFINITY;
+            float2 l2 = make_float2(0.f, 0.f);
+            for (int round = 0; round < rounds; ++round) {
+                const int j = DUAL ? round : 2 * round + i;
+                const int left = lim - j * kBlock;  // visible keys from this block on
+                bool bad[2] = {false, false};
+                if (PAGED) {
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const int pi = (c0 + j * kBlock) / kTile + half;
+                        if (pi * kTile < it.Lk && pi < p.max_pages) {
+                            const int pg = p.page_table[(size_t)it.seq * p.table_stride + pi];
+                            bad[half] = pg < 0 || pg >= p.num_pages;
+                        }
+                    }
+                }
+                ok = warp_wait(&s_full[i], s_round & 1u);
+                if (!ok) break;
+                ++s_round;
+                tc_fence_after();
+                uint32_t s[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld32(s[c], s_at + 32 * c);
+                tmem_wait_ld();
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tie32(s[c]);
+                if (__any_sync(0xffffffffu, left < kBlock || bad[0] || bad[1])) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (32 * c + e >= left || bad[c >> 1]) s[c][e] = 0xff800000u;  // -inf
+                }
+                float mx[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    mx[c] = __uint_as_float(s[c][0]);
+#pragma unroll
+                    for (int e = 1; e < 32; ++e) mx[c] = fmaxf(mx[c], __uint_as_float(s[c][e]));
+                }
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+                if (__any_sync(0xffffffffu, top > m + kRescaleAt)) {
+                    const float mn = fmaxf(m, top);
+                    const float a = mn == -INFINITY ? 1.f : exp2_approx(m - mn);
+                    m = mn;
+                    l2 = f2mul(l2, make_float2(a, a));
+                    if (round > 0) {
+#pragma unroll
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t o[32];
+                            tmem_ld32(o, o_at + i * D + 32 * c);
+                            tmem_wait_ld();
+                            tie32(o);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+                            tmem_st32(o_at + i * D + 32 * c, o);
+                        }
+                    }
+                }
+                const float base = m == -INFINITY ? 0.f : m;
+                const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nb2 = make_float2(-base, -base);
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
-                    const int pi = (c0 + j * kBlock) / kTile + half;
-                    if (pi * kTile < it.Lk && pi < p.max_pages) {
-                        const int pg = p.page_table[(size_t)it.seq * p.table_stride + pi];
-                        bad[half] = pg < 0 || pg >= p.num_pages;
+                    uint32_t w[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const int c = 2 * half + e / 16, x = 2 * (e % 16);
+                        float2 f = f2fma(make_float2(__uint_as_float(s[c][x]), __uint_as_float(s[c][x + 1])), sc2, nb2);
+                        f = make_float2(exp2_approx(f.x), exp2_approx(f.y));
+                        l2 = __fadd2_rn(l2, f);
+                        w[e] = pack_bf16(f.x, f.y);
                     }
+                    tmem_st32(s_at + 32 * half, w);
                 }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[i]);
             }
-            if (!warp_wait(&s_full[i], (uint32_t)round & 1u)) {
-                ok = false;
-                break;
+            if (ok && rounds > 0) {
+                ok = warp_wait(&o_full[i], o_round & 1u);
+                ++o_round;
             }
             tc_fence_after();
-            uint32_t s[4][32];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32(s[c], s_at + 32 * c);
-            tmem_wait_ld();
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tie32(s[c]);
-            if (__any_sync(0xffffffffu, left < kBlock || bad[0] || bad[1])) {
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (32 * c + e >= left || bad[c >> 1]) s[c][e] = 0xff800000u;  // -inf
-            }
-            float mx[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                mx[c] = __uint_as_float(s[c][0]);
-#pragma unroll
-                for (int e = 1; e < 32; ++e) mx[c] = fmaxf(mx[c], __uint_as_float(s[c][e]));
-            }
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
-            if (__any_sync(0xffffffffu, top > m + kRescaleAt)) {
-                const float mn = fmaxf(m, top);
-                const float a = mn == -INFINITY ? 1.f : exp2_approx(m - mn);
-                m = mn;
-                l2 = f2mul(l2, make_float2(a, a));
-                if (round > 0) {
-#pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint32_t o[32];
-                        tmem_ld32(o, o_at + 32 * c);
-                        tmem_wait_ld();
-                        tie32(o);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
-                        tmem_st32(o_at + 32 * c, o);
-                    }
+            float l = ok ? l2.x + l2.y : 0.f;
+            if (!ok) m = -INFINITY;
+            // factors of the O of pipeline 0 and 1
+            float f0 = i ? 0.f : 1.f, f1 = i ? 1.f : 0.f;
+            const float inv_own = l > 0.f ? 1.f / l : 0.f;
+            if (DUAL) {
+                f0 *= inv_own;
+                f1 *= inv_own;
+            } else {
+                // pipeline 0 learns m and l of pipeline 1 and tells the factors; each
+                // warpgroup then writes half of the channels of the joined result
+                if (i == 1) {
+                    join[r] = m;
+                    join[128 + r] = l;
+                }
+                named_barrier(1, 256);
+                if (i == 0) {
+                    const float m1 = join[r], l1 = join[128 + r], m0 = m;
+                    m = fmaxf(m0, m1);
+                    f0 = m0 == -INFINITY ? 0.f : exp2_approx(m0 - m);
+                    f1 = m1 == -INFINITY ? 0.f : exp2_approx(m1 - m);
+                    l = f0 * l + f1 * l1;
+                    const float inv = l > 0.f ? 1.f / l : 0.f;
+                    join[r] = f0 *= inv;
+                    join[128 + r] = f1 *= inv;
+                }
+                named_barrier(1, 256);
+                if (i == 1) {
+                    f0 = join[r];
+                    f1 = join[128 + r];
                 }
             }
-            const float base = m == -INFINITY ? 0.f : m;
-            const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nb2 = make_float2(-base, -base);
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                uint32_t w[32];
-#pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    const int c = 2 * half + e / 16, x = 2 * (e % 16);
-                    float2 f = f2fma(make_float2(__uint_as_float(s[c][x]), __uint_as_float(s[c][x + 1])), sc2, nb2);
-                    f = make_float2(exp2_approx(f.x), exp2_approx(f.y));
-                    l2 = __fadd2_rn(l2, f);
-                    w[e] = pack_bf16(f.x, f.y);
-                }
-                tmem_st32(s_at + 32 * half, w);
-            }
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[i]);
-        }
-        if (ok && rounds > 0) ok = warp_wait(&s_full[i], (uint32_t)rounds & 1u);
-        if (!ok && lane == 0) atomicOr(&g_status_rows, kStatusTimeout);
-        tc_fence_after();
-        float l = ok ? l2.x + l2.y : 0.f;
-        if (!ok) m = -INFINITY;
-        float own = 1.f, other = 0.f;  // factors of this pipeline's and the other's O
-        float* o1 = reinterpret_cast<float*>(ring);  // [D][128]: O of pipeline 1
-        if (!DUAL) {
-            named_barrier(1, 256);  // both pipelines are done with the ring
-            if (i == 1) {
-                join[r] = m;
-                join[128 + r] = l;
-                if (rounds > 0) {
-#pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint32_t o[32];
-                        tmem_ld32(o, o_at + 32 * c);
-                        tmem_wait_ld();
-                        tie32(o);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o1[(32 * c + e) * 128 + r] = __uint_as_float(o[e]);
-                    }
-                }
-            }
-            named_barrier(1, 256);
-            if (i == 0) {
-                const float m1 = join[r], l1 = join[128 + r];
-                const float M = fmaxf(m, m1);
-                own = m == -INFINITY ? 0.f : exp2_approx(m - M);
-                other = m1 == -INFINITY ? 0.f : exp2_approx(m1 - M);
-                l = own * l + other * l1;
-                m = M;
-            }
-        }
-        const int head = h * p.G + r - tk * p.G;
-        const size_t row = (size_t)(it.q0 + first + tk) * p.Hq + head;
-        const size_t rec = row * p.rec_stride + p.rec0 + split;
-        const float inv = l > 0.f ? 1.f / l : 0.f;
-        own *= inv;
-        other *= inv;
-        if (DUAL || i == 0) {
+            const int head = h * p.G + r - tk * p.G;
+            const size_t row = (size_t)(it.q0 + first + tk) * p.Hq + head;
+            const size_t rec = row * p.rec_stride + p.rec0 + split;
+            const bool in0 = DUAL ? i == 0 && rounds > 0 : all > 0, in1 = DUAL ? i == 1 && rounds > 0 : all > 1;
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
+                if (!DUAL && c / (D / 64) != i) continue;
+                float f[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) f[e] = 0.f;
                 uint32_t o[32];
-                if (rounds > 0) {
+                if (in0) {
                     tmem_ld32(o, o_at + 32 * c);
                     tmem_wait_ld();
                     tie32(o);
-                }
-                float f[32];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    f[e] = own != 0.f ? __uint_as_float(o[e]) * own : 0.f;
-                    if (!DUAL && other != 0.f) f[e] += o1[(32 * c + e) * 128 + r] * other;
+                    for (int e = 0; e < 32; ++e) f[e] = f0 != 0.f ? __uint_as_float(o[e]) * f0 : 0.f;
+                }
+                if (in1) {
+                    tmem_ld32(o, o_at + D + 32 * c);
+                    tmem_wait_ld();
+                    tie32(o);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) f[e] += f1 != 0.f ? __uint_as_float(o[e]) * f1 : 0.f;
                 }
                 if (!live) continue;
                 if (!p.direct || !p.out_bf16) {
@@ -638,7 +788,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUt
                                             pack_bf16(f[8 * e + 4], f[8 * e + 5]), pack_bf16(f[8 * e + 6], f[8 * e + 7]));
                 }
             }
-            if (live) {
+            if (live && (DUAL || i == 0)) {
                 if (!p.direct) {
                     p.part_ml[2 * rec] = l > 0.f ? m : -INFINITY;
                     p.part_ml[2 * rec + 1] = l;
@@ -646,7 +796,10 @@ rows_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUt
                     p.lse[row] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
                 }
             }
+            tc_fence_before();
+            if (!DUAL) named_barrier(1, 256);  // both O and the factors are read
         }
+        if (!ok && lane == 0) atomicOr(&g_status_rows, kStatusTimeout);
         tc_fence_before();
     }
     __syncwarp();
@@ -811,6 +964,7 @@ cudaError_t launch_rows(const RowsArgs& a, cudaStream_t stream) {
     p.max_k = a.max_k;
     p.scale_log2 = a.scale * kLog2e;
     p.causal = a.causal;
+    p.splits = a.splits;
     p.chunk = a.chunk;
     p.out = a.out;
     p.out_bf16 = a.out_bf16;
@@ -839,7 +993,8 @@ cudaError_t launch_rows(const RowsArgs& a, cudaStream_t stream) {
     }
     if (!ok) return cudaErrorInvalidValue;
     const long long tiles = rows_tiles(a.B, a.total_q, p.G, a.cu_q != nullptr);
-    const dim3 grid((unsigned)(tiles * a.Hkv), (unsigned)a.splits);
+    p.tiles = (int)tiles;
+    const dim3 grid((unsigned)(tiles * a.Hkv * a.splits));
     const bool dual = rows_dual(a.B, a.total_q, p.G);
     if (a.D == 128) {
         if (paged) return dual ? launch_kernel<128, true, true>(tq, tk, tv, p, grid, stream)
