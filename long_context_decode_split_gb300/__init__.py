@@ -214,10 +214,15 @@ _WS_SIZES = {}
 
 def _remembered_size(name, *args):
     # the plan depends on the shape and the current device only: remembered per both
-    key = (name, torch.cuda.current_device() if torch.cuda.is_available() else -1, *args)
+    try:
+        key = (name, torch._C._cuda_getDevice(), args)
+    except (AttributeError, RuntimeError):  # no CUDA device
+        key = (name, -1, args)
     n = _WS_SIZES.get(key)
     if n is None:
         n = int(getattr(load(), name)(*args))
+        if len(_WS_SIZES) > 4096:  # prompt batches differ at every call
+            _WS_SIZES.clear()
         _WS_SIZES[key] = n
     return n
 
@@ -244,11 +249,12 @@ def _outputs(B, Hq, d, device, out, lse, out_dtype, want_lse):
     code, tdt = _out_code(out_dtype)
     if out is None:
         out = torch.empty((B, Hq, d), dtype=tdt, device=device)
-    _check_cuda(out, "out", tdt, (B, Hq, d))
-    if lse is None and want_lse:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=device)
+    else:
+        _check_cuda(out, "out", tdt, (B, Hq, d))
     if lse is not None:
         _check_cuda(lse, "lse", torch.float32, (B, Hq))
+    elif want_lse:
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=device)
     return code, out, lse
 
 
@@ -626,31 +632,49 @@ def fd_decode_paged_fp4(q, k_pages, k_page_scales, v_pages, v_page_scales, page_
 def _check_tokens(t, name, H=None, d=None):
     """[T, H, d] bf16 whose tokens may lie further apart than H * d elements (a
     slice of a fused projection); returns the token stride in elements."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    dev = torch._C._cuda_getDevice()
-    if t.get_device() != dev:
-        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev} (the first tensor's device)")
-    if t.dtype != torch.bfloat16:
-        raise ValueError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.dim() != 3 or (H is not None and t.shape[1] != H) or (d is not None and t.shape[2] != d):
+    shape = t.shape
+    if len(shape) != 3 or (H is not None and shape[1] != H) or (d is not None and shape[2] != d):
         raise ValueError(f"{name} must be [tokens, {'heads' if H is None else H}, {'d' if d is None else d}], "
-                         f"got {tuple(t.shape)}")
-    T, H, d = t.shape
-    row = H * d
+                         f"got {tuple(shape)}")
+    row = shape[1] * shape[2]
     if t.is_contiguous():
-        return row
-    if t.numel() and ((d > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != d)):
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    stride = t.stride(0) if T > 1 else row
-    if stride < row:
-        raise ValueError(f"{name}: tokens must not overlap")
+        stride = row
+    else:
+        T, H, d = shape
+        s = t.stride()
+        if t.numel() and ((d > 1 and s[2] != 1) or (H > 1 and s[1] != d)):
+            raise ValueError(f"{name}: the heads of a token must be contiguous")
+        stride = s[0] if T > 1 else row
+        if stride < row:
+            raise ValueError(f"{name}: tokens must not overlap")
+    if t.dtype is not torch.bfloat16 or t.get_device() != torch._C._cuda_getDevice():
+        # raises with the reason (get_device() is -1 for a CPU tensor)
+        _check_cuda(t.contiguous(), name, torch.bfloat16)
     return stride
 
 
-def _check_offsets(t, name, B=None):
-    _check_cuda(t, name, torch.int32, None if B is None else (B + 1,))
-    _need(t.dim() == 1 and t.numel() >= 1, f"{name} must be [B + 1]")
+_I32 = torch.int32
+
+
+def _check_ints(t, name, shape=None):
+    """A contiguous int32 tensor on the current device, of the given shape."""
+    if (t.dtype is not _I32 or t.get_device() != torch._C._cuda_getDevice() or not t.is_contiguous()
+            or (shape is not None and t.shape != shape)):
+        _check_cuda(t, name, _I32, shape)  # raises with the reason
+
+
+def _check_offsets(t, name):
+    _check_ints(t, name)
+    if t.dim() != 1 or t.numel() < 1:
+        raise ValueError(f"{name} must be [B + 1]")
+    return t.numel() - 1
+
+
+def _check_table(t, B):
+    _check_ints(t, "page_table")
+    if t.dim() != 2 or t.shape[0] != B:
+        raise ValueError("page_table must be [B, max_pages]")
+    return t.shape[1]
 
 
 def fd_prefill_num_splits(B, total_q, Hq, Hkv, max_k, d, num_splits=0) -> int:
@@ -661,8 +685,6 @@ def fd_prefill_num_splits(B, total_q, Hq, Hkv, max_k, d, num_splits=0) -> int:
 
 
 def fd_prefill_workspace_size(B, total_q, Hq, Hkv, max_k, d, num_splits=0) -> int:
-    if len(_WS_SIZES) > 4096:  # prompt batches differ at every call
-        _WS_SIZES.clear()
     return _remembered_size("fd_prefill_workspace_size", B, total_q, Hq, Hkv, max_k, d, num_splits)
 
 
@@ -673,33 +695,35 @@ def fd_prefill_packed(q, k, v, cu_seqlens_q, cu_seqlens_k=None, scale=None, caus
     k, v [Tk,Hkv,d] bf16 (tokens may be strided), cu_seqlens_q [B+1] int32,
     cu_seqlens_k [B+1] or None (= cu_seqlens_q).  Returns (out [Tq,Hq,d],
     lse [Tq,Hq] or None); rows of no sequence are not written."""
-    lib = load()
     qs = _check_tokens(q, "q")
     Tq, Hq, d = q.shape
     ks = _check_tokens(k, "k", None, d)
     Tk, Hkv, _ = k.shape
     vs = _check_tokens(v, "v", Hkv, d)
     _need(v.shape[0] == Tk, "k and v must have the same number of tokens")
-    _check_offsets(cu_seqlens_q, "cu_seqlens_q")
-    B = cu_seqlens_q.numel() - 1
+    B = _check_offsets(cu_seqlens_q, "cu_seqlens_q")
     if cu_seqlens_k is None:
         cu_seqlens_k = cu_seqlens_q
-    _check_offsets(cu_seqlens_k, "cu_seqlens_k", B)
+    else:
+        _check_ints(cu_seqlens_k, "cu_seqlens_k", (B + 1,))
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     code, out, lse = _outputs(Tq, Hq, d, q.device, out, lse, out_dtype, want_lse)
     ws = _workspace(fd_prefill_workspace_size(B, Tq, Hq, Hkv, Tk, d, num_splits), q.device, workspace)
-    st = lib.fd_prefill_packed(_p(q), _p(k), _p(v), qs, ks, vs, _p(cu_seqlens_q), _p(cu_seqlens_k), B, Tq, Tk, Hq, Hkv,
-                               d, scale, int(bool(causal)), int(num_splits), _p(out), code, _p(lse), _p(ws),
-                               _nbytes(ws), _stream(stream))
+    st = load().fd_prefill_packed(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), B, Tq,
+        Tk, Hq, Hkv, d, scale, 1 if causal else 0, num_splits, out.data_ptr(), code, _p(lse), _p(ws), _nbytes(ws),
+        _stream(stream))
     _raise(st, "fd_prefill_packed")
     return out, lse
 
 
-def _check_pool(k_pages, v_pages, d):
+def _check_pool(k_pages, v_pages, d, num_pages=0):
     _check_cuda(k_pages, "k_pages", torch.bfloat16)
     _need(k_pages.dim() == 4 and k_pages.shape[3] == d, "k_pages must be [P, Hkv, page, d]")
     _check_cuda(v_pages, "v_pages", torch.bfloat16, k_pages.shape)
-    return k_pages.shape[1], k_pages.shape[2]
+    P, Hkv, page_size, _ = k_pages.shape
+    _need(0 <= num_pages <= P, "num_pages must be within the pool")
+    return P, Hkv, page_size
 
 
 @_on_device_of_first_tensor
@@ -709,25 +733,21 @@ def fd_prefill_paged(q, k_pages, v_pages, page_table, num_pages, cu_seqlens_q, s
     values.  q [Tq,Hq,d] bf16 (tokens may be strided), k_pages/v_pages
     [P,Hkv,64,d] bf16, page_table [B,max_pages] int32, cu_seqlens_q [B+1]
     int32, seq_lens [B] int32 (all keys; the queries are the last ones)."""
-    lib = load()
     qs = _check_tokens(q, "q")
     Tq, Hq, d = q.shape
-    Hkv, page_size = _check_pool(k_pages, v_pages, d)
-    _check_offsets(cu_seqlens_q, "cu_seqlens_q")
-    B = cu_seqlens_q.numel() - 1
-    _check_cuda(page_table, "page_table", torch.int32)
-    _need(page_table.dim() == 2 and page_table.shape[0] == B, "page_table must be [B, max_pages]")
-    max_pages = page_table.shape[1]
-    _check_cuda(seq_lens, "seq_lens", torch.int32, (B,))
-    _need(0 <= int(num_pages) <= k_pages.shape[0], "num_pages must be within the pool")
+    num_pages = int(num_pages)
+    _, Hkv, page_size = _check_pool(k_pages, v_pages, d, num_pages)
+    B = _check_offsets(cu_seqlens_q, "cu_seqlens_q")
+    max_pages = _check_table(page_table, B)
+    _check_ints(seq_lens, "seq_lens", (B,))
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     code, out, lse = _outputs(Tq, Hq, d, q.device, out, lse, out_dtype, want_lse)
     ws = _workspace(fd_prefill_workspace_size(B, Tq, Hq, Hkv, max_pages * page_size, d, num_splits), q.device,
                     workspace)
-    st = lib.fd_prefill_paged(_p(q), _p(k_pages), _p(v_pages), qs, _p(page_table), max_pages, int(num_pages),
-                              _p(cu_seqlens_q), _p(seq_lens), page_size, B, Tq, Hq, Hkv, d, scale, int(bool(causal)),
-                              int(num_splits), _p(out), code, _p(lse), _p(ws),
-                              _nbytes(ws), _stream(stream))
+    st = load().fd_prefill_paged(
+        q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), qs, page_table.data_ptr(), max_pages, num_pages,
+        cu_seqlens_q.data_ptr(), seq_lens.data_ptr(), page_size, B, Tq, Hq, Hkv, d, scale, 1 if causal else 0,
+        num_splits, out.data_ptr(), code, _p(lse), _p(ws), _nbytes(ws), _stream(stream))
     _raise(st, "fd_prefill_paged")
     return out, lse
 
@@ -744,27 +764,24 @@ def fd_decode_paged_shared_prefix(q, k_pages, v_pages, prefix_table, page_table,
     64 * len(prefix_table) tokens, read once for the whole batch.
     prefix_table [n] int32 page ids (the first n entries of every page_table
     row are not read); seq_lens [B] int32 counts all tokens."""
-    lib = load()
     _check_cuda(q, "q", torch.bfloat16)
     _need(q.dim() == 3, "q must be [B, Hq, d]")
     B, Hq, d = q.shape
-    Hkv, page_size = _check_pool(k_pages, v_pages, d)
-    _check_cuda(prefix_table, "prefix_table", torch.int32)
+    num_pages = int(num_pages)
+    _, Hkv, page_size = _check_pool(k_pages, v_pages, d, num_pages)
+    _check_ints(prefix_table, "prefix_table")
     _need(prefix_table.dim() == 1, "prefix_table must be [prefix_pages]")
-    _check_cuda(page_table, "page_table", torch.int32)
-    _need(page_table.dim() == 2 and page_table.shape[0] == B, "page_table must be [B, max_pages]")
-    max_pages, n = page_table.shape[1], prefix_table.numel()
+    max_pages, n = _check_table(page_table, B), prefix_table.numel()
     _need(n <= max_pages, "prefix_table must be no longer than a row of page_table")
-    _check_cuda(seq_lens, "seq_lens", torch.int32, (B,))
-    _need(0 <= int(num_pages) <= k_pages.shape[0], "num_pages must be within the pool")
+    _check_ints(seq_lens, "seq_lens", (B,))
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     code, out, lse = _outputs(B, Hq, d, q.device, out, lse, out_dtype, want_lse)
     ws = _workspace(fd_shared_prefix_workspace_size(B, Hq, Hkv, n * page_size, (max_pages - n) * page_size, d,
                                                     num_splits), q.device, workspace)
-    st = lib.fd_decode_paged_shared_prefix(_p(q), _p(k_pages), _p(v_pages), _p(prefix_table), n, _p(page_table),
-                                           max_pages, int(num_pages), _p(seq_lens), page_size, B, Hq, Hkv, d, scale,
-                                           int(num_splits), _p(out), code, _p(lse), _p(ws),
-                                           _nbytes(ws), _stream(stream))
+    st = load().fd_decode_paged_shared_prefix(
+        q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), prefix_table.data_ptr(), n, page_table.data_ptr(),
+        max_pages, num_pages, seq_lens.data_ptr(), page_size, B, Hq, Hkv, d, scale, num_splits, out.data_ptr(), code,
+        _p(lse), _p(ws), _nbytes(ws), _stream(stream))
     _raise(st, "fd_decode_paged_shared_prefix")
     return out, lse
 
@@ -776,7 +793,6 @@ def fd_decode_dense_shared_prefix(q, k_prefix, v_prefix, k, v, seq_lens=None, sc
     k_prefix, v_prefix [Hkv,P,d] bf16 (read once for the whole batch), then
     every sequence's own k, v [B,Hkv,L_max,d] with seq_lens [B] int32 own
     tokens (or None)."""
-    lib = load()
     _check_cuda(q, "q", torch.bfloat16)
     _need(q.dim() == 3, "q must be [B, Hq, d]")
     B, Hq, d = q.shape
@@ -789,22 +805,15 @@ def fd_decode_dense_shared_prefix(q, k_prefix, v_prefix, k, v, seq_lens=None, sc
     L_max = k.shape[2]
     _check_cuda(v, "v", torch.bfloat16, k.shape)
     if seq_lens is not None:
-        _check_cuda(seq_lens, "seq_lens", torch.int32, (B,))
+        _check_ints(seq_lens, "seq_lens", (B,))
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     code, out, lse = _outputs(B, Hq, d, q.device, out, lse, out_dtype, want_lse)
     ws = _workspace(fd_shared_prefix_workspace_size(B, Hq, Hkv, P, L_max, d, num_splits), q.device, workspace)
-    st = lib.fd_decode_dense_shared_prefix(_p(q), _p(k_prefix), _p(v_prefix), P, _p(k), _p(v), _p(seq_lens), B, Hq, Hkv,
-                                           L_max, d, scale, int(num_splits), _p(out), code, _p(lse), _p(ws),
-                                           _nbytes(ws), _stream(stream))
+    st = load().fd_decode_dense_shared_prefix(
+        q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), P, k.data_ptr(), v.data_ptr(), _p(seq_lens), B, Hq, Hkv,
+        L_max, d, scale, num_splits, out.data_ptr(), code, _p(lse), _p(ws), _nbytes(ws), _stream(stream))
     _raise(st, "fd_decode_dense_shared_prefix")
     return out, lse
-
-
-def _int32_out(t, name, shape, device):
-    if t is None:
-        return torch.empty(shape, dtype=torch.int32, device=device)
-    _check_cuda(t, name, torch.int32, shape)
-    return t
 
 
 @_on_device_of_first_tensor
@@ -816,30 +825,46 @@ def fd_assign_pages(page_table, cached_lens, new_lens, free_pages, total_new, fr
     None = 0), total_new the number of slots.  Returns (seq_lens [B],
     cu_seqlens [B+1], slots [total_new] int64, free_head_out [1]); seq_lens may
     be cached_lens and free_head_out may be free_head (updated in place)."""
-    lib = load()
-    _check_cuda(page_table, "page_table", torch.int32)
-    _need(page_table.dim() == 2, "page_table must be [B, max_pages]")
+    _check_ints(page_table, "page_table")
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
     B, max_pages = page_table.shape
-    _check_cuda(cached_lens, "cached_lens", torch.int32, (B,))
-    _check_cuda(new_lens, "new_lens", torch.int32, (B,))
-    _check_cuda(free_pages, "free_pages", torch.int32)
-    _need(free_pages.dim() == 1, "free_pages must be [F]")
+    _check_ints(cached_lens, "cached_lens", (B,))
+    _check_ints(new_lens, "new_lens", (B,))
+    _check_ints(free_pages, "free_pages")
+    if free_pages.dim() != 1:
+        raise ValueError("free_pages must be [F]")
     if free_head is not None:
-        _check_cuda(free_head, "free_head", torch.int32, (1,))
+        _check_ints(free_head, "free_head", (1,))
     total_new = int(total_new)
     _need(total_new >= 0, "total_new must be >= 0")
-    dev = page_table.device
-    seq_lens = _int32_out(seq_lens, "seq_lens", (B,), dev)
-    cu_seqlens = _int32_out(cu_seqlens, "cu_seqlens", (B + 1,), dev)
-    free_head_out = _int32_out(free_head_out, "free_head_out", (1,), dev)
+    if seq_lens is None and cu_seqlens is None and free_head_out is None:
+        # one allocation for the three small outputs
+        small = torch.empty(2 * B + 2, dtype=_I32, device=page_table.device)
+        seq_lens = small.as_strided((B,), (1,), 0)
+        cu_seqlens = small.as_strided((B + 1,), (1,), B)
+        free_head_out = small.as_strided((1,), (1,), 2 * B + 1)
+    else:
+        seq_lens = _int32_out(seq_lens, "seq_lens", (B,), page_table.device)
+        cu_seqlens = _int32_out(cu_seqlens, "cu_seqlens", (B + 1,), page_table.device)
+        free_head_out = _int32_out(free_head_out, "free_head_out", (1,), page_table.device)
     if slots is None:
-        slots = torch.empty(total_new, dtype=torch.int64, device=dev)
-    _check_cuda(slots, "slots", torch.int64, (total_new,))
-    st = lib.fd_assign_pages(_p(cached_lens), _p(new_lens), B, _p(page_table), max_pages, int(page_size),
-                             _p(free_pages), free_pages.numel(), _p(free_head), total_new, _p(seq_lens),
-                             _p(cu_seqlens), _p(slots), _p(free_head_out), _stream(stream))
+        slots = torch.empty(total_new, dtype=torch.int64, device=page_table.device)
+    else:
+        _check_cuda(slots, "slots", torch.int64, (total_new,))
+    st = load().fd_assign_pages(
+        cached_lens.data_ptr(), new_lens.data_ptr(), B, page_table.data_ptr(), max_pages, int(page_size),
+        free_pages.data_ptr(), free_pages.numel(), _p(free_head), total_new, seq_lens.data_ptr(),
+        cu_seqlens.data_ptr(), slots.data_ptr(), free_head_out.data_ptr(), _stream(stream))
     _raise(st, "fd_assign_pages")
     return seq_lens, cu_seqlens, slots, free_head_out
+
+
+def _int32_out(t, name, shape, device):
+    if t is None:
+        return torch.empty(shape, dtype=_I32, device=device)
+    _check_ints(t, name, shape)
+    return t
 
 
 @_on_device_of_first_tensor
@@ -847,16 +872,15 @@ def fd_append_kv_paged(k, v, slots, k_pages, v_pages, stream=None):
     """Store new rows k, v [T,Hkv,d] bf16 (tokens may be strided) at slots [T]
     int64 of the pools k_pages, v_pages [P,Hkv,64,d] bf16 (negative slots are
     skipped).  Returns (k_pages, v_pages)."""
-    lib = load()
     ks = _check_tokens(k, "k")
     T, Hkv, d = k.shape
     vs = _check_tokens(v, "v", Hkv, d)
     _need(v.shape[0] == T, "k and v must have the same number of tokens")
     _check_cuda(slots, "slots", torch.int64, (T,))
-    heads, page_size = _check_pool(k_pages, v_pages, d)
+    P, heads, page_size = _check_pool(k_pages, v_pages, d)
     _need(heads == Hkv, "k_pages must have the heads of k")
-    st = lib.fd_append_kv_paged(_p(k), _p(v), ks, vs, _p(slots), T, Hkv, d, _p(k_pages), _p(v_pages),
-                                k_pages.shape[0], page_size, _stream(stream))
+    st = load().fd_append_kv_paged(k.data_ptr(), v.data_ptr(), ks, vs, slots.data_ptr(), T, Hkv, d, k_pages.data_ptr(),
+                                   v_pages.data_ptr(), P, page_size, _stream(stream))
     _raise(st, "fd_append_kv_paged")
     return k_pages, v_pages
 
@@ -866,7 +890,6 @@ def fd_append_kv_paged_fp8(k, v, slots, k_pages, k_page_scales, v_pages, v_page_
     """fd_append_kv_paged into the paged fp8 cache: k_pages, v_pages [P,Hkv,64,d]
     uint8 codes, k_page_scales, v_page_scales [P,Hkv,64] float32; rows are
     encoded as by fd_quantize_kv_fp8."""
-    lib = load()
     ks = _check_tokens(k, "k")
     T, Hkv, d = k.shape
     vs = _check_tokens(v, "v", Hkv, d)
@@ -878,8 +901,9 @@ def fd_append_kv_paged_fp8(k, v, slots, k_pages, k_page_scales, v_pages, v_page_
     _check_cuda(v_pages, "v_pages", torch.uint8, k_pages.shape)
     _check_cuda(k_page_scales, "k_page_scales", torch.float32, (P, Hkv, page_size))
     _check_cuda(v_page_scales, "v_page_scales", torch.float32, (P, Hkv, page_size))
-    st = lib.fd_append_kv_paged_fp8(_p(k), _p(v), ks, vs, _p(slots), T, Hkv, d, _p(k_pages), _p(k_page_scales),
-                                    _p(v_pages), _p(v_page_scales), P, page_size, _stream(stream))
+    st = load().fd_append_kv_paged_fp8(k.data_ptr(), v.data_ptr(), ks, vs, slots.data_ptr(), T, Hkv, d,
+                                       k_pages.data_ptr(), k_page_scales.data_ptr(), v_pages.data_ptr(),
+                                       v_page_scales.data_ptr(), P, page_size, _stream(stream))
     _raise(st, "fd_append_kv_paged_fp8")
     return k_pages, k_page_scales, v_pages, v_page_scales
 
