@@ -838,18 +838,12 @@ def fd_assign_pages(page_table, cached_lens, new_lens, free_pages, total_new, fr
         _check_ints(free_head, "free_head", (1,))
     total_new = int(total_new)
     _need(total_new >= 0, "total_new must be >= 0")
-    if seq_lens is None and cu_seqlens is None and free_head_out is None:
-        # one allocation for the three small outputs
-        small = torch.empty(2 * B + 2, dtype=_I32, device=page_table.device)
-        seq_lens = small.as_strided((B,), (1,), 0)
-        cu_seqlens = small.as_strided((B + 1,), (1,), B)
-        free_head_out = small.as_strided((1,), (1,), 2 * B + 1)
-    else:
-        seq_lens = _int32_out(seq_lens, "seq_lens", (B,), page_table.device)
-        cu_seqlens = _int32_out(cu_seqlens, "cu_seqlens", (B + 1,), page_table.device)
-        free_head_out = _int32_out(free_head_out, "free_head_out", (1,), page_table.device)
+    dev = page_table.device
+    seq_lens = _int32_out(seq_lens, "seq_lens", (B,), dev)
+    cu_seqlens = _int32_out(cu_seqlens, "cu_seqlens", (B + 1,), dev)
+    free_head_out = _int32_out(free_head_out, "free_head_out", (1,), dev)
     if slots is None:
-        slots = torch.empty(total_new, dtype=torch.int64, device=page_table.device)
+        slots = torch.empty(total_new, dtype=torch.int64, device=dev)
     else:
         _check_cuda(slots, "slots", torch.int64, (total_new,))
     st = load().fd_assign_pages(

@@ -447,7 +447,11 @@ struct SharedPlan {
 SharedPlan shared_plan(int B, int Hq, int Hkv, int prefix_len, int L_own, int d, int num_splits) {
     SharedPlan s;
     s.shared = shared_rows_plan(fd::rows_tiles(1, B, Hq / Hkv, false) * Hkv, prefix_len, num_splits);
-    s.own = decode_plan(B, Hq, Hkv, L_own, d, 0, true);
+    // own tokens: one chunk each while the sequences fill the SMs and are short
+    // (128 sequences of up to 1024 own tokens, 8 KV heads: 46.5 us, 60.5 us in the
+    // decode's 14-tile chunks)
+    const bool short_own = (long long)B * Hkv >= current_sm_count() && L_own <= 32 * kTile;
+    s.own = decode_plan(B, Hq, Hkv, L_own, d, short_own ? 1 : 0, true);
     s.list = s.shared.splits + (L_own > 0 ? s.own.splits : 0);
     return s;
 }

@@ -368,6 +368,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUt
             int id = blockIdx.x;
             for (int asked = 0; ok; ++asked) {
                 Work w;
+                int c0 = 0;  // first key of the chunk
                 w.valid = id >= 0;
                 bool some = !w.valid;
                 if (w.valid) {
@@ -376,7 +377,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUt
                     w.split = rest % p.splits;
                     w.it = find_item(p, p.tiles - 1 - rest / p.splits, TILES * p.tok);
                     some = w.it.t0 >= 0 && w.it.t0 < w.it.Lq;
-                    const int c0 = w.split * p.chunk;
+                    c0 = w.split * p.chunk;
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const int first = w.it.t0 + (DUAL ? i : 0) * p.tok;
@@ -412,26 +413,46 @@ rows_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUt
                                     tma_load_3d(sq + i * TILE + bx * BOX, &tmq, 64 * bx, w.h * p.G,
                                                 w.it.q0 + w.it.t0 + i * p.tok, q_full);
                         }
+                        // Page ids by the warp, 32 pages a register: the windows of 16 blocks alternate
+                        // between two of them, the next one fetched when the keys are 4 blocks into the
+                        // current one (the values are at most 2 blocks behind).
+                        int window[2] = {-1, -1};
+                        auto fetch = [&](int win) {
+                            const int pi = c0 / kTile + 32 * win + lane;
+                            const bool in = pi * kTile < w.it.Lk && pi < p.max_pages;
+                            return in ? p.page_table[(size_t)w.it.seq * p.table_stride + pi] : -1;
+                        };
+                        auto page = [&](int rel) {  // of page `rel` of the chunk
+                            return __shfl_sync(0xffffffffu, rel & 32 ? window[1] : window[0], rel & 31);
+                        };
                         // block j of the keys (which = 0) or values (1) into the next stage
                         auto load = [&](int j, int which) {
+                            int page0 = 0, page1 = 0;
+                            if (PAGED) {
+                                if (which == 0 && j == 0) window[0] = fetch(0);
+                                if (which == 0 && (j & 15) == 4) {
+                                    const int next = fetch((j >> 4) + 1);
+                                    if (j & 16) window[0] = next;
+                                    else window[1] = next;
+                                }
+                                page0 = page(2 * j);
+                                page1 = page(2 * j + 1);
+                            }
                             const int s = n % STAGES;
                             ok = ok && warp_wait(&empty[s], ((uint32_t)(n / STAGES) & 1u) ^ 1u);
                             if (!ok) return;
                             if (lane == 0) {
                                 const void* map = which ? static_cast<const void*>(&tmv) : static_cast<const void*>(&tmk);
                                 unsigned char* dst = ring + s * TILE;
-                                const int at = w.split * p.chunk + j * kBlock;
+                                const int at = c0 + j * kBlock;
                                 mbar_arrive_expect_tx(&full[s], TILE);
                                 if (PAGED) {
 #pragma unroll
                                     for (int half = 0; half < 2; ++half) {
-                                        const int pi = at / kTile + half;
+                                        const int pg = half ? page1 : page0;
                                         int y = p.zero_row;  // past the pool: zeros
-                                        if (pi * kTile < w.it.Lk && pi < p.max_pages) {
-                                            const int pg = p.page_table[(size_t)w.it.seq * p.table_stride + pi];
-                                            if (pg >= 0 && pg < p.num_pages) y = (pg * p.Hkv + w.h) * kTile;
-                                            else atomicOr(&g_status_rows, kStatusBadPage);
-                                        }
+                                        if (pg >= 0 && pg < p.num_pages) y = (pg * p.Hkv + w.h) * kTile;
+                                        else if (at + half * kTile < w.it.Lk) atomicOr(&g_status_rows, kStatusBadPage);
 #pragma unroll
                                         for (int bx = 0; bx < BOXES; ++bx)
                                             tma_load_2d(dst + bx * BOX + half * (BOX / 2), map, 64 * bx, y, &full[s]);
