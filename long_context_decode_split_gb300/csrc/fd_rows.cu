@@ -109,8 +109,8 @@ __device__ __forceinline__ int visible_keys(const RowsParams& p, const RowsItem&
 
 constexpr int kRows = 128;    // rows of a tile: the lanes of an accumulator in tensor memory
 constexpr int kBlock = 128;   // keys per step
-constexpr int kThreads = 384; // two softmax warpgroups, then the copy warp, the MMA warp and two idle ones
-constexpr int kCopyWarp = 8, kMmaWarp = 9;
+constexpr int kThreads = 384; // two softmax warpgroups, then the copy warp, two MMA warps and an idle one
+constexpr int kCopyWarp = 8, kMmaWarp = 9;  // (kMmaWarp + i issues pipeline i's products)
 // Registers per thread after the split: 168 x 384 at launch = 216 x 256 + 72 x 128.
 constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
 
@@ -126,7 +126,11 @@ struct RowsGeo {
     static constexpr int TILE = BOXES * BOX;        // 128 rows of D channels
     static constexpr int TILES = DUAL ? 2 : 1;      // of query rows
     static constexpr int STAGES = D == 128 ? (DUAL ? 5 : 6) : 8;
-    static constexpr int SMEM = 1024 + (TILES + STAGES) * TILE + (2 * STAGES + 14) * 8 + 16 + 2 * 64 + 16 + 2 * 128 * 4;
+    // Two tiles share one ring; the pipelines of a single tile have one each.
+    // (Every consumer of a ring waits for every tile of it: a barrier's parity
+    // tells only two phases apart.)
+    static constexpr int RING = DUAL ? STAGES : STAGES / 2;
+    static constexpr int SMEM = 1024 + (TILES + STAGES) * TILE + (2 * STAGES + 16) * 8 + 16 + 2 * 64 + 16 + 2 * 128 * 4;
     static_assert(SMEM <= 232448, "shared memory of a CTA");
 };
 
@@ -301,7 +305,7 @@ struct Work {
 // shuffles.  P (bf16) overwrites the first half of S; the products of a
 // pipeline run in the order they are issued, so S of block j + 1 is computed
 // after P of block j was read.  Tensor memory columns: S0 S1 | O0 O1.
-// Keys and values pass through one ring of 128-row tiles (K0 V0 K1 V1 ..).
+// Keys and values pass through rings of 128-row tiles (K V K V ..).
 //
 // A CTA goes from one piece of work to the next without a stop: the copy warp
 // is ahead with the next queries and keys, and the first products of the next
@@ -311,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 rows_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
             const __grid_constant__ CUtensorMap tmv, const RowsParams p) {
     using Geo = RowsGeo<D, DUAL>;
-    constexpr int TILES = Geo::TILES, STAGES = Geo::STAGES, BOXES = Geo::BOXES, BOX = Geo::BOX, TILE = Geo::TILE;
+    constexpr int TILES = Geo::TILES, STAGES = Geo::STAGES, RING = Geo::RING, BOXES = Geo::BOXES, BOX = Geo::BOX, TILE = Geo::TILE;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     unsigned char* sq = smem;
@@ -327,7 +331,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUt
     uint64_t* work_empty = work_full + 2;
     uint64_t* next_full = work_empty + 2;
     uint64_t* drained = next_full + 1;
-    unsigned char* answer = reinterpret_cast<unsigned char*>(drained + 1);  // 16 bytes
+    unsigned char* answer = reinterpret_cast<unsigned char*>(drained + 3);  // 16 bytes
     Work* work = reinterpret_cast<Work*>(answer + 16);                      // [2]
     uint32_t* tmem_at = reinterpret_cast<uint32_t*>(work + 2);
     float* join = reinterpret_cast<float*>(tmem_at + 4);  // [2][128] what the pipelines tell each other (single)
@@ -336,19 +340,19 @@ rows_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUt
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
+            mbar_init(&empty[s], DUAL ? 2 : 1);
         }
         mbar_init(q_full, 1);
-        mbar_init(q_empty, 1);
+        mbar_init(q_empty, 2);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 4);
             mbar_init(&o_full[i], 1);
             mbar_init(&work_full[i], 1);
-            mbar_init(&work_empty[i], 9);
+            mbar_init(&work_empty[i], 10);
+            mbar_init(&drained[i], 1);
         }
         mbar_init(next_full, 1);
-        mbar_init(drained, 1);
         fence_barrier_init();
     }
     if (warp == kMmaWarp) tmem_alloc(tmem_at, 512);
@@ -364,7 +368,8 @@ rows_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUt
         if (warp == kCopyWarp) {
             // ---------------- work and copies ----------------
             bool ok = true;
-            int n = 0, qn = 0, wn = 0;  // tiles through the ring, query loads, pieces of work
+            int n0 = 0, n1 = 0;   // tiles through the ring of pipeline 0 (or both) and 1
+            int qn = 0, wn = 0;   // query loads, pieces of work
             int id = blockIdx.x;
             for (int asked = 0; ok; ++asked) {
                 Work w;
@@ -438,8 +443,9 @@ rows_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUt
                                 page0 = page(2 * j);
                                 page1 = page(2 * j + 1);
                             }
-                            const int s = n % STAGES;
-                            ok = ok && warp_wait(&empty[s], ((uint32_t)(n / STAGES) & 1u) ^ 1u);
+                            int& n = !DUAL && (j & 1) ? n1 : n0;
+                            const int s = (!DUAL && (j & 1) ? RING : 0) + n % RING;
+                            ok = ok && warp_wait(&empty[s], ((uint32_t)(n / RING) & 1u) ^ 1u);
                             if (!ok) return;
                             if (lane == 0) {
                                 const void* map = which ? static_cast<const void*>(&tmv) : static_cast<const void*>(&tmk);
@@ -487,50 +493,51 @@ rows_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUt
                 // the others stopped early: let the copies in flight land before the CTA ends
                 if (lane == 0) atomicOr(&g_status_rows, kStatusTimeout);
                 if (qn > 0) mbar_wait(q_full, (uint32_t)(qn - 1) & 1u);
-                for (int u = max(0, n - STAGES); u < n; ++u) mbar_wait(&full[u % STAGES], (uint32_t)(u / STAGES) & 1u);
+                for (int u = max(0, n0 - RING); u < n0; ++u) mbar_wait(&full[u % RING], (uint32_t)(u / RING) & 1u);
+                for (int u = max(0, n1 - RING); u < n1; ++u)
+                    mbar_wait(&full[RING + u % RING], (uint32_t)(u / RING) & 1u);
                 mbar_wait(next_full, 0);
                 mbar_wait(next_full, 1);
             }
-        } else if (warp == kMmaWarp) {
+        } else if (warp < kMmaWarp + 2) {
             // ---------------- products ----------------
+            // One warp per pipeline: an MMA is taken about when it starts to run, so what a warp does
+            // between its products (waits, commits) leaves the tensor cores to the other one.
             constexpr uint32_t IQK = mma_desc(kBlock, false), IPV = mma_desc(D, true);
-            const uint32_t q_at = smem_u32(sq), ring_at = smem_u32(ring);
-            const uint32_t tm = uniform(tmem);
+            const uint32_t ring_at = smem_u32(ring), tm = uniform(tmem);
+            const uint32_t i = uniform(warp - kMmaWarp);
+            const uint32_t q_desc = desc_rows(smem_u32(sq) + (DUAL ? i : 0) * TILE);
+            const uint32_t s_tm = tm + i * 128, o_tm = tm + 256 + i * D;
             bool ok = true;
-            int n = 0, qn = 0;           // ring position, pieces of work with keys
-            uint32_t rounds0 = 0, rounds1 = 0;  // blocks of each pipeline so far
-            auto arrive = [&](int& stage) {  // the next tile of the ring
-                stage = n % STAGES;
-                ok = ok && warp_wait(&full[stage], (uint32_t)(n / STAGES) & 1u);
-                ++n;
-            };
-            auto qk = [&](int i, int stage) {  // S_i = Q_i K^T
-                const uint32_t qa = desc_rows(q_at + (DUAL ? i : 0) * TILE), ka = desc_rows(ring_at + stage * TILE);
-                if (elect_one()) {
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t off = ((kk / 4) * BOX + (kk % 4) * 32) >> 4;
-                        mma_ss(tm + i * 128, qa + off, ka + off, IQK, kk > 0);
-                    }
-                    mma_commit(&s_full[i]);
-                }
-            };
-            auto pv = [&](int i, int stage, bool first) {  // O_i += P_i V
-                const uint32_t va = desc_cols(ring_at + stage * TILE);
-                if (elect_one()) {
-#pragma unroll
-                    for (int kk = 0; kk < kBlock / 16; ++kk)
-                        mma_ts(tm + 256 + i * D, tm + i * 128 + kk * 8, va + (kk * 16 * 128 >> 4), IPV, !first || kk > 0);
-                }
+            uint32_t n0 = 0, qn = 0, rounds = 0;  // ring position, pieces of work with keys, blocks so far
+            auto arrive = [&](uint32_t n) {  // tile n of the pipeline's ring is there: its stage
+                const uint32_t s = (DUAL ? 0 : i * RING) + n % RING;
+                ok = ok && warp_wait(&full[s], (n / RING) & 1u);
+                return s;
             };
             auto commit = [&](uint64_t* bar) {
                 if (elect_one()) mma_commit(bar);
             };
-            auto weights = [&](int i) {
-                uint32_t& rounds = i ? rounds1 : rounds0;
-                ok = ok && warp_wait(&p_full[i], rounds & 1u);
-                ++rounds;
-                tc_fence_after();
+            auto qk = [&](uint32_t stage) {  // S = Q K^T
+                const uint32_t ka = desc_rows(ring_at + stage * TILE);
+                if (elect_one()) {
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = ((kk / 4) * BOX + (kk % 4) * 32) >> 4;
+                        mma_ss(s_tm, q_desc + off, ka + off, IQK, kk > 0);
+                    }
+                    mma_commit(&s_full[i]);
+                    mma_commit(&empty[stage]);
+                }
+            };
+            auto pv = [&](uint32_t stage, bool first) {  // O += P V
+                const uint32_t va = desc_cols(ring_at + stage * TILE);
+                if (elect_one()) {
+#pragma unroll
+                    for (int kk = 0; kk < kBlock / 16; ++kk)
+                        mma_ts(o_tm, s_tm + kk * 8, va + (kk * 16 * 128 >> 4), IPV, !first || kk > 0);
+                    mma_commit(&empty[stage]);
+                }
             };
             for (int wn = 0; ok; ++wn) {
                 const int slot = wn & 1;
@@ -545,84 +552,58 @@ rows_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUt
                 if (!valid) break;
                 const int blocks = max(nb0, nb1);
                 if (blocks == 0) continue;
+                // the pipeline's rounds: blocks 0, 1, .. or every second one from i on
+                const int nb = DUAL ? (i ? nb1 : nb0) : (blocks + 1 - (int)i) / 2;
+                const int in_ring = DUAL ? blocks : nb;
                 // Value rows past the sequence may hold anything; their weight is 0, but 0 * NaN is NaN.
-                auto clear_tail = [&](int j, int stage) {
+                // (Both warps of a shared tile clear them, each before its own products.)
+                auto clear_tail = [&](int j, uint32_t stage) {
                     const int rows = left0 - j * kBlock;
                     if (rows >= kBlock) return;
                     unsigned char* v = ring + stage * TILE;
-                    for (int i = lane; i < (kBlock - rows) * 8; i += 32)
+                    for (int x = lane; x < (kBlock - rows) * 8; x += 32)
 #pragma unroll
                         for (int bx = 0; bx < BOXES; ++bx)
-                            *reinterpret_cast<uint4*>(v + bx * BOX + rows * 128 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+                            *reinterpret_cast<uint4*>(v + bx * BOX + rows * 128 + x * 16) = make_uint4(0u, 0u, 0u, 0u);
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
                 };
-                ok = warp_wait(q_full, (uint32_t)qn & 1u);
+                ok = warp_wait(q_full, qn & 1u);
                 ++qn;
-                int sk = 0, sv = 0;
-                if (DUAL) {
-                    arrive(sk);
+                if (ok && nb > 0) {
+                    const uint32_t s0 = arrive(n0);
                     if (!ok) break;
-                    if (nb0 > 0) qk(0, sk);
-                    if (nb1 > 0) qk(1, sk);
-                    commit(&empty[sk]);
-                    if (blocks == 1) commit(q_empty);
-                    for (int j = 0; j < blocks; ++j) {
-                        arrive(sv);
+                    qk(s0);
+                    if (nb == 1) commit(q_empty);
+                    for (int r = 0; r < nb; ++r) {
+                        const bool more = r + 1 < nb;
+                        const uint32_t sv = arrive(n0 + 2 * r + 1);
                         if (!ok) break;
-                        clear_tail(j, sv);
-                        const bool more = j + 1 < blocks;
-                        if (more) arrive(sk);
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const int nb = i ? nb1 : nb0;
-                            if (j < nb) {
-                                weights(i);
-                                if (!ok) break;
-                                pv(i, sv, j == 0);
-                                if (j + 1 < nb) qk(i, sk);
-                                else commit(&o_full[i]);
-                            }
-                        }
+                        clear_tail(DUAL ? r : 2 * r + (int)i, sv);
+                        const uint32_t sk = more ? arrive(n0 + 2 * r + 2) : 0;
+                        ok = ok && warp_wait(&p_full[i], rounds & 1u);
                         if (!ok) break;
-                        commit(&empty[sv]);
-                        if (more) commit(&empty[sk]);
-                        if (j + 2 == blocks) commit(q_empty);
+                        ++rounds;
+                        tc_fence_after();
+                        pv(sv, r == 0);
+                        if (more) qk(sk);
+                        else commit(&o_full[i]);
+                        if (r + 2 == nb) commit(q_empty);
                     }
-                } else {
-                    for (int j = 0; ok && j < 2 && j < blocks; ++j) {
-                        arrive(sk);
-                        if (!ok) break;
-                        if (j) qk(1, sk);
-                        else qk(0, sk);
-                        commit(&empty[sk]);
-                    }
-                    if (ok && blocks <= 2) commit(q_empty);
-                    for (int j = 0; ok && j < blocks; j += 2) {
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            if (j + i >= blocks) break;
-                            arrive(sv);
-                            if (!ok) break;
-                            clear_tail(j + i, sv);
-                            const bool more = j + i + 2 < blocks;
-                            if (more) arrive(sk);
-                            weights(i);
-                            if (!ok) break;
-                            pv(i, sv, j == 0);
-                            if (more) qk(i, sk);
-                            else commit(&o_full[i]);
-                            commit(&empty[sv]);
-                            if (more) commit(&empty[sk]);
-                            if (j + i + 3 == blocks) commit(q_empty);
-                        }
-                    }
+                } else if (ok && lane == 0) {
+                    mbar_arrive(q_empty);
                 }
+                // tiles that only the other pipeline needs
+                for (int x = 2 * nb; ok && x < 2 * in_ring; ++x) {
+                    const uint32_t s = arrive(n0 + x);
+                    if (ok && lane == 0) mbar_arrive(&empty[s]);
+                }
+                n0 += 2 * in_ring;
             }
             if (!ok) {
                 if (lane == 0) atomicOr(&g_status_rows, kStatusTimeout);
-                commit(drained);
-                warp_wait(drained, 0);
+                commit(&drained[i]);
+                warp_wait(&drained[i], 0);
             }
         }
     } else {
