@@ -390,7 +390,7 @@ RowsPlan prefill_plan(int B, int total_q, int Hq, int Hkv, int max_k, int num_sp
     const long long mean = B > 0 ? (total_q + B - 1) / B : 0;  // tokens of a sequence
     const long long ctas = (long long)B * ((mean + per - 1) / per) * Hkv;
     long long want = 1;
-    if (sms > 0 && ctas > 0 && ctas < 2LL * sms) want = (4LL * sms + ctas - 1) / ctas;
+    if (sms > 0 && ctas > 0 && ctas < 2LL * sms) want = 4LL * sms / ctas;
     if (want > max_k / 512) want = max_k / 512;
     return rows_chunks(max_k, want < 1 ? 1 : want, false);
 }

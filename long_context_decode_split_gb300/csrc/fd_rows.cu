@@ -41,6 +41,7 @@ struct RowsParams {
     float* part_o;
     float* part_ml;
     int rec0, rec_stride, direct;
+    int wide;      // results (or records) are 32-byte aligned
     int zero_row;  // a row past the page pool: a tile copied from there is zeros
 };
 
@@ -291,6 +292,19 @@ struct Work {
     int h, split;
     int nb[2];  // blocks of keys of each pipeline
 };
+
+// 32 bytes to global memory: whole sectors from one thread.  `wide`: the
+// address is 32-byte aligned (16 otherwise).
+__device__ __forceinline__ void store32(void* at, const uint32_t* x, bool wide) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(at), "r"(x[0]), "r"(x[1]), "r"(x[2]),
+                     "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4*>(at)[0] = make_uint4(x[0], x[1], x[2], x[3]);
+        reinterpret_cast<uint4*>(at)[1] = make_uint4(x[4], x[5], x[6], x[7]);
+    }
+}
 
 // ---- the pass -------------------------------------------------------------------
 //
@@ -778,16 +792,16 @@ rows_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUt
                 }
                 if (!live) continue;
                 if (!p.direct || !p.out_bf16) {
-                    float4* dst = reinterpret_cast<float4*>(
-                        (p.direct ? static_cast<float*>(p.out) + row * D : p.part_o + rec * D) + 32 * c);
+                    float* dst = (p.direct ? static_cast<float*>(p.out) + row * D : p.part_o + rec * D) + 32 * c;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) dst[e] = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+                    for (int e = 0; e < 4; ++e) store32(dst + 8 * e, reinterpret_cast<uint32_t*>(f) + 8 * e, p.wide);
                 } else {
-                    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * D + 32 * c);
+                    uint16_t* dst = static_cast<uint16_t*>(p.out) + row * D + 32 * c;
+                    uint32_t x[16];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        dst[e] = make_uint4(pack_bf16(f[8 * e], f[8 * e + 1]), pack_bf16(f[8 * e + 2], f[8 * e + 3]),
-                                            pack_bf16(f[8 * e + 4], f[8 * e + 5]), pack_bf16(f[8 * e + 6], f[8 * e + 7]));
+                    for (int e = 0; e < 16; ++e) x[e] = pack_bf16(f[2 * e], f[2 * e + 1]);
+                    store32(dst, x, p.wide);
+                    store32(dst + 16, x + 8, p.wide);
                 }
             }
             if (live && (DUAL || i == 0)) {
@@ -976,6 +990,7 @@ cudaError_t launch_rows(const RowsArgs& a, cudaStream_t stream) {
     p.rec0 = a.rec0;
     p.rec_stride = a.rec_stride;
     p.direct = a.direct;
+    p.wide = (reinterpret_cast<uintptr_t>(a.direct ? a.out : static_cast<void*>(a.part_o)) & 31u) == 0;
     const bool paged = a.page_table != nullptr;
     const uint64_t pool_rows = paged ? (uint64_t)a.num_pages * a.Hkv * kTile : 0;
     p.zero_row = (int)(pool_rows > 0 ? pool_rows : 1);
