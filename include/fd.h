@@ -535,12 +535,15 @@ FD_API int fd_decode_dense_noalloc(const void* q, const void* k, const void* v,
 
 /* Fault injection for tests of the time-out path; not for production use.
  * Applies to the bf16 dense and paged decode (fd_decode_dense,
- * fd_decode_paged, their unified-max variants and fd_decode_dense_noalloc)
- * launched afterwards from this process:
+ * fd_decode_paged, their unified-max variants and fd_decode_dense_noalloc),
+ * the prompt attention and the shared-prefix decode (fd_prefill_packed,
+ * fd_prefill_paged, fd_decode_*_shared_prefix) launched afterwards from this
+ * process:
  *   wait_limit_ns  > 0: the time limit of every pipeline wait (default 2 s;
  *                  0 restores it)
  *   withhold_tile  >= 0: the producer of every chunk issues no copy and no
- *                  arrival for that tile index of the chunk (-1: off), so the
+ *                  arrival for that tile index of the chunk (-1: off; 64 keys
+ *                  and values, or 128 keys in the prompt calls), so the
  *                  consumers' wait for it runs out.
  * A kernel whose wait runs out records FD_ERR_DEVICE_TIMEOUT in the device
  * status word, stops using its pipeline, lets every copy it started land

@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import inspect
 import math
 import os
 import re
@@ -149,11 +150,21 @@ def _stream(stream):
 def _on_device_of_first_tensor(fn):
     """Run a wrapper with its leading tensor's device current, so the
     library's planner, its scratch lookup and the default stream all refer to
-    the device that holds the data (every other tensor is checked against it)."""
+    the device that holds the data (every other tensor is checked against it),
+    and with an explicit stream current too, so that what the wrapper allocates
+    belongs to that stream."""
+    at = list(inspect.signature(fn).parameters).index("stream")
+
     @functools.wraps(fn)
     def wrapper(t, *args, **kwargs):
         if not (isinstance(t, torch.Tensor) and t.is_cuda):
             raise ValueError(f"{fn.__name__}: the first argument must be a CUDA tensor")
+        stream = args[at - 1] if len(args) >= at else kwargs.get("stream")
+        if stream is not None:
+            if stream.device != t.device:
+                raise ValueError(f"stream is on {stream.device}, the tensors on {t.device}")
+            with torch.cuda.stream(stream):
+                return fn(t, *args, **kwargs)
         if t.get_device() == torch._C._cuda_getDevice():
             return fn(t, *args, **kwargs)
         with torch.cuda.device(t.device):

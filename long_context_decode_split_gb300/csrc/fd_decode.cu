@@ -647,9 +647,7 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream) {
     pp.chunk_fixed = a.chunk_fixed;
     pp.phi2 = a.phi * kLog2e;
     pp.lo2 = (a.phi - kUnifiedRange) * kLog2e;
-    const unsigned long long lim = g_inject_wait_limit_ns.load(std::memory_order_relaxed);
-    pp.wait_limit_ns = lim ? lim : kWaitLimitNs;
-    pp.withhold_tile = g_inject_withhold_tile.load(std::memory_order_relaxed);
+    injected_timeout(&pp.wait_limit_ns, &pp.withhold_tile);
     pp.st.part_o = a.part_o;
     pp.st.part_ml = a.part_ml;
     pp.st.out = a.out;
@@ -676,6 +674,12 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream) {
 void inject_wait_timeout(unsigned long long wait_limit_ns, int withhold_tile) {
     g_inject_wait_limit_ns.store(wait_limit_ns, std::memory_order_relaxed);
     g_inject_withhold_tile.store(withhold_tile < 0 ? -1 : withhold_tile, std::memory_order_relaxed);
+}
+
+void injected_timeout(unsigned long long* wait_limit_ns, int* withhold_tile) {
+    const unsigned long long lim = g_inject_wait_limit_ns.load(std::memory_order_relaxed);
+    *wait_limit_ns = lim ? lim : kWaitLimitNs;
+    *withhold_tile = g_inject_withhold_tile.load(std::memory_order_relaxed);
 }
 
 cudaError_t decode_status_read(unsigned* bits, bool clear) {

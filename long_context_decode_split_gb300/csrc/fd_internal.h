@@ -67,8 +67,9 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream);
 // Device status words, one per translation unit that owns kernels.
 cudaError_t decode_status_read(unsigned* bits, bool clear);
 
-// Fault injection for the bf16 dense/paged pass (fd_debug_inject_wait_timeout).
+// Fault injection for the bf16 dense/paged pass and the prompt rows (fd_debug_inject_wait_timeout).
 void inject_wait_timeout(unsigned long long wait_limit_ns, int withhold_tile);
+void injected_timeout(unsigned long long* wait_limit_ns, int* withhold_tile);  // what a launch has to use
 
 struct QuantArgs {
     const void* k;            // [B, Hkv, L_max, D] bf16

@@ -35,6 +35,8 @@ struct RowsParams {
     int causal;
     int splits, chunk;
     int tiles;  // slots of every (head, chunk)
+    unsigned long long wait_limit_ns;  // time limit of every pipeline wait
+    int withhold_tile;                 // >= 0: fault injection, that block's keys of each chunk are never copied
     void* out;
     int out_bf16;
     float* lse;
@@ -410,7 +412,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUt
                 if (some) {
                     // hand it on (or the end)
                     const int slot = wn & 1;
-                    ok = warp_wait(&work_empty[slot], ((uint32_t)(wn >> 1) & 1u) ^ 1u);
+                    ok = warp_wait(&work_empty[slot], ((uint32_t)(wn >> 1) & 1u) ^ 1u, p.wait_limit_ns);
                     if (!ok) break;
                     if (lane == 0) {
                         work[slot] = w;
@@ -420,7 +422,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUt
                     if (!w.valid) break;
                     const int blocks = max(w.nb[0], w.nb[1]);
                     if (blocks > 0) {
-                        ok = warp_wait(q_empty, ((uint32_t)qn & 1u) ^ 1u);
+                        ok = warp_wait(q_empty, ((uint32_t)qn & 1u) ^ 1u, p.wait_limit_ns);
                         if (!ok) break;
                         ++qn;
                         if (lane == 0) {
@@ -459,9 +461,10 @@ rows_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUt
                             }
                             int& n = !DUAL && (j & 1) ? n1 : n0;
                             const int s = (!DUAL && (j & 1) ? RING : 0) + n % RING;
-                            ok = ok && warp_wait(&empty[s], ((uint32_t)(n / RING) & 1u) ^ 1u);
+                            ok = ok && warp_wait(&empty[s], ((uint32_t)(n / RING) & 1u) ^ 1u, p.wait_limit_ns);
                             if (!ok) return;
-                            if (lane == 0) {
+                            // (fault injection: that key tile gets no copy and no arrival)
+                            if (lane == 0 && (which || j != p.withhold_tile)) {
                                 const void* map = which ? static_cast<const void*>(&tmv) : static_cast<const void*>(&tmk);
                                 unsigned char* dst = ring + s * TILE;
                                 const int at = c0 + j * kBlock;
@@ -499,19 +502,19 @@ rows_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUt
                     mbar_arrive_expect_tx(next_full, 16);
                     next_cta_request(answer, next_full);
                 }
-                ok = warp_wait(next_full, (uint32_t)asked & 1u);
+                ok = warp_wait(next_full, (uint32_t)asked & 1u, p.wait_limit_ns);
                 if (ok) id = next_cta(answer);
                 __syncwarp();
             }
             if (!ok) {
                 // the others stopped early: let the copies in flight land before the CTA ends
                 if (lane == 0) atomicOr(&g_status_rows, kStatusTimeout);
-                if (qn > 0) mbar_wait(q_full, (uint32_t)(qn - 1) & 1u);
-                for (int u = max(0, n0 - RING); u < n0; ++u) mbar_wait(&full[u % RING], (uint32_t)(u / RING) & 1u);
+                if (qn > 0) mbar_wait(q_full, (uint32_t)(qn - 1) & 1u, p.wait_limit_ns);
+                for (int u = max(0, n0 - RING); u < n0; ++u) mbar_wait(&full[u % RING], (uint32_t)(u / RING) & 1u, p.wait_limit_ns);
                 for (int u = max(0, n1 - RING); u < n1; ++u)
-                    mbar_wait(&full[RING + u % RING], (uint32_t)(u / RING) & 1u);
-                mbar_wait(next_full, 0);
-                mbar_wait(next_full, 1);
+                    mbar_wait(&full[RING + u % RING], (uint32_t)(u / RING) & 1u, p.wait_limit_ns);
+                mbar_wait(next_full, 0, p.wait_limit_ns);
+                mbar_wait(next_full, 1, p.wait_limit_ns);
             }
         } else if (warp < kMmaWarp + 2) {
             // ---------------- products ----------------
@@ -526,7 +529,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUt
             uint32_t n0 = 0, qn = 0, rounds = 0;  // ring position, pieces of work with keys, blocks so far
             auto arrive = [&](uint32_t n) {  // tile n of the pipeline's ring is there: its stage
                 const uint32_t s = (DUAL ? 0 : i * RING) + n % RING;
-                ok = ok && warp_wait(&full[s], (n / RING) & 1u);
+                ok = ok && warp_wait(&full[s], (n / RING) & 1u, p.wait_limit_ns);
                 return s;
             };
             auto commit = [&](uint64_t* bar) {
@@ -555,7 +558,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUt
             };
             for (int wn = 0; ok; ++wn) {
                 const int slot = wn & 1;
-                ok = warp_wait(&work_full[slot], (uint32_t)(wn >> 1) & 1u);
+                ok = warp_wait(&work_full[slot], (uint32_t)(wn >> 1) & 1u, p.wait_limit_ns);
                 if (!ok) break;
                 const Work& w = work[slot];
                 const bool valid = uniform(w.valid) != 0;
@@ -582,7 +585,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUt
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
                 };
-                ok = warp_wait(q_full, qn & 1u);
+                ok = warp_wait(q_full, qn & 1u, p.wait_limit_ns);
                 ++qn;
                 if (ok && nb > 0) {
                     const uint32_t s0 = arrive(n0);
@@ -595,7 +598,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUt
                         if (!ok) break;
                         clear_tail(DUAL ? r : 2 * r + (int)i, sv);
                         const uint32_t sk = more ? arrive(n0 + 2 * r + 2) : 0;
-                        ok = ok && warp_wait(&p_full[i], rounds & 1u);
+                        ok = ok && warp_wait(&p_full[i], rounds & 1u, p.wait_limit_ns);
                         if (!ok) break;
                         ++rounds;
                         tc_fence_after();
@@ -617,7 +620,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUt
             if (!ok) {
                 if (lane == 0) atomicOr(&g_status_rows, kStatusTimeout);
                 commit(&drained[i]);
-                warp_wait(&drained[i], 0);
+                warp_wait(&drained[i], 0, p.wait_limit_ns);
             }
         }
     } else {
@@ -632,7 +635,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUt
         uint32_t s_round = 0, o_round = 0;
         for (int wn = 0; DUAL ? ok : true; ++wn) {
             const int slot = wn & 1;
-            ok = ok && warp_wait(&work_full[slot], (uint32_t)(wn >> 1) & 1u);
+            ok = ok && warp_wait(&work_full[slot], (uint32_t)(wn >> 1) & 1u, p.wait_limit_ns);
             // the warpgroups of a single tile meet at barriers: all of them stop, or none
             if (DUAL ? !ok : named_barrier_or(2, 256, !ok)) break;
             const Work& wk = work[slot];
@@ -665,7 +668,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUt
                         }
                     }
                 }
-                ok = warp_wait(&s_full[i], s_round & 1u);
+                ok = warp_wait(&s_full[i], s_round & 1u, p.wait_limit_ns);
                 if (!ok) break;
                 ++s_round;
                 tc_fence_after();
@@ -729,7 +732,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUt
                 if (lane == 0) mbar_arrive(&p_full[i]);
             }
             if (ok && rounds > 0) {
-                ok = warp_wait(&o_full[i], o_round & 1u);
+                ok = warp_wait(&o_full[i], o_round & 1u, p.wait_limit_ns);
                 ++o_round;
             }
             tc_fence_after();
@@ -1011,6 +1014,7 @@ cudaError_t launch_rows(const RowsArgs& a, cudaStream_t stream) {
     if (!ok) return cudaErrorInvalidValue;
     const long long tiles = rows_tiles(a.B, a.total_q, p.G, a.cu_q != nullptr);
     p.tiles = (int)tiles;
+    injected_timeout(&p.wait_limit_ns, &p.withhold_tile);
     const dim3 grid((unsigned)(tiles * a.Hkv * a.splits));
     const bool dual = rows_dual(a.B, a.total_q, p.G);
     if (a.D == 128) {

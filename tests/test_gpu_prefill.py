@@ -210,6 +210,69 @@ def test_deterministic_and_captured(fd):
         assert torch.equal(out, want) and torch.equal(lse, wlse)
 
 
+def test_no_keys_at_all(fd):
+    g = generator(18)
+    q = randn(g, 37, 4, 64)
+    k = torch.empty((0, 2, 64), dtype=torch.bfloat16, device="cuda")
+    out, lse = fd.fd_prefill_packed(q, k, k, offsets([30, 7]), offsets([0, 0]))
+    assert torch.all(out == 0) and torch.all(torch.isneginf(lse))
+    out, lse = fd.fd_prefill_packed(q[:0], k, k, offsets([]))
+    assert out.shape == (0, 4, 64)
+    assert fd.fd_device_status(clear=True) == fd.FD_OK
+
+
+def test_explicit_stream_and_wrong_tensors(fd):
+    g = generator(19)
+    q, k, v = randn(g, 300, 8, 128), randn(g, 300, 2, 128), randn(g, 300, 2, 128)
+    cu = offsets([300])
+    want, wlse = fd.fd_prefill_packed(q, k, v, cu, num_splits=2)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):
+        # outputs and workspace are allocated on the stream that uses them: nothing is handed to
+        # the current stream's work while this call still runs
+        out, lse = fd.fd_prefill_packed(q, k, v, cu, num_splits=2, stream=side)
+        torch.full((1 << 20,), 255, dtype=torch.uint8, device="cuda")
+    side.synchronize()
+    assert torch.equal(out, want) and torch.equal(lse, wlse)
+    with pytest.raises(ValueError):
+        fd.fd_prefill_packed(q, k.float(), v, cu)
+    with pytest.raises(ValueError):
+        fd.fd_prefill_packed(q, k, v.cpu(), cu)
+    with pytest.raises(ValueError):
+        fd.fd_prefill_packed(q, k, v[:299], cu)
+    with pytest.raises(ValueError):
+        fd.fd_prefill_packed(q, k[:, :, :64], v, cu)
+    with pytest.raises(ValueError):
+        fd.fd_prefill_packed(q.transpose(0, 1), k, v, cu)
+    with pytest.raises(ValueError):
+        fd.fd_prefill_packed(q, k[:1].expand(300, 2, 128), v, cu)
+    with pytest.raises(ValueError):
+        fd.fd_prefill_packed(q, k, v, cu.long())
+    with pytest.raises(ValueError):
+        fd.fd_prefill_packed(q, k, v, cu, num_splits=2, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(fd.FdError):
+        fd.fd_prefill_packed(q, k, v, cu, scale=-1.0)
+
+
+def test_two_calls_at_once(fd):
+    # two streams, each call with its own results: nothing is shared between them
+    g = generator(20)
+    sets = [(randn(g, 3000, 8, 128), randn(g, 3000, 2, 128), randn(g, 3000, 2, 128)) for _ in range(2)]
+    cu = offsets([1000, 2000])
+    want = [fd.fd_prefill_packed(*s, cu) for s in sets]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(5):
+        for i in range(2):
+            got[i].append(fd.fd_prefill_packed(*sets[i], cu, stream=streams[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for out, lse in got[i]:
+            assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])
+
+
 # ---------------------------------------------------------------- paged
 
 def run_paged(fd, new, ctx, Hq, Hkv, d, seed, causal=True, **kw):
