@@ -55,8 +55,7 @@ struct RowsItem {
     int t0;      // first token of the tile within the sequence
 };
 
-__device__ __forceinline__ int checked_offset(const int32_t* cu, int i, int lo, int hi) {
-    const int c = cu[i];
+__device__ __forceinline__ int checked(int c, int lo, int hi) {
     if (c < lo || c > hi) {
         if ((threadIdx.x & 31) == 0) atomicOr(&g_status_rows, kStatusBadSeqLen);
         return c < lo ? lo : hi;
@@ -68,15 +67,11 @@ __device__ __forceinline__ int checked_offset(const int32_t* cu, int i, int lo, 
 // s + 1, at least as many as the tiles it has (`per` tokens each), so a slot's
 // sequence is found by a search of cu_q alone.
 __device__ __forceinline__ RowsItem find_item(const RowsParams& p, int slot, int per) {
-    RowsItem it;
-    it.seq = 0;
-    it.q0 = 0;
-    it.Lq = p.total_q;
-    it.k0 = 0;
+    int lo = 0;
     if (p.cu_q) {
         // the last s with first_slot(s) <= slot; each round every lane probes one of 32 places
         const int lane = threadIdx.x & 31;
-        int lo = 0, n = p.B;  // the answer is in [lo, lo + n)
+        int n = p.B;  // the answer is in [lo, lo + n)
         while (n > 1) {
             const int step = (n + 31) / 32;
             const int s = lo + lane * step;
@@ -86,19 +81,27 @@ __device__ __forceinline__ RowsItem find_item(const RowsParams& p, int slot, int
             lo += hit * step;
             n = min(step, n - hit * step);
         }
-        it.seq = lo;
-        it.q0 = checked_offset(p.cu_q, lo, 0, p.total_q);
-        it.Lq = checked_offset(p.cu_q, lo + 1, it.q0, p.total_q) - it.q0;
     }
-    it.t0 = (slot - (it.q0 / per + it.seq)) * per;
+    // every load first (one memory latency), then the checks
+    int q0 = 0, q1 = p.total_q, k0 = 0, k1 = p.page_table ? p.max_k : p.total_k;
+    if (p.cu_q) {
+        q0 = p.cu_q[lo];
+        q1 = p.cu_q[lo + 1];
+    }
     if (p.page_table) {
-        it.Lk = p.seq_lens ? checked_offset(p.seq_lens, it.seq, 0, p.max_k) : p.max_k;
+        if (p.seq_lens) k1 = p.seq_lens[lo];
     } else if (p.cu_k) {
-        it.k0 = checked_offset(p.cu_k, it.seq, 0, p.total_k);
-        it.Lk = checked_offset(p.cu_k, it.seq + 1, it.k0, p.total_k) - it.k0;
-    } else {
-        it.Lk = p.total_k;
+        k0 = p.cu_k[lo];
+        k1 = p.cu_k[lo + 1];
     }
+    RowsItem it;
+    it.seq = lo;
+    it.q0 = checked(q0, 0, p.total_q);
+    it.Lq = checked(q1, it.q0, p.total_q) - it.q0;
+    const int most = p.page_table ? p.max_k : p.total_k;
+    it.k0 = checked(k0, 0, most);
+    it.Lk = checked(k1, it.k0, most) - it.k0;
+    it.t0 = (slot - (it.q0 / per + it.seq)) * per;
     return it;
 }
 
