@@ -5,7 +5,9 @@ shapes, devices and contiguity, allocates outputs and workspace with torch
 when the caller did not pass them, and calls the C entry point of the same
 name (declared in include/fd.h) on the current CUDA stream.  All arithmetic
 runs in the library's CUDA kernels; there is no fallback.  A missing or
-unloadable libfd.so raises an error.
+unloadable libfd.so raises an error.  The prompt, shared-prefix, page and
+append calls do these steps in the compiled module _marshal
+(csrc/fd_binding.cpp), the others in Python.
 """
 from __future__ import annotations
 
@@ -640,52 +642,27 @@ def fd_decode_paged_fp4(q, k_pages, k_page_scales, v_pages, v_page_scales, page_
                            seq_lens, scale, num_splits, out, lse, out_dtype, want_lse, workspace, stream)
 
 
-def _check_tokens(t, name, H=None, d=None):
-    """[T, H, d] bf16 whose tokens may lie further apart than H * d elements (a
-    slice of a fused projection); returns the token stride in elements."""
-    shape = t.shape
-    if len(shape) != 3 or (H is not None and shape[1] != H) or (d is not None and shape[2] != d):
-        raise ValueError(f"{name} must be [tokens, {'heads' if H is None else H}, {'d' if d is None else d}], "
-                         f"got {tuple(shape)}")
-    row = shape[1] * shape[2]
-    if t.is_contiguous():
-        stride = row
-    else:
-        T, H, d = shape
-        s = t.stride()
-        if t.numel() and ((d > 1 and s[2] != 1) or (H > 1 and s[1] != d)):
-            raise ValueError(f"{name}: the heads of a token must be contiguous")
-        stride = s[0] if T > 1 else row
-        if stride < row:
-            raise ValueError(f"{name}: tokens must not overlap")
-    if t.dtype is not torch.bfloat16 or t.get_device() != torch._C._cuda_getDevice():
-        # raises with the reason (get_device() is -1 for a CPU tensor)
-        _check_cuda(t.contiguous(), name, torch.bfloat16)
-    return stride
+_native = None
 
 
-_I32 = torch.int32
+def _binding():
+    """The compiled half of the binding (checks, allocations and the C call of
+    the functions below), bound to libfd on first use."""
+    global _native
+    if _native is None:
+        load()
+        try:
+            from . import _marshal as native
+        except ImportError as e:
+            raise ImportError(f"the compiled binding is not built; run long_context_decode_split_gb300._build.build() "
+                              f"({e})") from None
+        native.bind(LIB_PATH, FdError)
+        _native = native
+    return _native
 
 
-def _check_ints(t, name, shape=None):
-    """A contiguous int32 tensor on the current device, of the given shape."""
-    if (t.dtype is not _I32 or t.get_device() != torch._C._cuda_getDevice() or not t.is_contiguous()
-            or (shape is not None and t.shape != shape)):
-        _check_cuda(t, name, _I32, shape)  # raises with the reason
-
-
-def _check_offsets(t, name):
-    _check_ints(t, name)
-    if t.dim() != 1 or t.numel() < 1:
-        raise ValueError(f"{name} must be [B + 1]")
-    return t.numel() - 1
-
-
-def _check_table(t, B):
-    _check_ints(t, "page_table")
-    if t.dim() != 2 or t.shape[0] != B:
-        raise ValueError("page_table must be [B, max_pages]")
-    return t.shape[1]
+def _code(out_dtype):
+    return FD_OUT_BF16 if out_dtype == "bf16" else _out_code(out_dtype)[0]
 
 
 def fd_prefill_num_splits(B, total_q, Hq, Hkv, max_k, d, num_splits=0) -> int:
@@ -699,75 +676,30 @@ def fd_prefill_workspace_size(B, total_q, Hq, Hkv, max_k, d, num_splits=0) -> in
     return _remembered_size("fd_prefill_workspace_size", B, total_q, Hq, Hkv, max_k, d, num_splits)
 
 
-@_on_device_of_first_tensor
 def fd_prefill_packed(q, k, v, cu_seqlens_q, cu_seqlens_k=None, scale=None, causal=True, num_splits=0, out=None,
                       lse=None, out_dtype="bf16", want_lse=True, workspace=None, stream=None):
     """Attention of whole prompts packed one behind the other.  q [Tq,Hq,d],
     k, v [Tk,Hkv,d] bf16 (tokens may be strided), cu_seqlens_q [B+1] int32,
     cu_seqlens_k [B+1] or None (= cu_seqlens_q).  Returns (out [Tq,Hq,d],
     lse [Tq,Hq] or None); rows of no sequence are not written."""
-    qs = _check_tokens(q, "q")
-    Tq, Hq, d = q.shape
-    ks = _check_tokens(k, "k", None, d)
-    Tk, Hkv, _ = k.shape
-    vs = _check_tokens(v, "v", Hkv, d)
-    _need(v.shape[0] == Tk, "k and v must have the same number of tokens")
-    B = _check_offsets(cu_seqlens_q, "cu_seqlens_q")
-    if cu_seqlens_k is None:
-        cu_seqlens_k = cu_seqlens_q
-    else:
-        _check_ints(cu_seqlens_k, "cu_seqlens_k", (B + 1,))
-    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    code, out, lse = _outputs(Tq, Hq, d, q.device, out, lse, out_dtype, want_lse)
-    ws = _workspace(fd_prefill_workspace_size(B, Tq, Hq, Hkv, Tk, d, num_splits), q.device, workspace)
-    st = load().fd_prefill_packed(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), B, Tq,
-        Tk, Hq, Hkv, d, scale, 1 if causal else 0, num_splits, out.data_ptr(), code, _p(lse), _p(ws), _nbytes(ws),
-        _stream(stream))
-    _raise(st, "fd_prefill_packed")
-    return out, lse
+    return _binding().prefill_packed(q, k, v, cu_seqlens_q, cu_seqlens_k, scale, causal, num_splits, out, lse,
+                                     _code(out_dtype), want_lse, workspace, stream)
 
 
-def _check_pool(k_pages, v_pages, d, num_pages=0):
-    _check_cuda(k_pages, "k_pages", torch.bfloat16)
-    _need(k_pages.dim() == 4 and k_pages.shape[3] == d, "k_pages must be [P, Hkv, page, d]")
-    _check_cuda(v_pages, "v_pages", torch.bfloat16, k_pages.shape)
-    P, Hkv, page_size, _ = k_pages.shape
-    _need(0 <= num_pages <= P, "num_pages must be within the pool")
-    return P, Hkv, page_size
-
-
-@_on_device_of_first_tensor
 def fd_prefill_paged(q, k_pages, v_pages, page_table, num_pages, cu_seqlens_q, seq_lens, scale=None, causal=True,
                      num_splits=0, out=None, lse=None, out_dtype="bf16", want_lse=True, workspace=None, stream=None):
     """Attention of prompt tails over a paged cache that holds their keys and
     values.  q [Tq,Hq,d] bf16 (tokens may be strided), k_pages/v_pages
     [P,Hkv,64,d] bf16, page_table [B,max_pages] int32, cu_seqlens_q [B+1]
     int32, seq_lens [B] int32 (all keys; the queries are the last ones)."""
-    qs = _check_tokens(q, "q")
-    Tq, Hq, d = q.shape
-    num_pages = int(num_pages)
-    _, Hkv, page_size = _check_pool(k_pages, v_pages, d, num_pages)
-    B = _check_offsets(cu_seqlens_q, "cu_seqlens_q")
-    max_pages = _check_table(page_table, B)
-    _check_ints(seq_lens, "seq_lens", (B,))
-    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    code, out, lse = _outputs(Tq, Hq, d, q.device, out, lse, out_dtype, want_lse)
-    ws = _workspace(fd_prefill_workspace_size(B, Tq, Hq, Hkv, max_pages * page_size, d, num_splits), q.device,
-                    workspace)
-    st = load().fd_prefill_paged(
-        q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), qs, page_table.data_ptr(), max_pages, num_pages,
-        cu_seqlens_q.data_ptr(), seq_lens.data_ptr(), page_size, B, Tq, Hq, Hkv, d, scale, 1 if causal else 0,
-        num_splits, out.data_ptr(), code, _p(lse), _p(ws), _nbytes(ws), _stream(stream))
-    _raise(st, "fd_prefill_paged")
-    return out, lse
+    return _binding().prefill_paged(q, k_pages, v_pages, page_table, num_pages, cu_seqlens_q, seq_lens, scale, causal,
+                                    num_splits, out, lse, _code(out_dtype), want_lse, workspace, stream)
 
 
 def fd_shared_prefix_workspace_size(B, Hq, Hkv, prefix_len, L_own, d, num_splits=0) -> int:
     return _remembered_size("fd_shared_prefix_workspace_size", B, Hq, Hkv, prefix_len, L_own, d, num_splits)
 
 
-@_on_device_of_first_tensor
 def fd_decode_paged_shared_prefix(q, k_pages, v_pages, prefix_table, page_table, num_pages, seq_lens, scale=None,
                                   num_splits=0, out=None, lse=None, out_dtype="bf16", want_lse=True, workspace=None,
                                   stream=None):
@@ -775,59 +707,20 @@ def fd_decode_paged_shared_prefix(q, k_pages, v_pages, prefix_table, page_table,
     64 * len(prefix_table) tokens, read once for the whole batch.
     prefix_table [n] int32 page ids (the first n entries of every page_table
     row are not read); seq_lens [B] int32 counts all tokens."""
-    _check_cuda(q, "q", torch.bfloat16)
-    _need(q.dim() == 3, "q must be [B, Hq, d]")
-    B, Hq, d = q.shape
-    num_pages = int(num_pages)
-    _, Hkv, page_size = _check_pool(k_pages, v_pages, d, num_pages)
-    _check_ints(prefix_table, "prefix_table")
-    _need(prefix_table.dim() == 1, "prefix_table must be [prefix_pages]")
-    max_pages, n = _check_table(page_table, B), prefix_table.numel()
-    _need(n <= max_pages, "prefix_table must be no longer than a row of page_table")
-    _check_ints(seq_lens, "seq_lens", (B,))
-    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    code, out, lse = _outputs(B, Hq, d, q.device, out, lse, out_dtype, want_lse)
-    ws = _workspace(fd_shared_prefix_workspace_size(B, Hq, Hkv, n * page_size, (max_pages - n) * page_size, d,
-                                                    num_splits), q.device, workspace)
-    st = load().fd_decode_paged_shared_prefix(
-        q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), prefix_table.data_ptr(), n, page_table.data_ptr(),
-        max_pages, num_pages, seq_lens.data_ptr(), page_size, B, Hq, Hkv, d, scale, num_splits, out.data_ptr(), code,
-        _p(lse), _p(ws), _nbytes(ws), _stream(stream))
-    _raise(st, "fd_decode_paged_shared_prefix")
-    return out, lse
+    return _binding().paged_shared_prefix(q, k_pages, v_pages, prefix_table, page_table, num_pages, seq_lens, scale,
+                                          num_splits, out, lse, _code(out_dtype), want_lse, workspace, stream)
 
 
-@_on_device_of_first_tensor
 def fd_decode_dense_shared_prefix(q, k_prefix, v_prefix, k, v, seq_lens=None, scale=None, num_splits=0, out=None,
                                   lse=None, out_dtype="bf16", want_lse=True, workspace=None, stream=None):
     """fd_decode_dense for a batch whose sequences start with the same tokens:
     k_prefix, v_prefix [Hkv,P,d] bf16 (read once for the whole batch), then
     every sequence's own k, v [B,Hkv,L_max,d] with seq_lens [B] int32 own
     tokens (or None)."""
-    _check_cuda(q, "q", torch.bfloat16)
-    _need(q.dim() == 3, "q must be [B, Hq, d]")
-    B, Hq, d = q.shape
-    _check_cuda(k_prefix, "k_prefix", torch.bfloat16)
-    _need(k_prefix.dim() == 3 and k_prefix.shape[2] == d, "k_prefix must be [Hkv, P, d]")
-    Hkv, P, _ = k_prefix.shape
-    _check_cuda(v_prefix, "v_prefix", torch.bfloat16, k_prefix.shape)
-    _check_cuda(k, "k", torch.bfloat16)
-    _need(k.dim() == 4 and k.shape[0] == B and k.shape[1] == Hkv and k.shape[3] == d, "k must be [B, Hkv, L_max, d]")
-    L_max = k.shape[2]
-    _check_cuda(v, "v", torch.bfloat16, k.shape)
-    if seq_lens is not None:
-        _check_ints(seq_lens, "seq_lens", (B,))
-    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    code, out, lse = _outputs(B, Hq, d, q.device, out, lse, out_dtype, want_lse)
-    ws = _workspace(fd_shared_prefix_workspace_size(B, Hq, Hkv, P, L_max, d, num_splits), q.device, workspace)
-    st = load().fd_decode_dense_shared_prefix(
-        q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), P, k.data_ptr(), v.data_ptr(), _p(seq_lens), B, Hq, Hkv,
-        L_max, d, scale, num_splits, out.data_ptr(), code, _p(lse), _p(ws), _nbytes(ws), _stream(stream))
-    _raise(st, "fd_decode_dense_shared_prefix")
-    return out, lse
+    return _binding().dense_shared_prefix(q, k_prefix, v_prefix, k, v, seq_lens, scale, num_splits, out, lse,
+                                          _code(out_dtype), want_lse, workspace, stream)
 
 
-@_on_device_of_first_tensor
 def fd_assign_pages(page_table, cached_lens, new_lens, free_pages, total_new, free_head=None, page_size=64,
                     seq_lens=None, cu_seqlens=None, slots=None, free_head_out=None, stream=None):
     """Pages and slots for the new tokens of a batch.  page_table [B,max_pages]
@@ -836,81 +729,22 @@ def fd_assign_pages(page_table, cached_lens, new_lens, free_pages, total_new, fr
     None = 0), total_new the number of slots.  Returns (seq_lens [B],
     cu_seqlens [B+1], slots [total_new] int64, free_head_out [1]); seq_lens may
     be cached_lens and free_head_out may be free_head (updated in place)."""
-    _check_ints(page_table, "page_table")
-    if page_table.dim() != 2:
-        raise ValueError("page_table must be [B, max_pages]")
-    B, max_pages = page_table.shape
-    _check_ints(cached_lens, "cached_lens", (B,))
-    _check_ints(new_lens, "new_lens", (B,))
-    _check_ints(free_pages, "free_pages")
-    if free_pages.dim() != 1:
-        raise ValueError("free_pages must be [F]")
-    if free_head is not None:
-        _check_ints(free_head, "free_head", (1,))
-    total_new = int(total_new)
-    _need(total_new >= 0, "total_new must be >= 0")
-    dev = page_table.device
-    seq_lens = _int32_out(seq_lens, "seq_lens", (B,), dev)
-    cu_seqlens = _int32_out(cu_seqlens, "cu_seqlens", (B + 1,), dev)
-    free_head_out = _int32_out(free_head_out, "free_head_out", (1,), dev)
-    if slots is None:
-        slots = torch.empty(total_new, dtype=torch.int64, device=dev)
-    else:
-        _check_cuda(slots, "slots", torch.int64, (total_new,))
-    st = load().fd_assign_pages(
-        cached_lens.data_ptr(), new_lens.data_ptr(), B, page_table.data_ptr(), max_pages, int(page_size),
-        free_pages.data_ptr(), free_pages.numel(), _p(free_head), total_new, seq_lens.data_ptr(),
-        cu_seqlens.data_ptr(), slots.data_ptr(), free_head_out.data_ptr(), _stream(stream))
-    _raise(st, "fd_assign_pages")
-    return seq_lens, cu_seqlens, slots, free_head_out
+    return _binding().assign_pages(page_table, cached_lens, new_lens, free_pages, total_new, free_head, page_size,
+                                   seq_lens, cu_seqlens, slots, free_head_out, stream)
 
 
-def _int32_out(t, name, shape, device):
-    if t is None:
-        return torch.empty(shape, dtype=_I32, device=device)
-    _check_ints(t, name, shape)
-    return t
-
-
-@_on_device_of_first_tensor
 def fd_append_kv_paged(k, v, slots, k_pages, v_pages, stream=None):
     """Store new rows k, v [T,Hkv,d] bf16 (tokens may be strided) at slots [T]
     int64 of the pools k_pages, v_pages [P,Hkv,64,d] bf16 (negative slots are
     skipped).  Returns (k_pages, v_pages)."""
-    ks = _check_tokens(k, "k")
-    T, Hkv, d = k.shape
-    vs = _check_tokens(v, "v", Hkv, d)
-    _need(v.shape[0] == T, "k and v must have the same number of tokens")
-    _check_cuda(slots, "slots", torch.int64, (T,))
-    P, heads, page_size = _check_pool(k_pages, v_pages, d)
-    _need(heads == Hkv, "k_pages must have the heads of k")
-    st = load().fd_append_kv_paged(k.data_ptr(), v.data_ptr(), ks, vs, slots.data_ptr(), T, Hkv, d, k_pages.data_ptr(),
-                                   v_pages.data_ptr(), P, page_size, _stream(stream))
-    _raise(st, "fd_append_kv_paged")
-    return k_pages, v_pages
+    return _binding().append_kv(k, v, slots, k_pages, v_pages, stream)
 
 
-@_on_device_of_first_tensor
 def fd_append_kv_paged_fp8(k, v, slots, k_pages, k_page_scales, v_pages, v_page_scales, stream=None):
     """fd_append_kv_paged into the paged fp8 cache: k_pages, v_pages [P,Hkv,64,d]
     uint8 codes, k_page_scales, v_page_scales [P,Hkv,64] float32; rows are
     encoded as by fd_quantize_kv_fp8."""
-    ks = _check_tokens(k, "k")
-    T, Hkv, d = k.shape
-    vs = _check_tokens(v, "v", Hkv, d)
-    _need(v.shape[0] == T, "k and v must have the same number of tokens")
-    _check_cuda(slots, "slots", torch.int64, (T,))
-    _check_cuda(k_pages, "k_pages", torch.uint8)
-    _need(k_pages.dim() == 4 and k_pages.shape[1] == Hkv and k_pages.shape[3] == d, "k_pages must be [P, Hkv, page, d]")
-    P, _, page_size, _ = k_pages.shape
-    _check_cuda(v_pages, "v_pages", torch.uint8, k_pages.shape)
-    _check_cuda(k_page_scales, "k_page_scales", torch.float32, (P, Hkv, page_size))
-    _check_cuda(v_page_scales, "v_page_scales", torch.float32, (P, Hkv, page_size))
-    st = load().fd_append_kv_paged_fp8(k.data_ptr(), v.data_ptr(), ks, vs, slots.data_ptr(), T, Hkv, d,
-                                       k_pages.data_ptr(), k_page_scales.data_ptr(), v_pages.data_ptr(),
-                                       v_page_scales.data_ptr(), P, page_size, _stream(stream))
-    _raise(st, "fd_append_kv_paged_fp8")
-    return k_pages, k_page_scales, v_pages, v_page_scales
+    return _binding().append_kv_fp8(k, v, slots, k_pages, k_page_scales, v_pages, v_page_scales, stream)
 
 
 def fd_debug_inject_wait_timeout(wait_limit_ns=0, withhold_tile=-1) -> int:

@@ -1,6 +1,7 @@
-"""Build libfd.so (the C-ABI CUDA library) in-tree for sm_103a.
+"""Build libfd.so (the C-ABI CUDA library) in-tree for sm_103a, and the compiled
+half of the Python binding (_marshal.so, host code against torch's headers).
 
-Each translation unit under csrc/ is compiled by nvcc in parallel, then
+Each CUDA translation unit under csrc/ is compiled by nvcc in parallel, then
 linked (static CUDA runtime) into long_context_decode_split_gb300/libfd.so.
 Run ``python -m long_context_decode_split_gb300._build``.
 """
@@ -18,6 +19,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJ_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfd.so")
+BINDING = os.path.join(PKG, "_marshal.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -35,14 +37,39 @@ def nvcc() -> str:
 
 def _inputs():
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "fd.h")]
-    return [f for f in files if f.endswith((".cu", ".cuh", ".h"))]
+    return [f for f in files if f.endswith((".cu", ".cuh", ".h", ".cpp"))]
 
 
 def is_stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return any(os.path.getmtime(f) > t for f in _inputs())
+
+
+def _cuda_include():
+    return os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+
+
+def build_binding() -> str:
+    import sysconfig
+
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    lib = os.path.join(root, "lib")
+    includes = [INCLUDE, os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                sysconfig.get_paths()["include"], _cuda_include()]
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[f for i in includes for f in ("-isystem", i)], os.path.join(CSRC, "fd_binding.cpp"), "-o", tmp,
+           f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{lib}", "-ldl"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on fd_binding.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 def build(verbose: bool = False, force: bool = False) -> str:
@@ -63,8 +90,10 @@ def build(verbose: bool = False, force: bool = False) -> str:
             print(r.stdout + r.stderr, flush=True)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(build_binding)
         objs = list(ex.map(compile_one, SOURCES))
+        binding.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [cc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     if verbose:
