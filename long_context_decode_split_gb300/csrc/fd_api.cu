@@ -1,6 +1,7 @@
 // fd_api.cu -- the extern "C" entry points declared in include/fd.h: host-side
 // argument checks, the split planner and the dispatch to the kernels.  No
 // entry point allocates memory or synchronises (except fd_device_status).
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -347,11 +348,16 @@ RowsPlan rows_chunks(int max_k, long long splits, bool exact) {
     return pl;
 }
 
-// The shared part of a shared-prefix decode: `ctas` CTAs per chunk, one per SM
-// at a time, all with the same work.  A wave of chunks of c blocks takes about
-// c + 4 blocks of time (set-up, first copies, last output), every chunk costs
-// merge work, so: the count with the least waves x (c + 4) + chunks / 8.
-RowsPlan shared_rows_plan(long long ctas, int max_k, int requested) {
+// The shared part of a shared-prefix decode: `ctas` pieces of work per chunk,
+// all alike, one per SM at a time; with `own` further pieces of about own_blocks
+// blocks beside them.  A piece of c blocks takes about c + 4 blocks of time
+// (set-up, first copies, last output), every chunk costs merge work, so: the
+// count with the least of that, the longest SM's share or the mean.  Own pieces
+// are short, and with nothing but them running the copies do not fill HBM: where
+// the SMs that the chunks leave free get through them in a chunk's time, that
+// counts a tenth less (32 sequences behind 128K tokens: 14 chunks 108 us, 16 to
+// 19 chunks 119 to 121 us).
+RowsPlan shared_rows_plan(long long ctas, int max_k, int requested, long long own, double own_blocks) {
     if (requested > 0) return rows_chunks(max_k, requested, true);
     const int sms = current_sm_count(), blocks = (max_k + 127) / 128;
     long long best_s = 1;
@@ -360,8 +366,11 @@ RowsPlan shared_rows_plan(long long ctas, int max_k, int requested) {
         for (long long S = 1; S <= blocks && (S == 1 || ctas * S <= 8LL * sms); ++S) {
             const long long c = (blocks + S - 1) / S;
             if ((blocks + c - 1) / c != S) continue;  // the chunks of a smaller count
-            const long long waves = (ctas * S + sms - 1) / sms;
-            const double cost = (double)waves * (double)(c + 4) + (double)S / 8.0;
+            const double waves = (double)((ctas * S + sms - 1) / sms);
+            const double mean = ((double)(ctas * S) * (double)(c + 4) + (double)own * (own_blocks + 4)) / sms;
+            const bool beside = (double)own * (own_blocks + 4) <= (double)(sms - ctas * S) * (double)(c + 4);
+            const double busy = std::max(waves * (double)(c + 4), mean);
+            const double cost = (own > 0 && !beside ? 1.1 * busy : busy) + (double)S / 8.0;
             if (cost < best) {
                 best = cost;
                 best_s = S;
@@ -437,23 +446,56 @@ int prefill_entry(fd::RowsArgs& a, int num_splits, int out_dtype, void* workspac
 }
 
 // The two parts of a shared-prefix decode: chunks of the shared tokens, then
-// chunks of every sequence's own tokens, in one list of partials.
+// chunks of every sequence's own tokens, in one list of partials.  While the
+// batch's queries of a KV head fit one tile, both are work of one launch (8
+// sequences behind 8K tokens: 17.5 us, 20.4 us in two; 32 behind 128K: 105.8 and
+// 112.9 us); beyond that the shared part is bound by the tensor cores, where a
+// piece with a few own rows would waste a tile, and the split-KV pass takes the
+// own tokens (128 behind 64K: 286 us together, 250 us apart).
 struct SharedPlan {
     RowsPlan shared;
-    Plan own;
-    int list;  // records per (sequence, query head)
+    bool together;
+    RowsPlan own_rows;  // together
+    Plan own;           // apart
+    int list;           // records per (sequence, query head)
+    int own_splits() const { return together ? own_rows.splits : own.splits; }
 };
 
-SharedPlan shared_plan(int B, int Hq, int Hkv, int prefix_len, int L_own, int d, int num_splits) {
+SharedPlan shared_plan_uncached(int B, int Hq, int Hkv, int prefix_len, int L_own, int d, int num_splits) {
     SharedPlan s;
-    s.shared = shared_rows_plan(fd::rows_tiles(1, B, Hq / Hkv, false) * Hkv, prefix_len, num_splits);
-    // own tokens: one chunk each while the sequences fill the SMs and are short
-    // (128 sequences of up to 1024 own tokens, 8 KV heads: 46.5 us, 60.5 us in the
-    // decode's 14-tile chunks)
+    s.together = fd::rows_single(1, B, Hq / Hkv);
+    const int blocks = (L_own + 127) / 128;
+    // own tokens in pieces of up to 16 blocks, 16 pieces at most
+    s.own_rows = rows_chunks(L_own, blocks <= 16 ? 1 : blocks < 256 ? (blocks + 15) / 16 : 16, false);
+    // one chunk each while the sequences fill the SMs and are short (128 sequences
+    // of up to 1024 own tokens, 8 KV heads: 46.5 us, 60.5 us in the decode's
+    // 14-tile chunks)
     const bool short_own = (long long)B * Hkv >= current_sm_count() && L_own <= 32 * kTile;
     s.own = decode_plan(B, Hq, Hkv, L_own, d, short_own ? 1 : 0, true);
-    s.list = s.shared.splits + (L_own > 0 ? s.own.splits : 0);
+    const long long own = s.together && L_own > 0 ? (long long)B * Hkv * s.own_rows.splits : 0;
+    s.shared = shared_rows_plan(fd::rows_tiles(1, B, Hq / Hkv, false) * Hkv, prefix_len, num_splits, own,
+                                0.5 * blocks / s.own_rows.splits);
+    s.list = s.shared.splits + (L_own > 0 ? s.own_splits() : 0);
     return s;
+}
+
+// Remembered per thread for the last few argument sets, like the decode's plans.
+SharedPlan shared_plan(int B, int Hq, int Hkv, int prefix_len, int L_own, int d, int num_splits) {
+    struct Entry {
+        int key[8];
+        SharedPlan pl;
+    };
+    constexpr int kEntries = 8;
+    thread_local Entry cache[kEntries] = {};
+    thread_local int next = 0;
+    const int key[8] = {B, Hq, Hkv, prefix_len, L_own, d, num_splits, current_sm_count()};
+    for (const Entry& e : cache)
+        if (e.pl.list > 0 && std::memcmp(e.key, key, sizeof key) == 0) return e.pl;
+    Entry& e = cache[next];
+    next = (next + 1) % kEntries;
+    std::memcpy(e.key, key, sizeof key);
+    e.pl = shared_plan_uncached(B, Hq, Hkv, prefix_len, L_own, d, num_splits);
+    return e.pl;
 }
 
 int check_shared(int B, int Hq, int Hkv, int prefix_len, int L_own, int d, int num_splits) {
@@ -503,9 +545,21 @@ int shared_entry(fd::RowsArgs& r, fd::DecodeArgs& o, int prefix_len, int L_own, 
     r.part_ml = ml;
     r.rec0 = 0;
     r.rec_stride = pl.list;
+    if (L_own > 0 && pl.together) {
+        r.own_k = o.k;
+        r.own_v = o.v;
+        r.own_lens = o.seq_lens;
+        r.own_table = o.page_table;
+        r.own_table_stride = o.max_pages;
+        r.own_max = L_own;
+        r.own_skip = o.skip_tokens;
+        r.own_splits = pl.own_rows.splits;
+        r.own_chunk = pl.own_rows.chunk;
+        r.own_rec0 = pl.shared.splits;
+    }
     cudaError_t e = fd::launch_rows(r, s);
     if (e != cudaSuccess) return to_status(e);
-    if (L_own > 0) {
+    if (L_own > 0 && !pl.together) {
         o.splits = pl.own.splits;
         o.chunk_fixed = pl.own.chunk_fixed;
         o.out_bf16 = out_bf16;

@@ -164,7 +164,19 @@ struct RowsArgs {
     float* part_ml;           // and [total_q, Hq, rec_stride, 2]
     int rec0, rec_stride;     // (every record of a query row is written, empty ones with m = -inf)
     int direct;               // write out/lse instead of records
+    // Own tokens of a shared-prefix decode, beside a single tile's work (own_work(..)
+    // > 0): query token b also attends own_lens[b] - own_skip tokens of its own, in
+    // chunks written to the records own_rec0 + chunk.
+    const void* own_k;        // contiguous [total_q, Hkv, own_max, D]; paged: the pools above
+    const void* own_v;
+    const int32_t* own_lens;  // [total_q] or null (own_max)
+    const int32_t* own_table; // paged: [total_q, own_table_stride]
+    long long own_table_stride;
+    int own_max, own_skip;    // own_max: most own tokens of a sequence
+    int own_splits, own_chunk, own_rec0;  // own_splits == 0: they are someone else's
 };
+// Whether the tokens of this call take one tile per CTA (own tokens are then part of its work).
+bool rows_single(int B, int total_q, int G);
 // Tiles of `total_q` tokens: how many tokens one takes, and how many tiles there are at most
 // (B sequences by offsets) or exactly (one sequence).
 int rows_tokens(int B, int total_q, int G);

@@ -45,10 +45,22 @@ struct RowsParams {
     int rec0, rec_stride, direct;
     int wide;      // results (or records) are 32-byte aligned
     int zero_row;  // a row past the page pool: a tile copied from there is zeros
+    // every query token's own keys (a shared-prefix decode of a single tile)
+    int shared_work;  // pieces of work before those
+    const int32_t* own_lens;
+    const int32_t* own_table;
+    long long own_table_stride;
+    int own_max, own_skip, own_splits, own_chunk, own_rec0;
+};
+
+// The tensor maps of a launch: queries, keys, values; then the same of the own keys.
+struct RowsMaps {
+    CUtensorMap q, k, v, own_q, own_k, own_v;
 };
 
 // One tile's place: the sequence, its query tokens and its keys.
 struct RowsItem {
+    int own;  // a query token with its own keys
     int seq;
     int q0, Lq;  // first query token of the sequence in the packed array, and their number
     int k0, Lk;  // the same of its keys (k0 = 0 when paged)
@@ -95,6 +107,7 @@ __device__ __forceinline__ RowsItem find_item(const RowsParams& p, int slot, int
         k1 = p.cu_k[lo + 1];
     }
     RowsItem it;
+    it.own = 0;
     it.seq = lo;
     it.q0 = checked(q0, 0, p.total_q);
     it.Lq = checked(q1, it.q0, p.total_q) - it.q0;
@@ -105,9 +118,21 @@ __device__ __forceinline__ RowsItem find_item(const RowsParams& p, int slot, int
     return it;
 }
 
+// Query token b with its own keys.
+__device__ __forceinline__ RowsItem own_item(const RowsParams& p, int b) {
+    RowsItem it;
+    it.own = 1;
+    it.seq = it.q0 = b;
+    it.Lq = 1;
+    it.k0 = it.t0 = 0;
+    it.Lk = p.own_lens ? max(checked(p.own_lens[b], 0, p.own_skip + p.own_max) - p.own_skip, 0) : p.own_max;
+    return it;
+}
+
 // Keys that query token t of the item's sequence sees.
 __device__ __forceinline__ int visible_keys(const RowsParams& p, const RowsItem& it, int t) {
     int n = it.Lk;
+    if (it.own) return n;
     if (p.causal) n = min(n, it.Lk - it.Lq + t + 1);
     if (p.row_lens) n = min(n, p.row_lens[it.q0 + t]);
     return max(n, 0);
@@ -290,12 +315,23 @@ __device__ __forceinline__ bool named_barrier_or(int id, int nthreads, bool x) {
     return r != 0;
 }
 
+// A paged item's row of the page table, and how many entries of it hold its keys.
+__device__ __forceinline__ const int32_t* table_of(const RowsParams& p, const RowsItem& it) {
+    return it.own ? p.own_table + (size_t)it.seq * p.own_table_stride : p.page_table + (size_t)it.seq * p.table_stride;
+}
+__device__ __forceinline__ int pages_of(const RowsParams& p, const RowsItem& it) {
+    const int n = (it.Lk + kTile - 1) / kTile;
+    return it.own ? n : min(n, p.max_pages);
+}
+
 // A piece of work as the copy warp hands it to the others.
 struct Work {
     int valid;  // 0: there is no more
     RowsItem it;
-    int h, split;
-    int nb[2];  // blocks of keys of each pipeline
+    int h;
+    int c0, c1;  // its keys [c0, c1)
+    int rec;     // its record
+    int nb[2];   // blocks of keys of each pipeline
 };
 
 // 32 bytes to global memory: whole sectors from one thread.  `wide`: the
@@ -331,8 +367,7 @@ __device__ __forceinline__ void store32(void* at, const uint32_t* x, bool wide) 
 // piece run while the softmax warpgroups write the last one's results.
 template <int D, bool PAGED, bool DUAL>
 __global__ void __launch_bounds__(kThreads, 1)
-rows_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
-            const __grid_constant__ CUtensorMap tmv, const RowsParams p) {
+rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
     using Geo = RowsGeo<D, DUAL>;
     constexpr int TILES = Geo::TILES, STAGES = Geo::STAGES, RING = Geo::RING, BOXES = Geo::BOXES, BOX = Geo::BOX, TILE = Geo::TILE;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -352,6 +387,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUt
     uint64_t* drained = next_full + 1;
     unsigned char* answer = reinterpret_cast<unsigned char*>(drained + 3);  // 16 bytes
     Work* work = reinterpret_cast<Work*>(answer + 16);                      // [2]
+    static_assert(sizeof(Work) <= 64, "room for two pieces of work");
     uint32_t* tmem_at = reinterpret_cast<uint32_t*>(work + 2);
     float* join = reinterpret_cast<float*>(tmem_at + 4);  // [2][128] what the pipelines tell each other (single)
 
@@ -392,23 +428,26 @@ rows_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUt
             int id = blockIdx.x;
             for (int asked = 0; ok; ++asked) {
                 Work w;
-                int c0 = 0;  // first key of the chunk
                 w.valid = id >= 0;
                 bool some = !w.valid;
                 if (w.valid) {
-                    w.h = id % p.Hkv;
-                    const int rest = id / p.Hkv;
-                    w.split = rest % p.splits;
-                    w.it = find_item(p, p.tiles - 1 - rest / p.splits, TILES * p.tok);
+                    const bool own = !DUAL && id >= p.shared_work;
+                    const int at = own ? id - p.shared_work : id;
+                    const int rest = at / p.Hkv, splits = own ? p.own_splits : p.splits;
+                    const int chunk = own ? p.own_chunk : p.chunk, split = rest % splits;
+                    w.h = at % p.Hkv;
+                    w.it = own ? own_item(p, rest / splits) : find_item(p, p.tiles - 1 - rest / splits, TILES * p.tok);
                     some = w.it.t0 >= 0 && w.it.t0 < w.it.Lq;
-                    c0 = w.split * p.chunk;
+                    w.c0 = split * chunk;
+                    w.c1 = min(w.it.Lk, w.c0 + chunk);
+                    w.rec = (own ? p.own_rec0 : p.rec0) + split;
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const int first = w.it.t0 + (DUAL ? i : 0) * p.tok;
                         const int ntok = min(p.tok, w.it.Lq - first);
-                        int most = w.it.Lk;
+                        int most = w.c1;
                         if (p.causal) most = min(most, w.it.Lk - w.it.Lq + first + ntok);
-                        most = min(most, c0 + p.chunk) - c0;
+                        most -= w.c0;
                         w.nb[i] = ntok > 0 && most > 0 ? (most + kBlock - 1) / kBlock : 0;
                     }
                 }
@@ -429,22 +468,23 @@ rows_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUt
                         if (!ok) break;
                         ++qn;
                         if (lane == 0) {
-                            const uint32_t qbytes = (uint32_t)(p.tok * p.G * D * 2);
+                            const uint32_t qbytes = (uint32_t)((w.it.own ? 1 : p.tok) * p.G * D * 2);
+                            const void* map = w.it.own ? static_cast<const void*>(&maps.own_q) : &maps.q;
                             const int qtiles = DUAL && w.nb[1] > 0 ? 2 : 1;
                             mbar_arrive_expect_tx(q_full, qbytes * qtiles);
                             for (int i = 0; i < qtiles; ++i)
                                 for (int bx = 0; bx < BOXES; ++bx)
-                                    tma_load_3d(sq + i * TILE + bx * BOX, &tmq, 64 * bx, w.h * p.G,
+                                    tma_load_3d(sq + i * TILE + bx * BOX, map, 64 * bx, w.h * p.G,
                                                 w.it.q0 + w.it.t0 + i * p.tok, q_full);
                         }
                         // Page ids by the warp, 32 pages a register: the windows of 16 blocks alternate
                         // between two of them, the next one fetched when the keys are 4 blocks into the
                         // current one (the values are at most 2 blocks behind).
                         int window[2] = {-1, -1};
+                        const int pages = PAGED ? pages_of(p, w.it) : 0;
                         auto fetch = [&](int win) {
-                            const int pi = c0 / kTile + 32 * win + lane;
-                            const bool in = pi * kTile < w.it.Lk && pi < p.max_pages;
-                            return in ? p.page_table[(size_t)w.it.seq * p.table_stride + pi] : -1;
+                            const int pi = w.c0 / kTile + 32 * win + lane;
+                            return pi < pages ? table_of(p, w.it)[pi] : -1;
                         };
                         auto page = [&](int rel) {  // of page `rel` of the chunk
                             return __shfl_sync(0xffffffffu, rel & 32 ? window[1] : window[0], rel & 31);
@@ -468,9 +508,9 @@ rows_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUt
                             if (!ok) return;
                             // (fault injection: that key tile gets no copy and no arrival)
                             if (lane == 0 && (which || j != p.withhold_tile)) {
-                                const void* map = which ? static_cast<const void*>(&tmv) : static_cast<const void*>(&tmk);
+                                const void* map = which ? static_cast<const void*>(&maps.v) : &maps.k;
                                 unsigned char* dst = ring + s * TILE;
-                                const int at = c0 + j * kBlock;
+                                const int at = w.c0 + j * kBlock;
                                 mbar_arrive_expect_tx(&full[s], TILE);
                                 if (PAGED) {
 #pragma unroll
@@ -484,9 +524,14 @@ rows_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUt
                                             tma_load_2d(dst + bx * BOX + half * (BOX / 2), map, 64 * bx, y, &full[s]);
                                     }
                                 } else {
+                                    int y = w.h;
+                                    if (w.it.own) {
+                                        map = which ? &maps.own_v : &maps.own_k;
+                                        y += w.it.seq * p.Hkv;
+                                    }
 #pragma unroll
                                     for (int bx = 0; bx < BOXES; ++bx)
-                                        tma_load_3d(dst + bx * BOX, map, 64 * bx, w.h, w.it.k0 + at, &full[s]);
+                                        tma_load_3d(dst + bx * BOX, map, 64 * bx, y, w.it.k0 + at, &full[s]);
                                 }
                             }
                             ++n;
@@ -566,7 +611,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUt
                 const Work& w = work[slot];
                 const bool valid = uniform(w.valid) != 0;
                 const int nb0 = (int)uniform(w.nb[0]), nb1 = (int)uniform(w.nb[1]);
-                const int left0 = w.it.Lk - w.split * p.chunk;  // keys of the sequence from the chunk on
+                const int left0 = w.it.Lk - w.c0;  // keys of the sequence from the chunk on
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&work_empty[slot]);
                 if (!valid) break;
@@ -643,18 +688,20 @@ rows_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUt
             if (DUAL ? !ok : named_barrier_or(2, 256, !ok)) break;
             const Work& wk = work[slot];
             const bool valid = wk.valid != 0;
-            const RowsItem it = wk.it;
-            const int h = wk.h, split = wk.split;
+            RowsItem it = wk.it;
+            if (DUAL) it.own = 0;  // known to be
+            const int h = wk.h, c0 = wk.c0, c1 = wk.c1, rec_at = wk.rec;
             const int nb = i ? wk.nb[1] : wk.nb[0];
             const int all = wk.nb[0];
             __syncwarp();
             if (lane == 0) mbar_arrive(&work_empty[slot]);
             if (!valid) break;
-            const int c0 = split * p.chunk;
             const int first = it.t0 + (DUAL ? i : 0) * p.tok;
             const bool live = tk < p.tok && first + tk < it.Lq;
-            const int lim = live ? min(visible_keys(p, it, first + tk), c0 + p.chunk) - c0 : 0;
+            const int lim = live ? min(visible_keys(p, it, first + tk), c1) - c0 : 0;
             const int rounds = DUAL ? nb : (nb + 1 - i) / 2;
+            const int32_t* table = PAGED ? table_of(p, it) : nullptr;
+            const int pages = PAGED ? pages_of(p, it) : 0;
             float m = -INFINITY;
             float2 l2 = make_float2(0.f, 0.f);
             for (int round = 0; round < rounds; ++round) {
@@ -665,8 +712,8 @@ rows_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUt
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         const int pi = (c0 + j * kBlock) / kTile + half;
-                        if (pi * kTile < it.Lk && pi < p.max_pages) {
-                            const int pg = p.page_table[(size_t)it.seq * p.table_stride + pi];
+                        if (pi < pages) {
+                            const int pg = table[pi];
                             bad[half] = pg < 0 || pg >= p.num_pages;
                         }
                     }
@@ -773,7 +820,7 @@ rows_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUt
             }
             const int head = h * p.G + r - tk * p.G;
             const size_t row = (size_t)(it.q0 + first + tk) * p.Hq + head;
-            const size_t rec = row * p.rec_stride + p.rec0 + split;
+            const size_t rec = row * p.rec_stride + rec_at;
             const bool in0 = DUAL ? i == 0 && rounds > 0 : all > 0, in1 = DUAL ? i == 1 && rounds > 0 : all > 1;
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
@@ -935,8 +982,7 @@ int rows_tok(int G) { return kRows / G; }
 bool rows_dual(int B, int total_q, int G) { return B > 0 && total_q / B > rows_tok(G); }
 
 template <int D, bool PAGED, bool DUAL>
-cudaError_t launch_kernel(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const RowsParams& p,
-                          dim3 grid, cudaStream_t stream) {
+cudaError_t launch_kernel(const RowsMaps& maps, const RowsParams& p, dim3 grid, cudaStream_t stream) {
     constexpr auto kernel = rows_kernel<D, PAGED, DUAL>;
     constexpr int SMEM = RowsGeo<D, DUAL>::SMEM;
     static bool done[64] = {};
@@ -953,10 +999,12 @@ cudaError_t launch_kernel(const CUtensorMap& q, const CUtensorMap& k, const CUte
         if (attr.numRegs * kThreads < 256 * kSoftmaxRegs + 128 * kOtherRegs) return cudaErrorInvalidConfiguration;
         if (dev < 64) done[dev] = true;
     }
-    return launch_pdl(kernel, grid, dim3(kThreads), SMEM, stream, q, k, v, p);
+    return launch_pdl(kernel, grid, dim3(kThreads), SMEM, stream, maps, p);
 }
 
 }  // namespace
+
+bool rows_single(int B, int total_q, int G) { return !rows_dual(B, total_q, G); }
 
 int rows_tokens(int B, int total_q, int G) { return rows_tok(G) * (rows_dual(B, total_q, G) ? 2 : 1); }
 
@@ -1000,36 +1048,56 @@ cudaError_t launch_rows(const RowsArgs& a, cudaStream_t stream) {
     const bool paged = a.page_table != nullptr;
     const uint64_t pool_rows = paged ? (uint64_t)a.num_pages * a.Hkv * kTile : 0;
     p.zero_row = (int)(pool_rows > 0 ? pool_rows : 1);
-    CUtensorMap tq, tk, tv;
-    if (!make_token_map(&tq, a.q, a.D, a.Hq, a.total_q, a.D, a.q_stride, p.G, p.tok)) return cudaErrorInvalidValue;
-    bool ok;
+    RowsMaps m;
+    if (!make_token_map(&m.q, a.q, a.D, a.Hq, a.total_q, a.D, a.q_stride, p.G, p.tok)) return cudaErrorInvalidValue;
+    bool ok = true;
     if (paged && pool_rows > 0) {
-        ok = make_row_map(&tk, a.k, pool_rows, (uint32_t)a.D * 2) && make_row_map(&tv, a.v, pool_rows, (uint32_t)a.D * 2);
+        ok = make_row_map(&m.k, a.k, pool_rows, (uint32_t)a.D * 2) && make_row_map(&m.v, a.v, pool_rows, (uint32_t)a.D * 2);
     } else if (paged) {  // an empty pool: nothing is read, any well-formed map will do
-        ok = make_row_map(&tk, a.q, 1, (uint32_t)a.D * 2) && make_row_map(&tv, a.q, 1, (uint32_t)a.D * 2);
+        ok = make_row_map(&m.k, a.q, 1, (uint32_t)a.D * 2);
+        m.v = m.k;
     } else if (a.total_k > 0) {
-        ok = make_token_map(&tk, a.k, a.D, a.Hkv, a.total_k, a.k_head_stride, a.k_stride, 1, kBlock) &&
-             make_token_map(&tv, a.v, a.D, a.Hkv, a.total_k, a.v_head_stride, a.v_stride, 1, kBlock);
+        ok = make_token_map(&m.k, a.k, a.D, a.Hkv, a.total_k, a.k_head_stride, a.k_stride, 1, kBlock) &&
+             make_token_map(&m.v, a.v, a.D, a.Hkv, a.total_k, a.v_head_stride, a.v_stride, 1, kBlock);
     } else {
-        tk = tv = tq;
-        ok = true;
+        m.k = m.v = m.q;
+    }
+    m.own_q = m.own_k = m.own_v = m.q;
+    const bool dual = rows_dual(a.B, a.total_q, p.G);
+    const long long own_work = a.own_max > 0 ? (long long)a.total_q * a.Hkv * a.own_splits : 0;
+    if (own_work > 0) {
+        if (dual) return cudaErrorInvalidValue;
+        ok = ok && make_token_map(&m.own_q, a.q, a.D, a.Hq, a.total_q, a.D, a.q_stride, p.G, 1);
+        if (!paged) {
+            const long long head = (long long)a.own_max * a.D;
+            ok = ok && make_token_map(&m.own_k, a.own_k, a.D, a.total_q * a.Hkv, a.own_max, head, a.D, 1, kBlock) &&
+                 make_token_map(&m.own_v, a.own_v, a.D, a.total_q * a.Hkv, a.own_max, head, a.D, 1, kBlock);
+        }
     }
     if (!ok) return cudaErrorInvalidValue;
+    p.own_lens = a.own_lens;
+    p.own_table = a.own_table;
+    p.own_table_stride = a.own_table_stride;
+    p.own_max = a.own_max;
+    p.own_skip = a.own_skip;
+    p.own_splits = a.own_splits;
+    p.own_chunk = a.own_chunk;
+    p.own_rec0 = a.own_rec0;
     const long long tiles = rows_tiles(a.B, a.total_q, p.G, a.cu_q != nullptr);
     p.tiles = (int)tiles;
     injected_timeout(&p.wait_limit_ns, &p.withhold_tile);
-    const dim3 grid((unsigned)(tiles * a.Hkv * a.splits));
-    const bool dual = rows_dual(a.B, a.total_q, p.G);
+    p.shared_work = (int)(tiles * a.Hkv * a.splits);
+    const dim3 grid((unsigned)(p.shared_work + own_work));
     if (a.D == 128) {
-        if (paged) return dual ? launch_kernel<128, true, true>(tq, tk, tv, p, grid, stream)
-                               : launch_kernel<128, true, false>(tq, tk, tv, p, grid, stream);
-        return dual ? launch_kernel<128, false, true>(tq, tk, tv, p, grid, stream)
-                    : launch_kernel<128, false, false>(tq, tk, tv, p, grid, stream);
+        if (paged) return dual ? launch_kernel<128, true, true>(m, p, grid, stream)
+                               : launch_kernel<128, true, false>(m, p, grid, stream);
+        return dual ? launch_kernel<128, false, true>(m, p, grid, stream)
+                    : launch_kernel<128, false, false>(m, p, grid, stream);
     }
-    if (paged) return dual ? launch_kernel<64, true, true>(tq, tk, tv, p, grid, stream)
-                           : launch_kernel<64, true, false>(tq, tk, tv, p, grid, stream);
-    return dual ? launch_kernel<64, false, true>(tq, tk, tv, p, grid, stream)
-                : launch_kernel<64, false, false>(tq, tk, tv, p, grid, stream);
+    if (paged) return dual ? launch_kernel<64, true, true>(m, p, grid, stream)
+                           : launch_kernel<64, true, false>(m, p, grid, stream);
+    return dual ? launch_kernel<64, false, true>(m, p, grid, stream)
+                : launch_kernel<64, false, false>(m, p, grid, stream);
 }
 
 cudaError_t launch_merge_list(const float* part_o, const float* part_ml, const int32_t* cu, int B, int tokens, int Hq,

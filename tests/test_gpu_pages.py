@@ -46,7 +46,8 @@ def problem(B, ctx, most, seed, wide=None, spare=5):
 
 
 @pytest.mark.parametrize("B,ctx,most", [(1, 0, 1), (1, 0, 300), (3, 200, 130), (70, 500, 1), (256, 3000, 1),
-                                        (1023, 100, 70), (1025, 100, 3), (2500, 90, 20), (40, 1000, 3000)])
+                                        (1023, 100, 70), (1025, 100, 3), (2500, 90, 20), (40, 1000, 3000), (1030, 70, 601),
+                                        (3100, 10, 3)])
 @pytest.mark.parametrize("pad", [0, 37])
 def test_assign(fd, B, ctx, most, pad):
     cached, new, table, free = problem(B, ctx, most, seed=B + most)
@@ -73,6 +74,20 @@ def test_assign_in_place_over_steps(fd):
         table, cached = want[0], want[1]
         assert slots.tolist() == want[3] and lens.tolist() == cached and head.tolist() == [want[4]]
     assert t.tolist() == table
+
+
+@pytest.mark.parametrize("B,ctx,most", [(300, 100, 200), (1500, 50, 30), (3, 4000, 9000), (2100, 0, 9)])
+def test_assign_in_place_with_many_tokens(fd, B, ctx, most):
+    # beyond what one block does alone: a cluster for the table, the whole GPU for the slots
+    cached, new, table, free = problem(B, ctx, most, seed=B, spare=9)
+    total = sum(new) + 13
+    want = assign_plain(table, cached, new, free, 0, total)
+    t, lens, head = ints(table), ints(cached), ints([0])
+    _, cu, slots, _ = fd.fd_assign_pages(t, lens, ints(new), ints(free), total, free_head=head, seq_lens=lens,
+                                         free_head_out=head)
+    assert t.tolist() == want[0] and lens.tolist() == want[1] and cu.tolist() == want[2]
+    assert slots.tolist() == want[3] and head.tolist() == [want[4]]
+    assert fd.fd_device_status(clear=True) == fd.FD_OK
 
 
 def test_assign_nothing(fd):
