@@ -262,8 +262,9 @@ __global__ void __launch_bounds__(256) slots_kernel(const AssignParams p) {
                 if (page >= 0) out[e] = (int64_t)page * kTile + pos % kTile;
             }
         }
-        if (run + i + 1 < p.total_new) *reinterpret_cast<longlong2*>(p.slots + run + i) = make_longlong2(out[0], out[1]);
-        else if (run + i < p.total_new) p.slots[run + i] = out[0];
+        int64_t* to = p.slots + run + i;
+        if (run + i + 1 < p.total_new) *reinterpret_cast<longlong2*>(to) = make_longlong2(out[0], out[1]);
+        else if (run + i < p.total_new) *to = out[0];
     }
 }
 
@@ -299,7 +300,8 @@ __device__ __forceinline__ long long pool_row(const AppendParams& p, long long s
 
 // A thread per 16 bytes of K and of V.  The rows are loaded beside the slot,
 // not after it: waiting for the slot first is a second memory latency for the
-// same bytes in flight.
+// same bytes in flight (31K tokens x 8 heads x 128: 41.2 us that way, 38.9 us
+// this way, 6.6 TB/s of HBM; a decode step of 256 tokens 1.6 us).
 template <int D>
 __global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
     constexpr int C = D / 8;  // 16-byte chunks of a row
@@ -380,6 +382,8 @@ __device__ __forceinline__ void load16(uint32_t (&w)[8], const uint16_t* x) {
     w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
 }
 
+// HBM bounds it: 31K tokens x 8 heads x 128 in 29.8 us, 6.5 TB/s (35.5 us with the
+// rows loaded after their slots).
 template <int D>
 __global__ void __launch_bounds__(256) append_fp8_kernel(const AppendParams p) {
     constexpr int C = D / 16;
@@ -411,15 +415,21 @@ unsigned append_grid(long long n) { return (unsigned)((n + 255) / 256); }
 
 }  // namespace
 
-// In place, assign_kernel writes the slots itself up to this many new tokens (a
-// round of its block per 2048); more go to slots_kernel on the whole GPU.
-constexpr int kSlotsHere = 8192;
-// In place, a cluster of eight CTAs shares out the new pages from this bound on them.
-constexpr int kPagesAlone = 2048;
-// Otherwise a CTA per so many tokens and pages, up to one per SM: 512 prompts
-// with a million new tokens take 9.3 us in one launch, 11.1 us in the two of a call in
-// place.
-constexpr int kPerCta = 4096;
+// In place, assign_kernel writes the slots itself up to kSlotsHere new tokens; more
+// go to slots_kernel on the whole GPU (32768 tokens: 7.1 us here, 8.0 us there; 131072:
+// 14.2 and 8.4 us).
+constexpr int kSlotsHere = 32768;
+// In place, a cluster of eight CTAs shares out more new pages than kPagesAlone and
+// more slots than kSlotsAlone, a single CTA writes fewer (256 tokens: 5.5 us with
+// eight, 4.7 us alone; 4096: 5.9 and 6.7 us; 4096 pages: 9.3 and 11.2 us, 16384: 11.5
+// and 22.6 us).
+constexpr int kPagesAlone = 2048, kSlotsAlone = 2048;
+// Otherwise a CTA per so many tokens and pages, a thread each, up to one CTA per SM
+// (131072 tokens: 4.0 us, 5.6 us with 4096 and 4.0 us with 512 per CTA).  512 prompts
+// with a million new tokens take 9.0 us, 11.5 us in the two launches of a call in place;
+// their 8.8 MB would pass HBM in 1.3 us, a launch and the chain length -> sums ->
+// search -> page -> store of dependent accesses is what the rest goes to.
+constexpr int kPerCta = 1024;
 
 cudaError_t launch_assign(const AssignArgs& a, cudaStream_t stream) {
     AssignParams p{a.cached_lens, a.new_lens, a.B, a.page_table, a.max_pages, a.free_pages, a.num_free, a.free_head,
@@ -430,7 +440,7 @@ cudaError_t launch_assign(const AssignArgs& a, cudaStream_t stream) {
     const long long pages = (long long)a.total_new / kTile + a.B;
     unsigned parts = 1;
     if (p.in_place) {
-        if (pages > kPagesAlone) parts = 8;
+        if (pages > kPagesAlone || (p.slots_here && a.total_new > kSlotsAlone)) parts = 8;
     } else {
         int dev = 0, sms = 0;
         cudaError_t e = cudaGetDevice(&dev);
