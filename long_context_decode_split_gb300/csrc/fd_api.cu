@@ -390,18 +390,45 @@ int check_rows(int B, int total_q, int Hq, int Hkv, int max_k, int d, int num_sp
     return FD_OK;
 }
 
-// Prompts: one chunk while the tiles fill the SMs twice, else enough chunks for
-// about four CTAs per SM (the sequences' lengths are not known here), each of
-// at least 512 keys.
+// Prompts: the kernel cuts what each tile attends into `splits` equal parts of at
+// least `chunk` keys (the lengths are on the device).  One part while the tiles
+// fill the SMs twice, else the count with the least of
+//   E  every sequence max_k keys long: rounds of the SMs times a piece (c blocks
+//      take about c + 6 blocks of time)
+//   R  (more than one sequence) lengths from a quarter of max_k up: the work shared
+//      out evenly and half of the longest piece behind it
+// plus the records' way to memory and back and the merge.  max_k may be no more
+// than the room of a table, so that 32K keys stand for all beyond.  With 32 query
+// and 8 KV heads of 128: 2048 tokens alone 36 us in one part, 86 us in two; 512
+// tokens behind 8192 cached ones 97 us in one, 65 us in two, 84 us in three; 2 x 64
+// behind 32K 344 us in one, 65 us in nine, 79 us in sixteen; 16 x 8 behind 16K to 64K
+// 464 us in one, 348 us in three, 338 us in seven, 359 us in sixteen.
 RowsPlan prefill_plan(int B, int total_q, int Hq, int Hkv, int max_k, int num_splits) {
-    if (num_splits > 0) return rows_chunks(max_k, num_splits, true);
-    const int sms = current_sm_count(), per = fd::rows_tokens(B, total_q, Hq / Hkv);
+    RowsPlan pl;
+    pl.splits = num_splits > 0 ? num_splits : 1;
+    pl.chunk = num_splits > 0 ? 128 : 512;
+    const int sms = num_splits > 0 ? 0 : current_sm_count(), per = fd::rows_tokens(B, total_q, Hq / Hkv);
     const long long mean = B > 0 ? (total_q + B - 1) / B : 0;  // tokens of a sequence
     const long long ctas = (long long)B * ((mean + per - 1) / per) * Hkv;
-    long long want = 1;
-    if (sms > 0 && ctas > 0 && ctas < 2LL * sms) want = 4LL * sms / ctas;
-    if (want > max_k / 512) want = max_k / 512;
-    return rows_chunks(max_k, want < 1 ? 1 : want, false);
+    if (sms <= 0 || ctas <= 0 || ctas >= 2LL * sms) return pl;
+    const double kPiece = 6.0, kMerge = 4.0, kRecords = 1.6e-4;  // in blocks of time
+    const double blocks = std::min(max_k, 1 << 15) / 128.0;
+    const long long most = std::min((long long)max_k / pl.chunk, 8LL * sms / ctas + 1);
+    double best = 1e300;
+    for (long long S = 1; S == 1 || S <= most; ++S) {
+        const double c = std::max(blocks / (double)S, 1.0), pieces = (double)(ctas * S);
+        double cost = std::ceil(pieces / sms) * (c + kPiece);
+        if (B > 1) {
+            const double mean_piece = 0.625 * c + kPiece, longest = c + kPiece;
+            cost = 0.5 * (cost + std::max(pieces * mean_piece / sms + 0.5 * longest, longest));
+        }
+        if (S > 1) cost += kMerge + kRecords * (double)S * (double)total_q * Hq;
+        if (cost < best) {
+            best = cost;
+            pl.splits = (int)S;
+        }
+    }
+    return pl;
 }
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -465,7 +492,8 @@ SharedPlan shared_plan_uncached(int B, int Hq, int Hkv, int prefix_len, int L_ow
     SharedPlan s;
     s.together = fd::rows_single(1, B, Hq / Hkv);
     const int blocks = (L_own + 127) / 128;
-    // own tokens in pieces of up to 16 blocks, 16 pieces at most
+    // own tokens in pieces of up to 16 blocks, 16 pieces at most (32 sequences, 8 KV heads,
+    // up to 4096 own tokens behind 32K: 82 us, 87 us with 8 blocks, 95 us with 32)
     s.own_rows = rows_chunks(L_own, blocks <= 16 ? 1 : blocks < 256 ? (blocks + 15) / 16 : 16, false);
     // one chunk each while the sequences fill the SMs and are short (128 sequences
     // of up to 1024 own tokens, 8 KV heads: 46.5 us, 60.5 us in the decode's

@@ -156,7 +156,7 @@ struct RowsArgs {
     int max_k;                // bound on Lk
     float scale;
     int causal;
-    int splits, chunk;        // chunks of `chunk` keys (a multiple of 128); splits == 1: all keys
+    int splits, chunk;        // equal parts of a tile's keys, of at least `chunk` (both multiples of 128)
     void* out;                // splits == 1: [total_q, Hq, D] and lse [total_q, Hq] or null
     int out_bf16;
     float* lse;
@@ -164,8 +164,7 @@ struct RowsArgs {
     float* part_ml;           // and [total_q, Hq, rec_stride, 2]
     int rec0, rec_stride;     // (every record of a query row is written, empty ones with m = -inf)
     int direct;               // write out/lse instead of records
-    // Own tokens of a shared-prefix decode, beside a single tile's work (own_work(..)
-    // > 0): query token b also attends own_lens[b] - own_skip tokens of its own, in
+    // Own tokens of a shared-prefix decode, beside the work of single tiles: query token b also attends own_lens[b] - own_skip tokens of its own, in
     // chunks written to the records own_rec0 + chunk.
     const void* own_k;        // contiguous [total_q, Hkv, own_max, D]; paged: the pools above
     const void* own_v;

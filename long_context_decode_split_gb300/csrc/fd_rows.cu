@@ -1,14 +1,16 @@
 // fd_rows.cu -- attention of packed query rows for sm_103a: whole prompts,
-// prompt tails over a paged cache, and the shared part of a shared-prefix
-// decode.  A tile holds TOK consecutive query tokens of one sequence times the
-// G query heads of one KV head (row = token * G + head), so every key and
-// value read serves the whole group.
+// prompt tails over a paged cache, and the decode of a batch with a shared
+// prefix.  A tile holds consecutive query tokens of one sequence times the G
+// query heads of one KV head (row = token * G + head, 128 / G tokens), so every
+// key and value read serves the whole group.
 //
 // For a row with the visible keys [0, n):
 //   s_j = scale <q, k_j>,  out = sum_j e^(s_j) v_j / sum_j e^(s_j),
 //   lse = ln sum_j e^(s_j)
 // in one pass over the keys: m is the running maximum, l the running sum of
-// 2^(s_j log2e - m), and O is rescaled when m moves.
+// 2^(s_j log2e - m), and O is rescaled when m moves.  Scores, m, l and O are
+// binary32; the weights are rounded to bf16 (2^-8 relative at most) for the
+// product with V, whose operands have one type, and l takes them unrounded.
 #include <cmath>
 
 #include "fd_device.cuh"
@@ -75,9 +77,10 @@ __device__ __forceinline__ int checked(int c, int lo, int hi) {
     return c;
 }
 
-// All lanes of a warp together.  Tile slots: sequence s owns the slots floor(cu_q[s] / per) + s up to those of
-// s + 1, at least as many as the tiles it has (`per` tokens each), so a slot's
-// sequence is found by a search of cu_q alone.
+// All lanes of a warp together.  Tile slots: sequence s owns the slots from
+// floor(cu_q[s] / per) + s up to those of s + 1, at least as many as the tiles it
+// has (`per` tokens each), so a slot's sequence is found by a search of cu_q
+// alone.
 __device__ __forceinline__ RowsItem find_item(const RowsParams& p, int slot, int per) {
     int lo = 0;
     if (p.cu_q) {
@@ -351,7 +354,7 @@ __device__ __forceinline__ void store32(void* at, const uint32_t* x, bool wide) 
 //
 // S = Q K^T and O += P V run on tcgen05 with S, P and O in tensor memory.  Two
 // pipelines (i = 0, 1) alternate on the tensor cores: while the softmax
-// warpgroup of one turns its S into P, the MMA warp runs the other's products.
+// warpgroup of one turns its S into P, the other's products run.
 //   DUAL    the two pipelines hold two tiles of query rows and share every
 //           block of keys and values
 //   single  both hold the same tile and take the even and the odd blocks; their
@@ -363,13 +366,37 @@ __device__ __forceinline__ void store32(void* at, const uint32_t* x, bool wide) 
 // Keys and values pass through rings of 128-row tiles (K V K V ..).
 //
 // A CTA goes from one piece of work to the next without a stop: the copy warp
-// is ahead with the next queries and keys, and the first products of the next
-// piece run while the softmax warpgroups write the last one's results.
+// is ahead with the next queries and keys, and the next piece's first products
+// run while the softmax warpgroups write the last one's results.  Pieces come in
+// the order of (tile, KV head): the SMs that run at the same time then read the
+// same keys of a sequence from L2 (longest tiles first, across sequences: ragged
+// prompts 6% slower; one head after the other: prompt tails 19% slower).
+//
+// What bounds it, and what each choice brought (32 query heads, 8 KV heads,
+// d = 128):
+//   * long prompts: the tensor cores at the power limit.  32K tokens take
+//     5.2-5.4 ms in a loop (1.63-1.69 PFLOP/s of the causal products; a bf16
+//     matrix product in a loop reaches 1.72) and 4.8-4.9 ms in a short run
+//     (1.78-1.84; 1.97).  64 cycles an MMA of the 128 x 128 x 16 shape.
+//   * an MMA is taken about when it starts to run, so whatever the issuing warp
+//     does in between leaves the tensor cores idle: operands that the compiler
+//     knows to be uniform, 1463 -> 1651 TFLOP/s; a warp per pipeline, whose waits
+//     and commits run beside the other's products, 1679 -> 1780.
+//   * a block's softmax is about 1100 cycles (60 to read S, 280 maximum, 690
+//     weights, 40 to store P) beside 2 x 1024 of products.  Handing P over in
+//     halves, three-operand maxima, a last block cut to its keys and a warpgroup
+//     of its own for the output all measured slower or the same.
+//   * short prompts pay about 5 us a piece of work for filling and draining the
+//     pipelines (ragged prompts of 257 to 6143 tokens: 1.05-1.1 ms, 1.4-1.47
+//     PFLOP/s).
+//   * few query rows (drafts, a shared prefix): HBM.  16 x 8 drafted tokens on
+//     16K-64K cached ones 328 us, 6.5 TB/s.
 template <int D, bool PAGED, bool DUAL>
 __global__ void __launch_bounds__(kThreads, 1)
 rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
     using Geo = RowsGeo<D, DUAL>;
-    constexpr int TILES = Geo::TILES, STAGES = Geo::STAGES, RING = Geo::RING, BOXES = Geo::BOXES, BOX = Geo::BOX, TILE = Geo::TILE;
+    constexpr int TILES = Geo::TILES, STAGES = Geo::STAGES, RING = Geo::RING;
+    constexpr int BOXES = Geo::BOXES, BOX = Geo::BOX, TILE = Geo::TILE;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     unsigned char* sq = smem;
@@ -411,6 +438,11 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
         fence_barrier_init();
     }
     if (warp == kMmaWarp) tmem_alloc(tmem_at, 512);
+    if (warp == kCopyWarp && lane == 0) {
+        prefetch_tmap(&maps.q);
+        prefetch_tmap(&maps.k);
+        prefetch_tmap(&maps.v);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -434,10 +466,17 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
                     const bool own = !DUAL && id >= p.shared_work;
                     const int at = own ? id - p.shared_work : id;
                     const int rest = at / p.Hkv, splits = own ? p.own_splits : p.splits;
-                    const int chunk = own ? p.own_chunk : p.chunk, split = rest % splits;
+                    const int split = rest % splits;
                     w.h = at % p.Hkv;
                     w.it = own ? own_item(p, rest / splits) : find_item(p, p.tiles - 1 - rest / splits, TILES * p.tok);
                     some = w.it.t0 >= 0 && w.it.t0 < w.it.Lq;
+                    int chunk = p.own_chunk;
+                    if (!own) {  // equal parts of what the tiles see
+                        int seen = w.it.Lk;
+                        if (p.causal) seen -= w.it.Lq - min(w.it.Lq, w.it.t0 + TILES * p.tok);
+                        const int blocks = (max(seen, 0) + kBlock - 1) / kBlock;
+                        chunk = max(p.chunk, (blocks + splits - 1) / splits * kBlock);
+                    }
                     w.c0 = split * chunk;
                     w.c1 = min(w.it.Lk, w.c0 + chunk);
                     w.rec = (own ? p.own_rec0 : p.rec0) + split;
@@ -558,7 +597,8 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
                 // the others stopped early: let the copies in flight land before the CTA ends
                 if (lane == 0) atomicOr(&g_status_rows, kStatusTimeout);
                 if (qn > 0) mbar_wait(q_full, (uint32_t)(qn - 1) & 1u, p.wait_limit_ns);
-                for (int u = max(0, n0 - RING); u < n0; ++u) mbar_wait(&full[u % RING], (uint32_t)(u / RING) & 1u, p.wait_limit_ns);
+                for (int u = max(0, n0 - RING); u < n0; ++u)
+                    mbar_wait(&full[u % RING], (uint32_t)(u / RING) & 1u, p.wait_limit_ns);
                 for (int u = max(0, n1 - RING); u < n1; ++u)
                     mbar_wait(&full[RING + u % RING], (uint32_t)(u / RING) & 1u, p.wait_limit_ns);
                 mbar_wait(next_full, 0, p.wait_limit_ns);
@@ -621,7 +661,8 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
                 const int nb = DUAL ? (i ? nb1 : nb0) : (blocks + 1 - (int)i) / 2;
                 const int in_ring = DUAL ? blocks : nb;
                 // Value rows past the sequence may hold anything; their weight is 0, but 0 * NaN is NaN.
-                // (Both warps of a shared tile clear them, each before its own products.)
+                // (Both warps of a shared tile clear them, each before its own products: the second
+                // stores zeros over zeros, before the tile is released.)
                 auto clear_tail = [&](int j, uint32_t stage) {
                     const int rows = left0 - j * kBlock;
                     if (rows >= kBlock) return;
@@ -801,7 +842,8 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
                     join[r] = m;
                     join[128 + r] = l;
                 }
-                named_barrier(1, 256);
+                tc_fence_before();
+                named_barrier(1, 256);  // (both O are complete: each warpgroup has waited for its own)
                 if (i == 0) {
                     const float m1 = join[r], l1 = join[128 + r], m0 = m;
                     m = fmaxf(m0, m1);
@@ -813,6 +855,7 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
                     join[128 + r] = f1 *= inv;
                 }
                 named_barrier(1, 256);
+                tc_fence_after();
                 if (i == 1) {
                     f0 = join[r];
                     f1 = join[128 + r];
@@ -883,6 +926,8 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
 // nothing was attended): out = sum_i w_i O_i / sum_i w_i, w_i = 2^(m_i - M) l_i.
 // W warps per row (1: eight rows per CTA; 8: one row, the warps taking every
 // eighth record and joining through shared memory), eight records in flight.
+// The records come from L2, and the length of the list bounds it: 10 us of a
+// shared prefix of 128 sequences.
 template <int D, int W>
 __global__ void __launch_bounds__(256)
 merge_list_kernel(const float* __restrict__ part_o, const float* __restrict__ part_ml, const int32_t* __restrict__ cu,
@@ -978,7 +1023,9 @@ merge_list_kernel(const float* __restrict__ part_o, const float* __restrict__ pa
 
 int rows_tok(int G) { return kRows / G; }
 
-// Two tiles per CTA when the sequences fill more than one on average.
+// Two tiles per CTA when the sequences fill more than one on average (64 x 128 tokens
+// behind 2048: 217 us in two, 294 us in one; 64 x 24: 126 and 107 us; between one tile and two
+// within 5% of each other, with nothing cached two are up to 30% faster).
 bool rows_dual(int B, int total_q, int G) { return B > 0 && total_q / B > rows_tok(G); }
 
 template <int D, bool PAGED, bool DUAL>
@@ -1103,7 +1150,9 @@ cudaError_t launch_rows(const RowsArgs& a, cudaStream_t stream) {
 cudaError_t launch_merge_list(const float* part_o, const float* part_ml, const int32_t* cu, int B, int tokens, int Hq,
                               int D, int n, void* out, int out_bf16, float* lse, cudaStream_t stream) {
     const long long rows = (long long)tokens * Hq;
-    // few rows with long lists leave most of the GPU idle with a warp each
+    // few rows with long lists leave most of the GPU idle with a warp each (the whole
+    // call, 512 rows: 40 records 31.3 us with a warp each, 23.9 us with eight, 12 records
+    // 23.3 and 24.7 us; 8192 rows of 20 records 231 and 244 us)
     const bool wide = n > 16 && rows < 4096;
     const dim3 grid((unsigned)(wide ? rows : (rows + 7) / 8));
     const auto kernel = D == 128 ? (wide ? merge_list_kernel<128, 8> : merge_list_kernel<128, 1>)
