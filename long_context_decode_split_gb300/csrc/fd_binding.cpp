@@ -2,7 +2,7 @@
 // prefix, page and append calls: the checks of their tensors, the allocation of
 // outputs and workspace on the stream that uses them, and the call of the C
 // entry point.  The same steps in Python cost 12-15 us a call beside 2-6 us of
-// GPU time (a decode step's page assignment: 18.9 us a call in Python, 7.4 us
+// GPU time (a decode step's page assignment: 18.9 us a call in Python, 6.4 us
 // here; four short prompts: 19.8 and 5.2 us).  libfd.so itself stays free of
 // torch: this module opens it at run time.
 #include <torch/csrc/Exceptions.h>
@@ -10,6 +10,7 @@
 #include <torch/csrc/utils/object_ptr.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
@@ -162,6 +163,11 @@ c10::Device first_device(PyObject* o, const char* call) {
     return THPVariable_Unpack(o).device();
 }
 
+// On the current stream, like at::empty, without its way through the dispatcher.
+Tensor fresh_tensor(at::IntArrayRef sizes, at::ScalarType type, c10::Device dev) {
+    return Tensor(at::detail::empty_cuda(sizes, type, dev, std::nullopt));
+}
+
 struct Outputs {
     Tensor out, lse;  // lse may be undefined: none wanted
     int code;
@@ -169,10 +175,10 @@ struct Outputs {
     Outputs(int64_t T, int64_t Hq, int64_t d, PyObject* o, PyObject* l, int out_code, bool want_lse, c10::Device dev)
         : code(out_code) {
         const at::ScalarType type = out_code == FD_OUT_BF16 ? at::kBFloat16 : at::kFloat;
-        if (o == Py_None) out = at::empty({T, Hq, d}, at::TensorOptions().dtype(type).device(dev));
+        if (o == Py_None) out = fresh_tensor({T, Hq, d}, type, dev);
         else out = check(tensor(o, "out"), "out", dev, type, {{T, Hq, d}});
         if (l != Py_None) lse = check(tensor(l, "lse"), "lse", dev, at::kFloat, {{T, Hq}});
-        else if (want_lse) lse = at::empty({T, Hq}, at::TensorOptions().dtype(at::kFloat).device(dev));
+        else if (want_lse) lse = fresh_tensor({T, Hq}, at::kFloat, dev);
     }
     float* lse_data() const { return lse.defined() ? lse.mutable_data_ptr<float>() : nullptr; }
 };
@@ -186,7 +192,7 @@ struct Workspace {
             TORCH_CHECK_VALUE(t.is_contiguous(), "workspace must be contiguous");
             TORCH_CHECK_VALUE((size_t)t.nbytes() >= bytes, "workspace too small");
         } else if (bytes > 0) {
-            t = at::empty({(int64_t)bytes}, at::TensorOptions().dtype(at::kByte).device(dev));
+            t = fresh_tensor({(int64_t)bytes}, at::kByte, dev);
         }
     }
     void* data() const { return t.defined() ? t.mutable_data_ptr() : nullptr; }
@@ -367,7 +373,7 @@ PyObject* dense_shared_prefix(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 Tensor ints_out(PyObject* o, const char* name, int64_t n, c10::Device dev) {
-    if (o == Py_None) return at::empty({n}, at::TensorOptions().dtype(at::kInt).device(dev));
+    if (o == Py_None) return fresh_tensor({n}, at::kInt, dev);
     return check(tensor(o, name), name, dev, at::kInt, {{n}});
 }
 
@@ -392,7 +398,7 @@ PyObject* assign_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
         head = check(tensor(a[5], "free_head"), "free_head", dev, at::kInt, {{(int64_t)1}}).const_data_ptr<int>();
     const int page = integer(a[6], "page_size");
     const Tensor lens = ints_out(a[7], "seq_lens", B, dev), cu = ints_out(a[8], "cu_seqlens", (int64_t)B + 1, dev);
-    const Tensor slots = a[9] == Py_None ? at::empty({(int64_t)total}, at::TensorOptions().dtype(at::kLong).device(dev))
+    const Tensor slots = a[9] == Py_None ? fresh_tensor({(int64_t)total}, at::kLong, dev)
                                          : check(tensor(a[9], "slots"), "slots", dev, at::kLong, {{(int64_t)total}});
     const Tensor head_out = ints_out(a[10], "free_head_out", 1, dev);
     expect(lib.assign_pages(cached.const_data_ptr<int>(), fresh.const_data_ptr<int>(), B, table.mutable_data_ptr<int>(),
