@@ -392,8 +392,9 @@ FD_API int fd_decode_paged_fp4(const void* q, const uint8_t* k_pages, const uint
  *                device status (FD_ERR_INVALID_ARG).
  *   out          [total_q, Hq, d] in out_dtype; lse [total_q, Hq] float32 or
  *                NULL.  Rows that belong to no sequence are left as they are.
- *   num_splits   0 = planner; > 0: the keys are cut into that many chunks of
- *                ceil(max_k / num_splits) rounded up to 128, merged at the end
+ *   num_splits   0 = planner (fd_prefill_num_splits, from the sizes alone);
+ *                > 0: the keys that a tile of query tokens sees are cut into
+ *                that many equal parts (whole blocks of 128), merged at the end
  *   workspace    fd_prefill_workspace_size(...) bytes, may be NULL when 0
  * max_k is total_k for fd_prefill_packed and max_pages * 64 for
  * fd_prefill_paged. */
@@ -404,8 +405,9 @@ FD_API size_t fd_prefill_workspace_size(int B, int total_q, int Hq, int Hkv, int
  *   k, v         [total_k, Hkv, d] bf16
  *   cu_seqlens_k [B + 1] int32 (pass cu_seqlens_q for self-attention).
  * Keys of other sequences, and rows past cu_seqlens_k[B], never influence a
- * result, whatever they hold.  Keys hidden from a query by the causal mask
- * have to be finite (a weight of 0 times infinity is NaN). */
+ * result, whatever they hold.  Values hidden from a query by the causal mask
+ * have to be finite, like all values of its sequence (a weight of 0 times
+ * infinity is NaN); keys hidden from it may hold anything. */
 FD_API int fd_prefill_packed(const void* q, const void* k, const void* v,
                              long long q_stride, long long k_stride, long long v_stride,
                              const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,
@@ -430,9 +432,8 @@ FD_API int fd_prefill_paged(const void* q, const void* k_pages, const void* v_pa
 /* Decode of one token per sequence for a batch whose sequences start with the
  * same tokens: the shared keys and values are read once for the whole batch
  * (every query of the batch against them as one matrix product), each
- * sequence's own tokens by the split-KV pass, and all partial results are
- * joined exactly.  The result is that of fd_decode_paged / fd_decode_dense
- * over the whole sequences; weights of the shared part are bf16 (see the
+ * sequence's own tokens apart, and all partial results are joined exactly.  The result is that of fd_decode_paged / fd_decode_dense
+ * over the whole sequences; weights are bf16 (see the
  * prompts above).  scale must be finite and > 0.
  *   num_splits  chunks of the shared tokens, 0 = planner
  *   workspace   fd_shared_prefix_workspace_size(B, Hq, Hkv, prefix_len, L_own,
@@ -445,7 +446,8 @@ FD_API size_t fd_shared_prefix_workspace_size(int B, int Hq, int Hkv, int prefix
  * prefix_table[t / 64]; later tokens follow page_table [B, max_pages] as in
  * fd_decode_paged (whose first prefix_pages entries are not read).  seq_lens
  * counts all tokens of a sequence, shared ones included; a sequence shorter
- * than the prefix attends its first seq_lens[b] tokens. */
+ * than the prefix attends its first seq_lens[b] tokens (all values of the prefix
+ * have to be finite for it too). */
 FD_API int fd_decode_paged_shared_prefix(const void* q, const void* k_pages, const void* v_pages,
                                          const int32_t* prefix_table, int prefix_pages,
                                          const int32_t* page_table, int max_pages, int num_pages,
@@ -554,8 +556,8 @@ FD_API int fd_debug_inject_wait_timeout(unsigned long long wait_limit_ns, int wi
 /* Synchronises `stream`, then reports the device status word of the current
  * device: FD_ERR_DEVICE_TIMEOUT, FD_ERR_BAD_PAGE_TABLE, FD_ERR_OUT_OF_PAGES,
  * FD_ERR_INVALID_ARG (a seq_lens entry outside [0, L_max], or an offset or
- * length of the prompt calls; the kernels clamped it) or FD_OK, in that order of precedence (FD_ERR_CUDA if the synchronisation itself
- * failed).  clear != 0 resets the word afterwards. */
+ * length of the prompt calls; the kernels clamped it) or FD_OK, in that order
+ * of precedence (FD_ERR_CUDA if the synchronisation itself failed).  clear != 0 resets the word afterwards. */
 FD_API int fd_device_status(int clear, void* stream);
 
 #ifdef __cplusplus

@@ -387,10 +387,11 @@ __device__ __forceinline__ void store32(void* at, const uint32_t* x, bool wide) 
 //     halves, three-operand maxima, a last block cut to its keys and a warpgroup
 //     of its own for the output all measured slower or the same.
 //   * short prompts pay about 5 us a piece of work for filling and draining the
-//     pipelines (ragged prompts of 257 to 6143 tokens: 1.05-1.1 ms, 1.4-1.47
-//     PFLOP/s).
-//   * few query rows (drafts, a shared prefix): HBM.  16 x 8 drafted tokens on
-//     16K-64K cached ones 328 us, 6.5 TB/s.
+//     pipelines (8 prompts of 257 to 6143 tokens, 64 query heads: 1.05-1.1 ms,
+//     1.4-1.47 PFLOP/s).  It is not the copies: the next queries in L2 ahead of
+//     time, or its first keys before its queries, changed nothing.
+//   * few query rows (drafts, a shared prefix): HBM.  16 x 8 drafted tokens of 64
+//     query heads on 16K-64K cached ones 337 us, 6.3 TB/s.
 template <int D, bool PAGED, bool DUAL>
 __global__ void __launch_bounds__(kThreads, 1)
 rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
