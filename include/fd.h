@@ -432,9 +432,10 @@ FD_API int fd_prefill_paged(const void* q, const void* k_pages, const void* v_pa
 /* Decode of one token per sequence for a batch whose sequences start with the
  * same tokens: the shared keys and values are read once for the whole batch
  * (every query of the batch against them as one matrix product), each
- * sequence's own tokens apart, and all partial results are joined exactly.  The result is that of fd_decode_paged / fd_decode_dense
- * over the whole sequences; weights are bf16 (see the
- * prompts above).  scale must be finite and > 0.
+ * sequence's own tokens apart, and all partial results are joined exactly.
+ * The result is that of fd_decode_paged / fd_decode_dense over the whole
+ * sequences; weights are bf16 (see the prompts above).  scale must be finite
+ * and > 0.
  *   num_splits  chunks of the shared tokens, 0 = planner
  *   workspace   fd_shared_prefix_workspace_size(B, Hq, Hkv, prefix_len, L_own,
  *               d, num_splits) bytes (never 0): prefix_len = prefix_pages * 64
