@@ -76,7 +76,8 @@ def test_assign_in_place_over_steps(fd):
     assert t.tolist() == table
 
 
-@pytest.mark.parametrize("B,ctx,most", [(300, 100, 200), (1500, 50, 30), (3, 4000, 9000), (2100, 0, 9)])
+@pytest.mark.parametrize("B,ctx,most", [(300, 100, 200), (1500, 50, 30), (3, 4000, 9000), (2100, 0, 9),
+                                        (1500, 50, 60), (4, 100, 20000), (2100, 1000, 40)])
 def test_assign_in_place_with_many_tokens(fd, B, ctx, most):
     # beyond what one block does alone: a cluster for the table, the whole GPU for the slots
     cached, new, table, free = problem(B, ctx, most, seed=B, spare=9)

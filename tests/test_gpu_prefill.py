@@ -299,6 +299,54 @@ def test_paged_tails(fd, G, d, num_splits):
               num_splits=num_splits)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("new,ctx,Hq,Hkv,d", [([64, 64], [20000, 100], 8, 2, 128), ([8, 8, 8, 8], [9000, 30, 0, 4000], 8, 2, 128),
+                                              ([500], [6000], 16, 2, 64), ([1, 70, 0, 3], [5000, 1, 12000, 0], 7, 1, 128)])
+def test_paged_parts_chosen_by_the_planner(fd, new, ctx, Hq, Hkv, d, causal):
+    width = -(-max(n + c for n, c in zip(new, ctx)) // 64)
+    assert fd.fd_prefill_num_splits(len(new), sum(new), Hq, Hkv, 64 * width, d) > 1
+    run_paged(fd, new, ctx, Hq, Hkv, d, seed=sum(new), causal=causal)
+
+
+def test_captured_parts_follow_the_lengths(fd):
+    # the parts are cut on the device: a replay with other lengths is the call with those lengths
+    g = generator(31)
+    new, room = [40, 3, 80], [9000, 7000, 8000]
+    kp, vp, table, pool = random_pool(room, 2, 128, g)
+    q = randn(g, sum(new), 8, 128)
+    cu = offsets(new)
+    lens = torch.tensor(room, dtype=torch.int32, device="cuda")
+    assert fd.fd_prefill_num_splits(3, sum(new), 8, 2, 64 * table.shape[1], 128) > 1
+    out, lse = torch.empty_like(q), torch.empty(sum(new), 8, device="cuda")
+    fd.fd_prefill_paged(q, kp, vp, table, pool, cu, lens, out=out, lse=lse)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        fd.fd_prefill_paged(q, kp, vp, table, pool, cu, lens, out=out, lse=lse)
+    for now in (room, [40, 6999, 300], [9000, 2, 0], [641, 3, 5000]):
+        lens.copy_(torch.tensor(now, dtype=torch.int32))
+        graph.replay()
+        want, wlse = fd.fd_prefill_paged(q, kp, vp, table, pool, cu, lens)
+        assert torch.equal(out, want) and torch.equal(lse, wlse)
+        a = 0
+        for i, (n, L) in enumerate(zip(new, now)):
+            k, v = gather_pages(kp, table[i], L), gather_pages(vp, table[i], L)
+            check_rows(out[a:a + n], lse[a:a + n], attend64(q[a:a + n], k, v, limits(n, L, True), 128 ** -0.5))
+            a += n
+    assert fd.fd_device_status(clear=True) == fd.FD_OK
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("num_splits", [1, 2])
+def test_keys_behind_the_causal_mask_may_hold_anything(fd, bad, num_splits):
+    g = generator(32)
+    q, k, v = randn(g, 333, 8, 128), randn(g, 333, 2, 128), randn(g, 333, 2, 128)
+    cu = offsets([333])
+    want, wlse = fd.fd_prefill_packed(q, k, v, cu, num_splits=num_splits)
+    k[300:] = bad
+    out, lse = fd.fd_prefill_packed(q, k, v, cu, num_splits=num_splits)
+    assert torch.equal(out[:300], want[:300]) and torch.equal(lse[:300], wlse[:300])
+
+
 def test_paged_not_causal_and_float32(fd):
     run_paged(fd, [5, 140], [300, 70], 8, 2, 128, seed=21, causal=False, out_dtype="f32")
 
