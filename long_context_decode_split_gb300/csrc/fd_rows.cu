@@ -1152,9 +1152,10 @@ cudaError_t launch_merge_list(const float* part_o, const float* part_ml, const i
                               int D, int n, void* out, int out_bf16, float* lse, cudaStream_t stream) {
     const long long rows = (long long)tokens * Hq;
     // few rows with long lists leave most of the GPU idle with a warp each (the whole
-    // call, 512 rows: 40 records 31.3 us with a warp each, 23.9 us with eight, 12 records
-    // 23.3 and 24.7 us; 8192 rows of 20 records 231 and 244 us)
-    const bool wide = n > 16 && rows < 4096;
+    // call, 256 rows: 14 records 17.7 us with a warp each, 15.8 us with eight, 8 records 18.0
+    // and 18.0 us; 512 rows: 12 records 22.3 and 25.4 us, 20 records 23.5 and 20.1 us;
+    // 8192 rows of 20 records 231 and 244 us)
+    const bool wide = n > (rows <= 256 ? 8 : 16) && rows < 4096;
     const dim3 grid((unsigned)(wide ? rows : (rows + 7) / 8));
     const auto kernel = D == 128 ? (wide ? merge_list_kernel<128, 8> : merge_list_kernel<128, 1>)
                                  : (wide ? merge_list_kernel<64, 8> : merge_list_kernel<64, 1>);
