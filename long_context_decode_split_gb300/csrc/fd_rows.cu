@@ -37,6 +37,7 @@ struct RowsParams {
     int causal;
     int splits, chunk;
     int tiles;  // slots of every (head, chunk)
+    int side_by_side;  // the tiles of a chunk follow each other, else the chunks of a tile
     unsigned long long wait_limit_ns;  // time limit of every pipeline wait
     int withhold_tile;                 // >= 0: fault injection, that block's keys of each chunk are never copied
     void* out;
@@ -466,10 +467,18 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
                 if (w.valid) {
                     const bool own = !DUAL && id >= p.shared_work;
                     const int at = own ? id - p.shared_work : id;
-                    const int rest = at / p.Hkv, splits = own ? p.own_splits : p.splits;
-                    const int split = rest % splits;
-                    w.h = at % p.Hkv;
-                    w.it = own ? own_item(p, rest / splits) : find_item(p, p.tiles - 1 - rest / splits, TILES * p.tok);
+                    const int splits = own ? p.own_splits : p.splits;
+                    int split, place;  // place: the tile, or the query token with own keys
+                    if (!own && p.side_by_side) {
+                        place = at % p.tiles;
+                        w.h = at / p.tiles % p.Hkv;
+                        split = at / p.tiles / p.Hkv;
+                    } else {
+                        w.h = at % p.Hkv;
+                        split = at / p.Hkv % splits;
+                        place = at / p.Hkv / splits;
+                    }
+                    w.it = own ? own_item(p, place) : find_item(p, p.tiles - 1 - place, TILES * p.tok);
                     some = w.it.t0 >= 0 && w.it.t0 < w.it.Lq;
                     int chunk = p.own_chunk;
                     if (!own) {  // equal parts of what the tiles see
@@ -1133,6 +1142,8 @@ cudaError_t launch_rows(const RowsArgs& a, cudaStream_t stream) {
     p.own_rec0 = a.own_rec0;
     const long long tiles = rows_tiles(a.B, a.total_q, p.G, a.cu_q != nullptr);
     p.tiles = (int)tiles;
+    // one sequence of keys for all tiles: those of a chunk read it from L2 together
+    p.side_by_side = a.cu_q == nullptr;
     injected_timeout(&p.wait_limit_ns, &p.withhold_tile);
     p.shared_work = (int)(tiles * a.Hkv * a.splits);
     const dim3 grid((unsigned)(p.shared_work + own_work));
