@@ -165,7 +165,7 @@ struct RowsGeo {
     // (Every consumer of a ring waits for every tile of it: a barrier's parity
     // tells only two phases apart.)
     static constexpr int RING = DUAL ? STAGES : STAGES / 2;
-    static constexpr int SMEM = 1024 + (TILES + STAGES) * TILE + (2 * STAGES + 16) * 8 + 16 + 2 * 64 + 16 + 2 * 128 * 4;
+    static constexpr int SMEM = 1024 + (TILES + STAGES) * TILE + (2 * STAGES + 18) * 8 + 16 + 2 * 64 + 16 + 2 * 128 * 4;
     static_assert(SMEM <= 232448, "shared memory of a CTA");
 };
 
@@ -406,8 +406,8 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
     uint64_t* full = reinterpret_cast<uint64_t*>(ring + STAGES * TILE);
     uint64_t* empty = full + STAGES;
     uint64_t* q_full = empty + STAGES;
-    uint64_t* q_empty = q_full + 1;
-    uint64_t* s_full = q_empty + 1;     // [2] S of the next block is complete
+    uint64_t* q_empty = q_full + 2;     // [2] each, a tile (the second one DUAL only)
+    uint64_t* s_full = q_empty + 2;     // [2] S of the next block is complete
     uint64_t* p_full = s_full + 2;      // [2] P is in place, and O is rescaled
     uint64_t* o_full = p_full + 2;      // [2] O is complete
     uint64_t* work_full = o_full + 2;   // [2]
@@ -426,9 +426,9 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], DUAL ? 2 : 1);
         }
-        mbar_init(q_full, 1);
-        mbar_init(q_empty, 2);
         for (int i = 0; i < 2; ++i) {
+            mbar_init(&q_full[i], 1);
+            mbar_init(&q_empty[i], DUAL ? 1 : 2);
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 4);
             mbar_init(&o_full[i], 1);
@@ -458,7 +458,8 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
             // ---------------- work and copies ----------------
             bool ok = true;
             int n0 = 0, n1 = 0;   // tiles through the ring of pipeline 0 (or both) and 1
-            int qn = 0, wn = 0;   // query loads, pieces of work
+            int qn[2] = {0, 0};   // loads of either query tile
+            int wn = 0;           // pieces of work
             int id = blockIdx.x;
             for (int asked = 0; ok; ++asked) {
                 Work w;
@@ -513,19 +514,22 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
                     if (!w.valid) break;
                     const int blocks = max(w.nb[0], w.nb[1]);
                     if (blocks > 0) {
-                        ok = warp_wait(q_empty, ((uint32_t)qn & 1u) ^ 1u, p.wait_limit_ns);
-                        if (!ok) break;
-                        ++qn;
-                        if (lane == 0) {
-                            const uint32_t qbytes = (uint32_t)((w.it.own ? 1 : p.tok) * p.G * D * 2);
-                            const void* map = w.it.own ? static_cast<const void*>(&maps.own_q) : &maps.q;
-                            const int qtiles = DUAL && w.nb[1] > 0 ? 2 : 1;
-                            mbar_arrive_expect_tx(q_full, qbytes * qtiles);
-                            for (int i = 0; i < qtiles; ++i)
+                        auto query = [&](int i) {  // tile i of the queries
+                            if (DUAL && w.nb[i] == 0) return;
+                            ok = ok && warp_wait(&q_empty[i], ((uint32_t)qn[i] & 1u) ^ 1u, p.wait_limit_ns);
+                            if (!ok) return;
+                            ++qn[i];
+                            if (lane == 0) {
+                                const uint32_t qbytes = (uint32_t)((w.it.own ? 1 : p.tok) * p.G * D * 2);
+                                const void* map = w.it.own ? static_cast<const void*>(&maps.own_q) : &maps.q;
+                                mbar_arrive_expect_tx(&q_full[i], qbytes);
                                 for (int bx = 0; bx < BOXES; ++bx)
                                     tma_load_3d(sq + i * TILE + bx * BOX, map, 64 * bx, w.h * p.G,
-                                                w.it.q0 + w.it.t0 + i * p.tok, q_full);
-                        }
+                                                w.it.q0 + w.it.t0 + i * p.tok, &q_full[i]);
+                            }
+                        };
+                        query(0);
+                        if (!ok) break;
                         // Page ids by the warp, 32 pages a register: the windows of 16 blocks alternate
                         // between two of them, the next one fetched when the keys are 4 blocks into the
                         // current one (the values are at most 2 blocks behind).
@@ -587,6 +591,7 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
                         };
                         constexpr int AHEAD = DUAL ? 1 : 2;  // blocks by which the keys run ahead of the values
                         for (int j = 0; j < AHEAD && j < blocks; ++j) load(j, 0);
+                        if (DUAL) query(1);
                         for (int j = 0; ok && j < blocks; ++j) {
                             load(j, 1);
                             if (j + AHEAD < blocks) load(j + AHEAD, 0);
@@ -606,7 +611,8 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
             if (!ok) {
                 // the others stopped early: let the copies in flight land before the CTA ends
                 if (lane == 0) atomicOr(&g_status_rows, kStatusTimeout);
-                if (qn > 0) mbar_wait(q_full, (uint32_t)(qn - 1) & 1u, p.wait_limit_ns);
+                for (int i = 0; i < 2; ++i)
+                    if (qn[i] > 0) mbar_wait(&q_full[i], (uint32_t)(qn[i] - 1) & 1u, p.wait_limit_ns);
                 for (int u = max(0, n0 - RING); u < n0; ++u)
                     mbar_wait(&full[u % RING], (uint32_t)(u / RING) & 1u, p.wait_limit_ns);
                 for (int u = max(0, n1 - RING); u < n1; ++u)
@@ -684,13 +690,16 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
                 };
-                ok = warp_wait(q_full, qn & 1u, p.wait_limit_ns);
-                ++qn;
+                const uint32_t qt = DUAL ? i : 0;
+                if (!DUAL || nb > 0) {
+                    ok = warp_wait(&q_full[qt], qn & 1u, p.wait_limit_ns);
+                    ++qn;
+                }
                 if (ok && nb > 0) {
                     const uint32_t s0 = arrive(n0);
                     if (!ok) break;
                     qk(s0);
-                    if (nb == 1) commit(q_empty);
+                    if (nb == 1) commit(&q_empty[qt]);
                     for (int r = 0; r < nb; ++r) {
                         const bool more = r + 1 < nb;
                         const uint32_t sv = arrive(n0 + 2 * r + 1);
@@ -704,9 +713,9 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
                         pv(sv, r == 0);
                         if (more) qk(sk);
                         else commit(&o_full[i]);
-                        if (r + 2 == nb) commit(q_empty);
+                        if (r + 2 == nb) commit(&q_empty[qt]);
                     }
-                } else if (ok && lane == 0) {
+                } else if (!DUAL && ok && lane == 0) {
                     mbar_arrive(q_empty);
                 }
                 // tiles that only the other pipeline needs
