@@ -350,14 +350,17 @@ RowsPlan rows_chunks(int max_k, long long splits, bool exact) {
 
 // The shared part of a shared-prefix decode: `ctas` pieces of work per chunk,
 // all alike, one per SM at a time; with `own` further pieces of about own_blocks
-// blocks beside them.  A piece of c blocks takes about c + 4 blocks of time
-// (set-up, first copies, last output), every chunk costs merge work, so: the
-// count with the least of that, the longest SM's share or the mean.  Own pieces
+// blocks beside them.  A piece of c blocks takes about c + `piece` blocks of time
+// (set-up, first copies, last output: 4 for a single tile, 14 for two tiles, whose
+// records all SMs write at the same time; 128 sequences of 64 query heads behind 32K
+// tokens: 146 us in 4 chunks, 154 us in 9; 64 behind 128K: 202 us in 9, 211 us in 19),
+// every chunk costs merge work, so: the count with the least of that, the longest
+// SM's share or the mean.  Own pieces
 // are short, and with nothing but them running the copies do not fill HBM: where
 // the SMs that the chunks leave free get through them in a chunk's time, that
 // counts a tenth less (32 sequences behind 128K tokens: 14 chunks 108 us, 16 to
 // 19 chunks 119 to 121 us).
-RowsPlan shared_rows_plan(long long ctas, int max_k, int requested, long long own, double own_blocks) {
+RowsPlan shared_rows_plan(long long ctas, int max_k, int requested, double piece, long long own, double own_blocks) {
     if (requested > 0) return rows_chunks(max_k, requested, true);
     const int sms = current_sm_count(), blocks = (max_k + 127) / 128;
     long long best_s = 1;
@@ -367,9 +370,10 @@ RowsPlan shared_rows_plan(long long ctas, int max_k, int requested, long long ow
             const long long c = (blocks + S - 1) / S;
             if ((blocks + c - 1) / c != S) continue;  // the chunks of a smaller count
             const double waves = (double)((ctas * S + sms - 1) / sms);
-            const double mean = ((double)(ctas * S) * (double)(c + 4) + (double)own * (own_blocks + 4)) / sms;
-            const bool beside = (double)own * (own_blocks + 4) <= (double)(sms - ctas * S) * (double)(c + 4);
-            const double busy = std::max(waves * (double)(c + 4), mean);
+            const double shared = (double)c + piece, own_time = (double)own * (own_blocks + piece);
+            const double mean = ((double)(ctas * S) * shared + own_time) / sms;
+            const bool beside = own_time <= (double)(sms - ctas * S) * shared;
+            const double busy = std::max(waves * shared, mean);
             const double cost = (own > 0 && !beside ? 1.1 * busy : busy) + (double)S / 8.0;
             if (cost < best) {
                 best = cost;
@@ -501,7 +505,8 @@ SharedPlan shared_plan_uncached(int B, int Hq, int Hkv, int prefix_len, int L_ow
     const bool short_own = (long long)B * Hkv >= current_sm_count() && L_own <= 32 * kTile;
     s.own = decode_plan(B, Hq, Hkv, L_own, d, short_own ? 1 : 0, true);
     const long long own = s.together && L_own > 0 ? (long long)B * Hkv * s.own_rows.splits : 0;
-    s.shared = shared_rows_plan(fd::rows_tiles(1, B, Hq / Hkv, false) * Hkv, prefix_len, num_splits, own,
+    s.shared = shared_rows_plan(fd::rows_tiles(1, B, Hq / Hkv, false) * Hkv, prefix_len, num_splits,
+                                s.together ? 4.0 : 14.0, own,
                                 0.5 * blocks / s.own_rows.splits);
     s.list = s.shared.splits + (L_own > 0 ? s.own_splits() : 0);
     return s;

@@ -387,10 +387,13 @@ __device__ __forceinline__ void store32(void* at, const uint32_t* x, bool wide) 
 //     weights, 40 to store P) beside 2 x 1024 of products.  Handing P over in
 //     halves, three-operand maxima, a last block cut to its keys and a warpgroup
 //     of its own for the output all measured slower or the same.
-//   * short prompts pay about 5 us a piece of work for filling and draining the
-//     pipelines (8 prompts of 257 to 6143 tokens, 64 query heads: 1.05-1.1 ms,
-//     1.4-1.47 PFLOP/s).  It is not the copies: the next queries in L2 ahead of
-//     time, or its first keys before its queries, changed nothing.
+//   * short prompts pay about 3 us a piece of work between its last product and the
+//     next one's first: the output (1.3 us), the next work and its scores, their
+//     softmax with both warpgroups at once (8 prompts of 257 to 6143 tokens, 64 query
+//     heads: 0.96 ms in a short run, 1.02 ms in a loop, 1.5-1.6 PFLOP/s).  It is not the
+//     copies: the next queries in L2 ahead of time, or its first keys before its
+//     queries, changed nothing; nor the stores: whole lines traded between lanes took
+//     longer.
 //   * few query rows (drafts, a shared prefix): HBM.  16 x 8 drafted tokens of 64
 //     query heads on 16K-64K cached ones 337 us, 6.3 TB/s.
 template <int D, bool PAGED, bool DUAL>
@@ -883,40 +886,57 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
             const int head = h * p.G + r - tk * p.G;
             const size_t row = (size_t)(it.q0 + first + tk) * p.Hq + head;
             const size_t rec = row * p.rec_stride + rec_at;
-            const bool in0 = DUAL ? i == 0 && rounds > 0 : all > 0, in1 = DUAL ? i == 1 && rounds > 0 : all > 1;
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-                if (!DUAL && c / (D / 64) != i) continue;
-                float f[32];
+            auto channels = [&](int c, float (&f)[32]) {  // 32 of the result's
+                uint32_t o[32];
 #pragma unroll
                 for (int e = 0; e < 32; ++e) f[e] = 0.f;
-                uint32_t o[32];
-                if (in0) {
-                    tmem_ld32(o, o_at + 32 * c);
+                if (DUAL ? rounds > 0 : all > 0) {
+                    const float by = DUAL ? inv_own : f0;
+                    tmem_ld32(o, o_at + (DUAL ? i * D : 0) + c);
                     tmem_wait_ld();
                     tie32(o);
+                    if (by != 0.f) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) f[e] = f0 != 0.f ? __uint_as_float(o[e]) * f0 : 0.f;
+                        for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(o[e]) * by;
+                    }
                 }
-                if (in1) {
-                    tmem_ld32(o, o_at + D + 32 * c);
+                if (!DUAL && all > 1) {
+                    tmem_ld32(o, o_at + D + c);
                     tmem_wait_ld();
                     tie32(o);
+                    if (f1 != 0.f) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) f[e] += f1 != 0.f ? __uint_as_float(o[e]) * f1 : 0.f;
+                        for (int e = 0; e < 32; ++e) f[e] += __uint_as_float(o[e]) * f1;
+                    }
                 }
-                if (!live) continue;
-                if (!p.direct || !p.out_bf16) {
-                    float* dst = (p.direct ? static_cast<float*>(p.out) + row * D : p.part_o + rec * D) + 32 * c;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) store32(dst + 8 * e, reinterpret_cast<uint32_t*>(f) + 8 * e, p.wide);
-                } else {
-                    uint16_t* dst = static_cast<uint16_t*>(p.out) + row * D + 32 * c;
+            };
+            // This code runs once a piece: fetching it takes longer than running it, so its loops are
+            // rolled up (32 prompts of 512: 116 us unrolled, 100 us).
+            constexpr int MINE = DUAL ? D : D / 2;  // channels that this warpgroup writes
+            const int c_mine = DUAL ? 0 : i * MINE;
+            if (p.direct && p.out_bf16) {
+                uint16_t* dst = static_cast<uint16_t*>(p.out) + row * D;
+#pragma unroll 1
+                for (int c = c_mine; c < c_mine + MINE; c += 32) {
+                    float f[32];
+                    channels(c, f);
+                    if (!live) continue;
                     uint32_t x[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) x[e] = pack_bf16(f[2 * e], f[2 * e + 1]);
-                    store32(dst, x, p.wide);
-                    store32(dst + 16, x + 8, p.wide);
+                    store32(dst + c, x, p.wide);
+                    store32(dst + c + 16, x + 8, p.wide);
+                }
+            } else {
+                float* dst = p.direct ? static_cast<float*>(p.out) + row * D : p.part_o + rec * D;
+#pragma unroll 1
+                for (int c = c_mine; c < c_mine + MINE; c += 32) {
+                    float f[32];
+                    channels(c, f);
+                    if (!live) continue;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        store32(dst + c + 8 * e, reinterpret_cast<uint32_t*>(f) + 8 * e, p.wide);
                 }
             }
             if (live && (DUAL || i == 0)) {
