@@ -793,10 +793,13 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
                 for (int c = 0; c < 4; ++c) tie32(s[c]);
                 if (__any_sync(0xffffffffu, left < kBlock || bad[0] || bad[1])) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
+                    for (int c = 0; c < 4; ++c) {
+                        const int n = bad[c >> 1] ? 0 : min(max(left - 32 * c, 0), 32);
+                        const uint32_t seen = n < 32 ? (1u << n) - 1u : 0xffffffffu;
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
-                            if (32 * c + e >= left || bad[c >> 1]) s[c][e] = 0xff800000u;  // -inf
+                            if (!(seen & 1u << e)) s[c][e] = 0xff800000u;  // -inf
+                    }
                 }
                 float mx[4];
 #pragma unroll
@@ -844,20 +847,33 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[i]);
             }
+            const int head = h * p.G + r - tk * p.G;
+            const size_t row = (size_t)(it.q0 + first + tk) * p.Hq + head;
+            const size_t rec = row * p.rec_stride + rec_at;
+            float l = ok ? l2.x + l2.y : 0.f;
+            auto statistics = [&] {
+                if (!p.direct) {
+                    p.part_ml[2 * rec] = l > 0.f ? m : -INFINITY;
+                    p.part_ml[2 * rec + 1] = l;
+                } else if (p.lse) {
+                    p.lse[row] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
+                }
+            };
+            // what does not need O goes before the wait for it
+            const float inv_own = l > 0.f ? 1.f / l : 0.f;
+            if (DUAL && live) statistics();
             if (ok && rounds > 0) {
                 ok = warp_wait(&o_full[i], o_round & 1u, p.wait_limit_ns);
                 ++o_round;
             }
             tc_fence_after();
-            float l = ok ? l2.x + l2.y : 0.f;
-            if (!ok) m = -INFINITY;
+            if (!ok) {
+                l = 0.f;
+                m = -INFINITY;
+            }
             // factors of the O of pipeline 0 and 1
             float f0 = i ? 0.f : 1.f, f1 = i ? 1.f : 0.f;
-            const float inv_own = l > 0.f ? 1.f / l : 0.f;
-            if (DUAL) {
-                f0 *= inv_own;
-                f1 *= inv_own;
-            } else {
+            if (!DUAL) {
                 // pipeline 0 learns m and l of pipeline 1 and tells the factors; each
                 // warpgroup then writes half of the channels of the joined result
                 if (i == 1) {
@@ -883,9 +899,6 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
                     f1 = join[128 + r];
                 }
             }
-            const int head = h * p.G + r - tk * p.G;
-            const size_t row = (size_t)(it.q0 + first + tk) * p.Hq + head;
-            const size_t rec = row * p.rec_stride + rec_at;
             auto channels = [&](int c, float (&f)[32]) {  // 32 of the result's
                 uint32_t o[32];
 #pragma unroll
@@ -939,14 +952,7 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
                         store32(dst + c + 8 * e, reinterpret_cast<uint32_t*>(f) + 8 * e, p.wide);
                 }
             }
-            if (live && (DUAL || i == 0)) {
-                if (!p.direct) {
-                    p.part_ml[2 * rec] = l > 0.f ? m : -INFINITY;
-                    p.part_ml[2 * rec + 1] = l;
-                } else if (p.lse) {
-                    p.lse[row] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
-                }
-            }
+            if (!DUAL && live && i == 0) statistics();
             tc_fence_before();
             if (!DUAL) named_barrier(1, 256);  // both O and the factors are read
         }
