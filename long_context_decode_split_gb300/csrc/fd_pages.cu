@@ -161,30 +161,44 @@ __global__ void __launch_bounds__(kAssignThreads) assign_kernel(const AssignPara
                 }
                 return lo;
             };
-            auto slot_of = [&](int t, int s) -> int64_t {
-                const int c = cached_s[s];
-                const long long pos = (long long)c + t - cu_s[s];
-                if (pos >= end_s[s]) return -1;
-                const int j = (int)(pos / kTile), old = pages_of(c);
+            auto page_of = [&](int s, int j) -> int {  // page j of a sequence
+                const int old = pages_of(cached_s[s]);
+                if (j < old) return p.page_table[(size_t)(b0 + s) * p.max_pages + j];
                 const long long at = base + first_s[s] + j - old;
-                int page = -1;
-                if (j < old) page = p.page_table[(size_t)(b0 + s) * p.max_pages + j];
-                else if (at < p.num_free) page = p.free_pages[at];
-                return page < 0 ? -1 : (int64_t)page * kTile + (int)(pos % kTile);
+                return at < p.num_free ? p.free_pages[at] : -1;
+            };
+            auto slot_in = [](int page, unsigned pos) {
+                return page < 0 ? (int64_t)-1 : (int64_t)page * kTile + pos % kTile;
+            };
+            auto slot_of = [&](int t, int s) -> int64_t {
+                const unsigned pos = cached_s[s] + (unsigned)(t - cu_s[s]);  // (cut tokens may pass 2^31)
+                return pos < (unsigned)end_s[s] ? slot_in(page_of(s, pos / kTile), pos) : -1;
             };
             if (t1 - t0 <= lanes) {
                 if (t0 + lane0 < t1) p.slots[t0 + lane0] = slot_of(t0 + lane0, sequence(t0 + lane0));
             } else {
-                // two tokens a thread, one 16-byte store; a pair may lie across two groups
-                for (long long pair = (long long)(t0 & ~1) + 2 * lane0; pair < t1; pair += 2LL * lanes) {
-                    const int t = (int)pair;
-                    const bool in0 = t >= t0, in1 = t + 1 < t1;
-                    const int s0 = sequence(in0 ? t : t0);
-                    const int s1 = in1 && t + 1 >= cu_s[s0 + 1] ? sequence(t + 1) : s0;
-                    if (in0 && in1)
-                        *reinterpret_cast<longlong2*>(p.slots + t) = make_longlong2(slot_of(t, s0), slot_of(t + 1, s1));
-                    else if (in0) p.slots[t] = slot_of(t, s0);
-                    else p.slots[t + 1] = slot_of(t + 1, s1);
+                // four tokens a thread, mostly of one sequence and one or two of its pages
+                for (long long four = (long long)(t0 & ~3) + 4 * lane0; four < t1; four += 4LL * lanes) {
+                    const int t = (int)four;
+                    int s = sequence(max(t, t0));
+                    const unsigned pos = cached_s[s] + (unsigned)(t - cu_s[s]);
+                    int64_t* to = p.slots + t;
+                    if (t >= cu_s[s] && t + 3 < min(cu_s[s + 1], t1) && pos + 3 < (unsigned)end_s[s]) {
+                        const int page = page_of(s, pos / kTile);
+                        const int next = pos % kTile > kTile - 4 ? page_of(s, pos / kTile + 1) : page;
+                        int64_t x[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            x[e] = slot_in(pos % kTile + e < kTile ? page : next, pos + e);
+                        reinterpret_cast<longlong2*>(to)[0] = make_longlong2(x[0], x[1]);
+                        reinterpret_cast<longlong2*>(to)[1] = make_longlong2(x[2], x[3]);
+                    } else {
+#pragma unroll 1
+                        for (int e = max(t0 - t, 0); e < 4 && t + e < t1; ++e) {
+                            if (t + e >= cu_s[s + 1]) s = sequence(t + e);
+                            to[e] = slot_of(t + e, s);
+                        }
+                    }
                 }
             }
         }
@@ -426,10 +440,10 @@ constexpr int kSlotsHere = 32768;
 constexpr int kPagesAlone = 2048, kSlotsAlone = 2048;
 // Otherwise a CTA per so many tokens and pages, a thread each, up to one CTA per SM
 // (131072 tokens: 4.0 us, 5.6 us with 4096 and 4.0 us with 512 per CTA).  512 prompts
-// with a million new tokens take 9.0 us, 11.5 us in the two launches of a call in place;
-// their 8.8 MB would pass HBM in 1.3 us; searches and page look-ups take 4.4 us of it,
-// the stores 1 us, the launch, lengths and sums 3.7 us.  Four tokens a thread, or a run
-// of tokens per CTA that keeps its sequence, measured the same.
+// with a million new tokens take 8.2 us, 11.5 us in the two launches of a call in place;
+// their 8.8 MB would pass HBM in 1.3 us; searches and page look-ups take 3.5 us of it,
+// the stores 1 us, the launch, lengths and sums 3.7 us (two tokens a thread 9.15 us; a
+// run of tokens per CTA that keeps its sequence 9.6 us).
 constexpr int kPerCta = 1024;
 
 cudaError_t launch_assign(const AssignArgs& a, cudaStream_t stream) {
