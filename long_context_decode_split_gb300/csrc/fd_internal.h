@@ -175,11 +175,11 @@ struct RowsArgs {
     int own_splits, own_chunk, own_rec0;  // own_splits == 0: they are someone else's
 };
 // Whether the tokens of this call take one tile per CTA (own tokens are then part of its work).
-bool rows_single(int B, int total_q, int G);
+bool rows_single(int B, int total_q, int G, int max_k);
 // Tiles of `total_q` tokens: how many tokens one takes, and how many tiles there are at most
 // (B sequences by offsets) or exactly (one sequence).
-int rows_tokens(int B, int total_q, int G);
-long long rows_tiles(int B, int total_q, int G, bool offsets);
+int rows_tokens(int B, int total_q, int G, int max_k);
+long long rows_tiles(int B, int total_q, int G, int max_k, bool offsets);
 cudaError_t launch_rows(const RowsArgs& a, cudaStream_t stream);
 cudaError_t rows_status_read(unsigned* bits, bool clear);
 // Merge of n records per row, all of them written (m = -inf: nothing attended).

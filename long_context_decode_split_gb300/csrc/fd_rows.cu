@@ -376,9 +376,9 @@ __device__ __forceinline__ void store32(void* at, const uint32_t* x, bool wide) 
 // What bounds it, and what each choice brought (32 query heads, 8 KV heads,
 // d = 128):
 //   * long prompts: the tensor cores at the power limit.  32K tokens take
-//     5.2-5.4 ms in a loop (1.63-1.69 PFLOP/s of the causal products; a bf16
-//     matrix product in a loop reaches 1.72) and 4.8-4.9 ms in a short run
-//     (1.78-1.84; 1.97).  64 cycles an MMA of the 128 x 128 x 16 shape.
+//     5.2-5.3 ms in a loop (1.66-1.69 PFLOP/s of the causal products; a bf16
+//     matrix product in a loop reaches 1.72) and 4.7 ms in a short run (1.88;
+//     1.97).  64 cycles an MMA of the 128 x 128 x 16 shape.
 //   * an MMA is taken about when it starts to run, so whatever the issuing warp
 //     does in between leaves the tensor cores idle: operands that the compiler
 //     knows to be uniform, 1463 -> 1651 TFLOP/s; a warp per pipeline, whose waits
@@ -395,7 +395,7 @@ __device__ __forceinline__ void store32(void* at, const uint32_t* x, bool wide) 
 //     queries, changed nothing; nor the stores: whole lines traded between lanes took
 //     longer.
 //   * few query rows (drafts, a shared prefix): HBM.  16 x 8 drafted tokens of 64
-//     query heads on 16K-64K cached ones 337 us, 6.3 TB/s.
+//     query heads on 16K-64K cached ones 332 us, 6.4 TB/s.
 template <int D, bool PAGED, bool DUAL>
 __global__ void __launch_bounds__(kThreads, 1)
 rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
@@ -1069,9 +1069,14 @@ merge_list_kernel(const float* __restrict__ part_o, const float* __restrict__ pa
 int rows_tok(int G) { return kRows / G; }
 
 // Two tiles per CTA when the sequences fill more than one on average (64 x 128 tokens
-// behind 2048: 217 us in two, 294 us in one; 64 x 24: 126 and 107 us; between one tile and two
-// within 5% of each other, with nothing cached two are up to 30% faster).
-bool rows_dual(int B, int total_q, int G) { return B > 0 && total_q / B > rows_tok(G); }
+// behind 2048: 207 us in two, 287 us in one; 64 x 24: 113 and 100 us; between one tile
+// and two within 12% of each other), or when whole prompts (as many keys as queries)
+// have a block of keys on average, which a single tile would leave to one of its
+// pipelines (64 x 24 tokens alone: 19.8 us in two, 24.0 us in one).
+bool rows_dual(int B, int total_q, int G, long long max_k) {
+    if (B <= 0) return false;
+    return total_q / B > rows_tok(G) || (B > 1 && max_k == total_q && max_k <= (long long)kBlock * B);
+}
 
 template <int D, bool PAGED, bool DUAL>
 cudaError_t launch_kernel(const RowsMaps& maps, const RowsParams& p, dim3 grid, cudaStream_t stream) {
@@ -1096,12 +1101,14 @@ cudaError_t launch_kernel(const RowsMaps& maps, const RowsParams& p, dim3 grid, 
 
 }  // namespace
 
-bool rows_single(int B, int total_q, int G) { return !rows_dual(B, total_q, G); }
+bool rows_single(int B, int total_q, int G, int max_k) { return !rows_dual(B, total_q, G, max_k); }
 
-int rows_tokens(int B, int total_q, int G) { return rows_tok(G) * (rows_dual(B, total_q, G) ? 2 : 1); }
+int rows_tokens(int B, int total_q, int G, int max_k) {
+    return rows_tok(G) * (rows_dual(B, total_q, G, max_k) ? 2 : 1);
+}
 
-long long rows_tiles(int B, int total_q, int G, bool offsets) {
-    const int per = rows_tokens(B, total_q, G);
+long long rows_tiles(int B, int total_q, int G, int max_k, bool offsets) {
+    const int per = rows_tokens(B, total_q, G, max_k);
     return offsets ? (long long)total_q / per + B : ((long long)total_q + per - 1) / per;
 }
 
@@ -1155,7 +1162,7 @@ cudaError_t launch_rows(const RowsArgs& a, cudaStream_t stream) {
         m.k = m.v = m.q;
     }
     m.own_q = m.own_k = m.own_v = m.q;
-    const bool dual = rows_dual(a.B, a.total_q, p.G);
+    const bool dual = rows_dual(a.B, a.total_q, p.G, a.max_k);
     const long long own_work = a.own_max > 0 ? (long long)a.total_q * a.Hkv * a.own_splits : 0;
     if (own_work > 0) {
         if (dual) return cudaErrorInvalidValue;
@@ -1175,7 +1182,7 @@ cudaError_t launch_rows(const RowsArgs& a, cudaStream_t stream) {
     p.own_splits = a.own_splits;
     p.own_chunk = a.own_chunk;
     p.own_rec0 = a.own_rec0;
-    const long long tiles = rows_tiles(a.B, a.total_q, p.G, a.cu_q != nullptr);
+    const long long tiles = rows_tiles(a.B, a.total_q, p.G, a.max_k, a.cu_q != nullptr);
     p.tiles = (int)tiles;
     // one sequence of keys for all tiles: those of a chunk read it from L2 together
     p.side_by_side = a.cu_q == nullptr;
@@ -1198,9 +1205,9 @@ cudaError_t launch_merge_list(const float* part_o, const float* part_ml, const i
                               int D, int n, void* out, int out_bf16, float* lse, cudaStream_t stream) {
     const long long rows = (long long)tokens * Hq;
     // few rows with long lists leave most of the GPU idle with a warp each (the whole
-    // call, 256 rows: 14 records 17.7 us with a warp each, 15.8 us with eight, 8 records 18.0
-    // and 18.0 us; 512 rows: 12 records 22.3 and 25.4 us, 20 records 23.5 and 20.1 us;
-    // 8192 rows of 20 records 231 and 244 us)
+    // call, 256 rows: 14 records 17.0 us with a warp each, 15.1 us with eight, 9 records 16.9
+    // and 17.2 us; 512 rows: 12 records 20.3 and 20.7 us, 20 records 20.6 and 17.0 us;
+    // 8192 rows of 20 records 220 and 233 us)
     const bool wide = n > (rows <= 256 ? 8 : 16) && rows < 4096;
     const dim3 grid((unsigned)(wide ? rows : (rows + 7) / 8));
     const auto kernel = D == 128 ? (wide ? merge_list_kernel<128, 8> : merge_list_kernel<128, 1>)
