@@ -355,11 +355,10 @@ RowsPlan rows_chunks(int max_k, long long splits, bool exact) {
 // records all SMs write at the same time; 128 sequences of 64 query heads behind 32K
 // tokens: 146 us in 4 chunks, 154 us in 9; 64 behind 128K: 202 us in 9, 211 us in 19),
 // every chunk costs merge work, so: the count with the least of that, the longest
-// SM's share or the mean.  Own pieces
-// are short, and with nothing but them running the copies do not fill HBM: where
-// the SMs that the chunks leave free get through them in a chunk's time, that
-// counts a tenth less (32 sequences behind 128K tokens: 14 chunks 108 us, 16 to
-// 19 chunks 119 to 121 us).
+// SM's share or the mean.  Own pieces are short, and with nothing but them running
+// the copies do not fill HBM: where the SMs that the chunks leave free get through
+// them in a chunk's time, that counts a tenth less (32 sequences behind 128K tokens:
+// 13 chunks 107 us, 16 to 19 chunks 118 to 120 us).
 RowsPlan shared_rows_plan(long long ctas, int max_k, int requested, double piece, long long own, double own_blocks) {
     if (requested > 0) return rows_chunks(max_k, requested, true);
     const int sms = current_sm_count(), blocks = (max_k + 127) / 128;
@@ -478,9 +477,9 @@ int prefill_entry(fd::RowsArgs& a, int num_splits, int out_dtype, void* workspac
 
 // The two parts of a shared-prefix decode: chunks of the shared tokens, then
 // chunks of every sequence's own tokens, in one list of partials.  While the
-// batch's queries of a KV head fit one tile, both are work of one launch (8
-// sequences behind 8K tokens: 17.5 us, 20.4 us in two; 32 behind 128K: 105.8 and
-// 112.9 us); beyond that the shared part is bound by the tensor cores, where a
+// batch's queries of a KV head fit one tile, both are work of one launch (when it
+// was built, 8 sequences behind 8K tokens: 17.5 us, 20.4 us in two; 32 behind 128K:
+// 105.8 and 112.9 us); beyond that the shared part is bound by the tensor cores, where a
 // piece with a few own rows would waste a tile, and the split-KV pass takes the
 // own tokens (128 behind 64K: 286 us together, 250 us apart).
 struct SharedPlan {

@@ -1075,7 +1075,7 @@ int rows_tok(int G) { return kRows / G; }
 // pipelines (64 x 24 tokens alone: 19.8 us in two, 24.0 us in one).
 bool rows_dual(int B, int total_q, int G, long long max_k) {
     if (B <= 0) return false;
-    return total_q / B > rows_tok(G) || (B > 1 && max_k == total_q && max_k <= (long long)kBlock * B);
+    return total_q / B > rows_tok(G) || (max_k == total_q && max_k <= (long long)kBlock * B);
 }
 
 template <int D, bool PAGED, bool DUAL>
