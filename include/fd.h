@@ -378,7 +378,9 @@ FD_API int fd_decode_paged_fp4(const void* q, const uint8_t* k_pages, const uint
  * sees the keys [0, Lk - Lq + i] (causal != 0: the last query at the last
  * key) or [0, Lk).  With s_j = scale * <q, k_j> over the visible keys,
  * out = sum_j e^(s_j) v_j / sum_j e^(s_j) and lse = ln sum_j e^(s_j); a query
- * that sees no key gets out = 0, lse = -inf.  scale must be finite and > 0.
+ * that sees no key gets out = 0, lse = -inf.  A visible score that is NaN or
+ * +inf makes its row NaN (out and lse); one of -inf weighs nothing.  scale must
+ * be finite and > 0.
  * Scores, maxima, sums and outputs are binary32; the weights e^(s - m) enter
  * the product with V as bf16 (relative rounding at most 2^-8), so out carries up to
  * 2^-8 of the weighted mean of |v| in error even as float32; lse does not (its sum takes the
@@ -434,8 +436,9 @@ FD_API int fd_prefill_paged(const void* q, const void* k_pages, const void* v_pa
  * (every query of the batch against them as one matrix product), each
  * sequence's own tokens apart, and all partial results are joined exactly.
  * The result is that of fd_decode_paged / fd_decode_dense over the whole
- * sequences; weights are bf16 (see the prompts above).  scale must be finite
- * and > 0.
+ * sequences; weights are bf16, and a NaN or +inf score makes its row NaN (see
+ * the prompts above; the other decode calls leave a chunk that holds such a
+ * score out).  scale must be finite and > 0.
  *   num_splits  chunks of the shared tokens, 0 = planner
  *   workspace   fd_shared_prefix_workspace_size(B, Hq, Hkv, prefix_len, L_own,
  *               d, num_splits) bytes (never 0): prefix_len = prefix_pages * 64

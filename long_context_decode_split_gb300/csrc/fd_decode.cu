@@ -92,7 +92,7 @@ constexpr float kUnifiedRange = 60.f;
 // mma.sync (A = the warp's K rows by ldmatrix from the swizzled tile, B = Q
 // fragments in registers; accumulator rows gid, gid + 8 are tokens, columns
 // 2 tig, 2 tig + 1 query heads), then the shared online-softmax / P.V step.
-template <int D>
+template <int D, bool NAN_OUT>
 __device__ __forceinline__ void mma_consume_tile(TokAcc<D>& ac, const uint32_t (&qa0)[D / 16],
                                                  const uint32_t (&qa2)[D / 16], uint32_t ks, uint32_t vs,
                                                  unsigned char* vgen, int warp, int lane, int rows, float scale_log2) {
@@ -112,7 +112,7 @@ __device__ __forceinline__ void mma_consume_tile(TokAcc<D>& ac, const uint32_t (
     sc[1] = r0 < rows ? sacc[1] * scale_log2 : -INFINITY;
     sc[2] = r0 + 8 < rows ? sacc[2] * scale_log2 : -INFINITY;
     sc[3] = r0 + 8 < rows ? sacc[3] * scale_log2 : -INFINITY;
-    mma_softmax_pv<D>(ac, sc, vs, vgen, warp, lane, rows);
+    mma_softmax_pv<D, NAN_OUT>(ac, sc, vs, vgen, warp, lane, rows);
 }
 
 // The same tile step through the unified-max variant.
@@ -141,7 +141,10 @@ __device__ __forceinline__ void mma_consume_tile_unified(TokAcc<D>& ac, bool& un
                             make_float2(lo2, lo2));
 }
 
-template <int D, int GP, int CW, int STAGES, bool PAGED, bool MMA, bool UMAX>
+// LISTED: the chunks of a shared-prefix decode's own tokens.  They are records of a
+// longer list (StoreTarget::listed), and a NaN score makes the result NaN; the other
+// passes answer as they always did (a NaN score attends nothing).
+template <int D, int GP, int CW, int STAGES, bool PAGED, bool MMA, bool UMAX, bool LISTED>
 __global__ void __launch_bounds__((CW + 1) * 32, (MMA || GP < 8) ? 2 : 1)
 partial_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                const PartialParams p) {
@@ -175,7 +178,7 @@ partial_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
             }
             if (p.st.lse && threadIdx.x < p.G) p.st.lse[b * p.Hq + hq0 + threadIdx.x] = -INFINITY;
         }
-        if (p.st.mark_empty && threadIdx.x < p.G) {
+        if (LISTED && threadIdx.x < p.G) {
             const size_t pi = (size_t)(b * p.Hq + hq0 + threadIdx.x) * p.st.splits + p.st.rec0 + split;
             p.st.part_ml[2 * pi + 0] = -INFINITY;
             p.st.part_ml[2 * pi + 1] = 0.f;
@@ -276,7 +279,7 @@ partial_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
                 mma_consume_tile_unified<D>(ac, unified, seen, qa0, qa2, smem_u32(sk), smem_u32(sk + BOXES * kBoxBytes),
                                             sk + BOXES * kBoxBytes, warp, lane, rows, p.scale_log2, p.phi2, p.lo2);
             else
-                mma_consume_tile<D>(ac, qa0, qa2, smem_u32(sk), smem_u32(sk + BOXES * kBoxBytes),
+                mma_consume_tile<D, LISTED>(ac, qa0, qa2, smem_u32(sk), smem_u32(sk + BOXES * kBoxBytes),
                                     sk + BOXES * kBoxBytes, warp, lane, rows, p.scale_log2);
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[s]);
@@ -400,8 +403,9 @@ partial_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ 
             for (int off = 16; off >= (1 << Gm::SH); off >>= 1)
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
             const float m_new = fmaxf(m_run[g], mx);
-            if (m_new == -INFINITY) {  // nothing valid yet (warp-uniform)
-                pr[g] = 0.f;
+            if (m_new == -INFINITY) {  // nothing valid yet (warp-uniform), NaN apart
+                pr[g] = LISTED ? exp2_approx(sc[g]) : 0.f;
+                if (LISTED) l_lane[g] += my_dup ? 0.f : pr[g];
                 continue;
             }
             const float alpha = exp2_approx(m_run[g] - m_new);
@@ -532,7 +536,7 @@ merge_kernel(const float* __restrict__ part_o, const float* __restrict__ part_ml
     if (dim == 0 && lse) lse[row] = wsum > 0.f ? (M + __log2f(wsum)) * kLn2 : -INFINITY;
 }
 
-template <int D, int GP, bool PAGED, bool UMAX = false>
+template <int D, int GP, bool PAGED, bool UMAX = false, bool LISTED = false>
 struct PartialLauncher {
     // groups of 2..8 run on the tensor cores; single queries on CUDA cores
     static constexpr bool MMA = GP >= 2;
@@ -542,7 +546,7 @@ struct PartialLauncher {
     static constexpr int SMEM = 1024 + STAGES * STAGE + STAGES * 16 + STAGES * 4 + 64;
     static constexpr int RED = CW * 8 * D * 4 + 2 * CW * 8 * 4;
     static_assert(STAGES * STAGE >= RED, "reduction scratch must fit in the ring");
-    static constexpr auto kernel = partial_kernel<D, MMA ? 8 : GP, CW, STAGES, PAGED, MMA, UMAX>;
+    static constexpr auto kernel = partial_kernel<D, MMA ? 8 : GP, CW, STAGES, PAGED, MMA, UMAX, LISTED>;
 
     // Per device: raise the dynamic shared-memory limit once, and remember
     // the occupancy the planner sizes its grids with.
@@ -582,18 +586,19 @@ int ctas_per_sm_dispatch(int G) {
     return PartialLauncher<D, 8, PAGED>::ctas_per_sm();
 }
 
-template <int D, bool PAGED, bool UMAX>
+template <int D, bool PAGED, bool UMAX, bool LISTED>
 cudaError_t launch_dispatch_v(int G, const CUtensorMap& tk, const CUtensorMap& tv, const PartialParams& pp,
                               dim3 grid, cudaStream_t st) {
-    if (G <= 1) return PartialLauncher<D, 1, PAGED, UMAX>::launch(tk, tv, pp, grid, st);
-    return PartialLauncher<D, 8, PAGED, UMAX>::launch(tk, tv, pp, grid, st);
+    if (G <= 1) return PartialLauncher<D, 1, PAGED, UMAX, LISTED>::launch(tk, tv, pp, grid, st);
+    return PartialLauncher<D, 8, PAGED, UMAX, LISTED>::launch(tk, tv, pp, grid, st);
 }
 
 template <int D, bool PAGED>
 cudaError_t launch_dispatch(int G, bool unified, const CUtensorMap& tk, const CUtensorMap& tv,
                             const PartialParams& pp, dim3 grid, cudaStream_t st) {
-    return unified ? launch_dispatch_v<D, PAGED, true>(G, tk, tv, pp, grid, st)
-                   : launch_dispatch_v<D, PAGED, false>(G, tk, tv, pp, grid, st);
+    if (pp.st.listed) return launch_dispatch_v<D, PAGED, false, true>(G, tk, tv, pp, grid, st);
+    return unified ? launch_dispatch_v<D, PAGED, true, false>(G, tk, tv, pp, grid, st)
+                   : launch_dispatch_v<D, PAGED, false, false>(G, tk, tv, pp, grid, st);
 }
 
 }  // namespace
@@ -658,7 +663,7 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream) {
     pp.st.direct = !listed && a.splits == 1 ? 1 : 0;
     pp.st.splits = listed ? a.list_splits : a.splits;
     pp.st.rec0 = a.rec0;
-    pp.st.mark_empty = listed ? 1 : 0;
+    pp.st.listed = listed ? 1 : 0;
     const dim3 grid((unsigned)a.splits, (unsigned)a.Hkv, (unsigned)a.B);
     cudaError_t e;
     const bool u = a.unified != 0;

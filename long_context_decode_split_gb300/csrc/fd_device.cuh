@@ -330,7 +330,9 @@ __device__ __forceinline__ void tok_acc_init(TokAcc<D>& ac) {
 // tensor cores as bf16 hi + lo (~2^-16 relative accuracy); movmatrix turns
 // each 8x8 block of the lane's P values into the B fragment of P^T.  The V
 // tile is stored as 64-row x 128-byte swizzled boxes.
-template <int D>
+// NAN_OUT: a column whose scores so far are all NaN gets NaN weights; without
+// it, it counts as having attended nothing.
+template <int D, bool NAN_OUT = false>
 __device__ __forceinline__ void mma_softmax_pv(TokAcc<D>& ac, const float (&sc)[4], uint32_t vs, unsigned char* vgen,
                                                int warp, int lane, int rows) {
     const int mi = lane >> 3;
@@ -356,10 +358,18 @@ __device__ __forceinline__ void mma_softmax_pv(TokAcc<D>& ac, const float (&sc)[
     const float a0 = none0 ? 1.f : exp2_approx(ac.m.x - m0);
     const float a1 = none1 ? 1.f : exp2_approx(ac.m.y - m1);
     float pr[4];
-    pr[0] = none0 ? 0.f : exp2_approx(sc[0] - m0);
-    pr[1] = none1 ? 0.f : exp2_approx(sc[1] - m1);
-    pr[2] = none0 ? 0.f : exp2_approx(sc[2] - m0);
-    pr[3] = none1 ? 0.f : exp2_approx(sc[3] - m1);
+    if constexpr (NAN_OUT) {
+        const float z0 = none0 ? 0.f : m0, z1 = none1 ? 0.f : m1;
+        pr[0] = exp2_approx(sc[0] - z0);  // 2^-inf = +0
+        pr[1] = exp2_approx(sc[1] - z1);
+        pr[2] = exp2_approx(sc[2] - z0);
+        pr[3] = exp2_approx(sc[3] - z1);
+    } else {
+        pr[0] = none0 ? 0.f : exp2_approx(sc[0] - m0);
+        pr[1] = none1 ? 0.f : exp2_approx(sc[1] - m1);
+        pr[2] = none0 ? 0.f : exp2_approx(sc[2] - m0);
+        pr[3] = none1 ? 0.f : exp2_approx(sc[3] - m1);
+    }
     ac.m = make_float2(m0, m1);
     ac.l.x = ac.l.x * a0 + (pr[0] + pr[2]);
     ac.l.y = ac.l.y * a1 + (pr[1] + pr[3]);
@@ -496,8 +506,9 @@ struct StoreTarget {
     float* part_ml;  // [rows, splits, 2]: (m_i in log2 units, l_i)
     int direct;
     int splits;
-    int rec0 = 0;        // record of chunk 0
-    int mark_empty = 0;  // empty chunks write m = -inf to their record (all D columns of O unwritten)
+    int rec0 = 0;    // record of chunk 0
+    int listed = 0;  // part of a longer list: an empty chunk writes l = 0 to its record (O unwritten), and a
+                     // NaN l is passed on to the merge
 };
 
 // Final step of both combines: red_o/red_m/red_l hold every consumer warp's
@@ -514,7 +525,7 @@ __device__ __forceinline__ void store_combined(unsigned char* smem, int tid, int
 #pragma unroll
         for (int w = 0; w < CW; ++w) M = fmaxf(M, red_m[w * GP + g]);
         float lsum = 0.f, acc = 0.f;
-        if (M != -INFINITY) {
+        if (M != -INFINITY || st.listed) {
 #pragma unroll
             for (int w = 0; w < CW; ++w) {
                 const float mw = red_m[w * GP + g];
@@ -524,7 +535,8 @@ __device__ __forceinline__ void store_combined(unsigned char* smem, int tid, int
             }
         }
         const int row = row0 + g;
-        const float val = lsum > 0.f ? acc / lsum : 0.f;
+        const bool some = st.listed ? lsum != 0.f : lsum > 0.f;
+        const float val = some ? acc / lsum : 0.f;
         if (st.direct) {
             const size_t oi = (size_t)row * D + dim;
             if (st.out_bf16) static_cast<uint16_t*>(st.out)[oi] = f32_to_bf16_bits(val);
@@ -534,7 +546,7 @@ __device__ __forceinline__ void store_combined(unsigned char* smem, int tid, int
             const size_t pi = (size_t)row * st.splits + st.rec0 + split;
             st.part_o[pi * D + dim] = val;
             if (dim == 0) {
-                st.part_ml[2 * pi + 0] = lsum > 0.f ? M : -INFINITY;
+                st.part_ml[2 * pi + 0] = some ? M : -INFINITY;
                 st.part_ml[2 * pi + 1] = lsum;
             }
         }

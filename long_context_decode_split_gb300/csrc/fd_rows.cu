@@ -7,7 +7,7 @@
 // For a row with the visible keys [0, n):
 //   s_j = scale <q, k_j>,  out = sum_j e^(s_j) v_j / sum_j e^(s_j),
 //   lse = ln sum_j e^(s_j)
-// in one pass over the keys: m is the running maximum, l the running sum of
+// (no visible key, or none of weight: out = 0, lse = -inf) in one pass over the keys: m is the running maximum, l the running sum of
 // 2^(s_j log2e - m), and O is rescaled when m moves.  Scores, m, l and O are
 // binary32; the weights are rounded to bf16 (2^-8 relative at most) for the
 // product with V, whose operands have one type, and l takes them unrounded.
@@ -853,17 +853,19 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
             const int head = h * p.G + r - tk * p.G;
             const size_t row = (size_t)(it.q0 + first + tk) * p.Hq + head;
             const size_t rec = row * p.rec_stride + rec_at;
+            // l is 0 only where nothing of weight was seen.  A NaN or +inf score makes it NaN (m skips NaN
+            // and may still be -inf), and that has to pass on to the result: hence no test l > 0.
             float l = ok ? l2.x + l2.y : 0.f;
             auto statistics = [&] {
                 if (!p.direct) {
-                    p.part_ml[2 * rec] = l > 0.f ? m : -INFINITY;
+                    p.part_ml[2 * rec] = m;
                     p.part_ml[2 * rec + 1] = l;
                 } else if (p.lse) {
-                    p.lse[row] = l > 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
+                    p.lse[row] = l != 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
                 }
             };
             // what does not need O goes before the wait for it
-            const float inv_own = l > 0.f ? 1.f / l : 0.f;
+            const float inv_own = l != 0.f ? 1.f / l : 0.f;
             if (DUAL && live) statistics();
             if (ok && rounds > 0) {
                 ok = warp_wait(&o_full[i], o_round & 1u, p.wait_limit_ns);
@@ -891,7 +893,7 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
                     f0 = m0 == -INFINITY ? 0.f : exp2_approx(m0 - m);
                     f1 = m1 == -INFINITY ? 0.f : exp2_approx(m1 - m);
                     l = f0 * l + f1 * l1;
-                    const float inv = l > 0.f ? 1.f / l : 0.f;
+                    const float inv = l != 0.f ? 1.f / l : 0.f;
                     join[r] = f0 *= inv;
                     join[128 + r] = f1 *= inv;
                 }
@@ -970,8 +972,9 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
     }
 }
 
-// Merge of a list of n partials per row (every record written; m = -inf where
+// Merge of a list of n partials per row (every record written; l = 0 where
 // nothing was attended): out = sum_i w_i O_i / sum_i w_i, w_i = 2^(m_i - M) l_i.
+// A NaN l (a NaN score, m = -inf where it saw no other) makes the row NaN.
 // W warps per row (1: eight rows per CTA; 8: one row, the warps taking every
 // eighth record and joining through shared memory), eight records in flight.
 // The records come from L2, and the length of the list bounds it: 10 us of a
@@ -1012,31 +1015,30 @@ merge_list_kernel(const float* __restrict__ part_o, const float* __restrict__ pa
     for (int i = lane; i < n; i += 32) M = fmaxf(M, ml[i].x);
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float top = M == -INFINITY ? 0.f : M;
     float sum = 0.f, acc[E] = {};
-    if (M != -INFINITY) {
-        // this warp's records i = w0 + W j, 32 at a time
-        const int mine = (n - w0 + W - 1) / W;
-        for (int base = 0; base < mine; base += 32) {
-            float w = 0.f;
-            if (base + lane < mine) {
-                const float2 x = ml[w0 + W * (base + lane)];
-                if (x.x != -INFINITY) w = exp2_approx(x.x - M) * x.y;
+    // this warp's records i = w0 + W j, 32 at a time
+    const int mine = (n - w0 + W - 1) / W;
+    for (int base = 0; base < mine; base += 32) {
+        float w = 0.f;
+        if (base + lane < mine) {
+            const float2 x = ml[w0 + W * (base + lane)];
+            if (x.y != 0.f) w = exp2_approx(x.x - top) * x.y;
+        }
+        const int cnt = min(32, mine - base);
+        for (int j = 0; j < cnt; j += AHEAD) {
+            if (base + j > 0) {
+#pragma unroll
+                for (int u = 0; u < AHEAD; ++u)
+                    if (j + u < cnt) load(w0 + W * (base + j + u), v[u]);
             }
-            const int cnt = min(32, mine - base);
-            for (int j = 0; j < cnt; j += AHEAD) {
-                if (base + j > 0) {
 #pragma unroll
-                    for (int u = 0; u < AHEAD; ++u)
-                        if (j + u < cnt) load(w0 + W * (base + j + u), v[u]);
-                }
+            for (int u = 0; u < AHEAD; ++u) {
+                const float wu = __shfl_sync(0xffffffffu, w, (j + u) & 31);
+                if (j + u < cnt && wu != 0.f) {
+                    sum += wu;
 #pragma unroll
-                for (int u = 0; u < AHEAD; ++u) {
-                    const float wu = __shfl_sync(0xffffffffu, w, (j + u) & 31);
-                    if (j + u < cnt && wu != 0.f) {
-                        sum += wu;
-#pragma unroll
-                        for (int e = 0; e < E; ++e) acc[e] += wu * v[u][e];
-                    }
+                    for (int e = 0; e < E; ++e) acc[e] += wu * v[u][e];
                 }
             }
         }
@@ -1054,7 +1056,7 @@ merge_list_kernel(const float* __restrict__ part_o, const float* __restrict__ pa
             for (int e = 0; e < E; ++e) acc[e] += part[u][lane * E + e];
         }
     }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const float inv = sum != 0.f ? 1.f / sum : 0.f;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] *= inv;
     if (out_bf16) {
@@ -1066,7 +1068,7 @@ merge_list_kernel(const float* __restrict__ part_o, const float* __restrict__ pa
 #pragma unroll
         for (int e = 0; e < E; ++e) o[e] = acc[e];
     }
-    if (lane == 0 && lse) lse[row] = sum > 0.f ? (M + __log2f(sum)) * kLn2 : -INFINITY;
+    if (lane == 0 && lse) lse[row] = sum != 0.f ? (M + __log2f(sum)) * kLn2 : -INFINITY;
 }
 
 int rows_tok(int G) { return kRows / G; }
