@@ -505,7 +505,7 @@ FD_API int fd_append_kv_paged(const void* k, const void* v, long long k_stride, 
                               void* k_pages, void* v_pages, int num_pages, int page_size, void* stream);
 
 /* The same into the paged fp8 cache of fd_decode_paged_fp8, each row encoded
- * as by fd_quantize_kv_fp8 (the same bytes). */
+ * as by fd_quantize_kv_fp8 (the same bytes, rows with NaN or infinities too). */
 FD_API int fd_append_kv_paged_fp8(const void* k, const void* v, long long k_stride, long long v_stride,
                                   const int64_t* slots, int T, int Hkv, int d,
                                   uint8_t* k_pages, float* k_page_scales, uint8_t* v_pages, float* v_page_scales,

@@ -352,7 +352,9 @@ __device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
 // multiply-add), q0 + (x - q0 s) r is that quotient (Markstein's theorem; it
 // needs s and 1 / s away from the ends of the range, other rows are divided).
 // The kernel carries -q, whose remainder steps keep the sign of a zero, and
-// flips the codes' signs.  C lanes hold a row, 16 channels each: with 8 the
+// flips the codes' signs.  The maximum skips NaN, as the encoder's does (finite
+// scale, NaN codes where the NaNs are); a lane that holds one divides, since a
+// flipped sign would show in the NaN's code.  C lanes hold a row, 16 channels each: with 8 the
 // pass was bound by its instructions (77 us against the 29 us that the bytes of
 // 31K tokens x 8 heads x 128 need).
 template <int C>
@@ -361,12 +363,21 @@ __device__ __forceinline__ void encode_row(const uint32_t (&w)[8], uint8_t* code
     uint32_t top = w[0] & 0x7fff7fffu;
 #pragma unroll
     for (int e = 1; e < 8; ++e) top = __vmaxu2(top, w[e] & 0x7fff7fffu);
+    const bool has_nan = __vcmpgtu2(top, 0x7f807f80u) != 0u;
+    if (has_nan) {
+        top = 0u;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint32_t x = w[e] & 0x7fff7fffu;
+            top = __vmaxu2(top, x & ~__vcmpgtu2(x, 0x7f807f80u));
+        }
+    }
 #pragma unroll
     for (int o = C / 2; o >= 1; o >>= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
     const float amax = __uint_as_float(max(top << 16, top & 0xffff0000u));
     const float s = amax / 448.0f;
     uint32_t out[4];
-    if (s > 1e-30f && s < 1e30f) {
+    if (s > 1e-30f && s < 1e30f && !has_nan) {
         const float r = 1.0f / s;
         const float2 s2 = make_float2(s, s), nr2 = make_float2(-r, -r);
 #pragma unroll

@@ -1,7 +1,9 @@
-"""Visible scores that are NaN or infinite, in the prompt attention and the
-shared-prefix decode: a NaN or +inf score makes its row NaN (softmax has no
-other answer), a score of -inf weighs nothing, and every other row is what the
-64-bit definition says, however many parts the keys are cut into."""
+"""NaN and infinities: visible scores in the prompt attention and the
+shared-prefix decode, rows of the fp8 append.
+
+A NaN or +inf score makes its row NaN (softmax has no other answer), a score of
+-inf weighs nothing, and every other row is what the 64-bit definition says,
+however many parts the keys are cut into."""
 import math
 
 import pytest
@@ -164,3 +166,31 @@ def test_dense_shared_prefix_overflow(fd, B, bad):
     rows = torch.zeros((B, Hkv * G), dtype=torch.bool, device="cuda")
     rows[0, 1] = True
     expect_nan(fd.fd_decode_dense_shared_prefix(q, kp, vp, k, v, lens), ref, rows)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_append_fp8_writes_the_encoders_bytes(fd, d):
+    # the encoder's maximum skips NaN: a finite scale and one NaN code, nothing at all in a row of NaN;
+    # an infinity makes the scale infinite
+    g = generator(8)
+    T, Hkv = 40, 3
+    rows = randn(g, T, Hkv, d)
+    neg = torch.tensor(-64, dtype=torch.int16, device="cuda").view(torch.bfloat16)  # 0xffc0
+    assert torch.isnan(neg) and torch.signbit(neg)
+    for t, (at, x) in enumerate(((5, NAN), (0, NAN), (d - 1, neg), (16, INF), (3, -INF), (slice(None), NAN), (slice(1, None), NAN),
+                                 (slice(None), INF), (slice(0, 8), neg), (slice(None, None, 2), NAN))):
+        rows[t, 1, at] = x
+    rows[10], rows[10, :, 7] = 0.0, NAN
+    rows[11, 0, 2], rows[11, 0, 9] = INF, NAN
+    rows[12] *= 1e-38
+    rows[12, 2, 4] = NAN
+    rows[13] = 3e38
+    rows[13, 0, 0], rows[13, 1, 40] = NAN, -INF
+    slots = torch.randperm(64, generator=g, device="cuda")[:T]
+    pools = [torch.full((1, Hkv, 64, d), 9, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    scales = [torch.full((1, Hkv, 64), 9.0, device="cuda") for _ in range(2)]
+    fd.fd_append_kv_paged_fp8(rows, rows.flip(0), slots, pools[0], scales[0], pools[1], scales[1])
+    for i, x in enumerate((rows, rows.flip(0))):
+        codes, s = fd.fd_quantize_kv_fp8(x.transpose(0, 1)[None].contiguous())
+        assert torch.equal(pools[i][0, :, slots], codes[0])
+        assert torch.equal(scales[i][0, :, slots].view(torch.int32), s[0].view(torch.int32))
