@@ -482,9 +482,10 @@ FD_API int fd_decode_dense_shared_prefix(const void* q, const void* k_prefix, co
  *                   t = cu_seqlens[b] + i of sequence b, pos = cached_lens[b] + i;
  *                   -1 behind the last new token, up to total_new (a padded batch)
  *   free_head_out[0] = entries of free_pages used up (may be free_head itself)
- * slots [total_new] must be 16-byte aligned.  Where free_pages [num_free] runs
- * out, table entries and slots become -1 and the device status records
- * FD_ERR_OUT_OF_PAGES; lengths below 0, beyond max_pages * 64, or adding up to
+ * slots [total_new] must be 16-byte aligned.  An output may overlap no other
+ * argument, those two cases of the very same buffer apart (FD_ERR_INVALID_ARG).
+ * Where free_pages [num_free] runs out, table entries and slots become -1 and
+ * the device status records FD_ERR_OUT_OF_PAGES; lengths below 0, beyond max_pages * 64, or adding up to
  * more than total_new are cut (slots -1, or not written) and recorded as
  * FD_ERR_INVALID_ARG. */
 FD_API int fd_assign_pages(const int32_t* cached_lens, const int32_t* new_lens, int B,

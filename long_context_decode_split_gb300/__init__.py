@@ -728,7 +728,8 @@ def fd_assign_pages(page_table, cached_lens, new_lens, free_pages, total_new, fr
     free_pages [F] int32 used in order from entry free_head[0] ([1] int32, or
     None = 0), total_new the number of slots.  Returns (seq_lens [B],
     cu_seqlens [B+1], slots [total_new] int64, free_head_out [1]); seq_lens may
-    be cached_lens and free_head_out may be free_head (updated in place)."""
+    be cached_lens and free_head_out may be free_head (updated in place); outputs
+    that overlap anything else are refused."""
     return _binding().assign_pages(page_table, cached_lens, new_lens, free_pages, total_new, free_head, page_size,
                                    seq_lens, cu_seqlens, slots, free_head_out, stream)
 

@@ -778,10 +778,24 @@ int fd_assign_pages(const int32_t* cached_lens, const int32_t* new_lens, int B, 
         !aligned4(free_head) || !aligned4(seq_lens) || !aligned4(cu_seqlens) || !aligned16(slots) ||
         !aligned4(free_head_out))
         return FD_ERR_INVALID_ARG;
-    // the new lengths may replace the old ones, but not shifted against them
-    const uintptr_t in = reinterpret_cast<uintptr_t>(cached_lens), to = reinterpret_cast<uintptr_t>(seq_lens);
-    const uintptr_t bytes = (uintptr_t)B * sizeof(int32_t);
-    if (in != to && in < to + bytes && to < in + bytes) return FD_ERR_INVALID_ARG;
+    // the CTAs read the inputs while others already write: an output may share memory with nothing else,
+    // except the new lengths in place of the old ones and the head in place of the head
+    const struct {
+        const void* at;
+        unsigned long long bytes;
+    } buffers[] = {{page_table, 4ULL * B * max_pages}, {seq_lens, 4ULL * B}, {cu_seqlens, 4ULL * B + 4},
+                   {slots, 8ULL * total_new}, {free_head_out, 4},  // the outputs, then the inputs
+                   {cached_lens, 4ULL * B}, {new_lens, 4ULL * B}, {free_pages, 4ULL * num_free},
+                   {free_head, free_head ? 4ULL : 0ULL}};
+    for (int o = 0; o < 5; ++o) {
+        for (int i = o + 1; i < 9; ++i) {
+            const uintptr_t a = reinterpret_cast<uintptr_t>(buffers[o].at), b = reinterpret_cast<uintptr_t>(buffers[i].at);
+            const bool in_place = a == b && ((o == 1 && i == 5) || (o == 4 && i == 8));
+            if (!in_place && a < b + buffers[i].bytes && b < a + buffers[o].bytes && buffers[i].bytes > 0 &&
+                buffers[o].bytes > 0)
+                return FD_ERR_INVALID_ARG;
+        }
+    }
     fd::AssignArgs a = {cached_lens, new_lens, B, page_table, max_pages, free_pages, num_free, free_head, total_new,
                         seq_lens, cu_seqlens, slots, free_head_out};
     return to_status(fd::launch_assign(a, static_cast<cudaStream_t>(stream)));
