@@ -577,6 +577,10 @@ int shared_entry(fd::RowsArgs& r, fd::DecodeArgs& o, int prefix_len, int L_own, 
     r.part_ml = ml;
     r.rec0 = 0;
     r.rec_stride = pl.list;
+    if (L_own == 0) {  // nobody else looks at the lengths
+        r.check_lens = o.seq_lens;
+        r.check_most = o.L_max;
+    }
     if (L_own > 0 && pl.together) {
         r.own_k = o.k;
         r.own_v = o.v;

@@ -149,6 +149,8 @@ struct RowsArgs {
     const int32_t* cu_k;      // contiguous keys: [B + 1] or null (sequence 0 has all total_k)
     const int32_t* seq_lens;  // pages: [B] keys of each sequence or null (max_pages * 64)
     const int32_t* row_lens;  // [total_q] or null: a further limit on the keys of a query
+    const int32_t* check_lens;// [total_q] or null: reported where outside [0, check_most]
+    int check_most;
     const int32_t* page_table;// [B, table_stride] when paged, else null
     int max_pages, num_pages; // entries of a row that may be read; pages in the pool
     long long table_stride;

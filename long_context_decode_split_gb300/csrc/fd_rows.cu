@@ -28,6 +28,8 @@ struct RowsParams {
     const int32_t* cu_k;
     const int32_t* seq_lens;
     const int32_t* row_lens;
+    const int32_t* check_lens;
+    int check_most;
     const int32_t* page_table;
     int max_pages, num_pages;
     long long table_stride;
@@ -139,6 +141,10 @@ __device__ __forceinline__ int visible_keys(const RowsParams& p, const RowsItem&
     if (it.own) return n;
     if (p.causal) n = min(n, it.Lk - it.Lq + t + 1);
     if (p.row_lens) n = min(n, p.row_lens[it.q0 + t]);
+    if (p.check_lens) {
+        const int len = p.check_lens[it.q0 + t];
+        if (len < 0 || len > p.check_most) atomicOr(&g_status_rows, kStatusBadSeqLen);
+    }
     return max(n, 0);
 }
 
@@ -1124,6 +1130,8 @@ cudaError_t launch_rows(const RowsArgs& a, cudaStream_t stream) {
     p.cu_k = a.cu_k;
     p.seq_lens = a.seq_lens;
     p.row_lens = a.row_lens;
+    p.check_lens = a.check_lens;
+    p.check_most = a.check_most;
     p.page_table = a.page_table;
     p.max_pages = a.max_pages;
     p.num_pages = a.num_pages;
