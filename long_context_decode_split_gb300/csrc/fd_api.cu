@@ -388,7 +388,7 @@ int check_rows(int B, int total_q, int Hq, int Hkv, int max_k, int d, int num_sp
     if (st != FD_OK) return st;
     if (total_q < 0 || total_q > (1 << 30) || num_splits < 0 || num_splits > 65535) return FD_ERR_INVALID_ARG;
     // grid x and the row indices of the tile copies are 32-bit
-    const long long ctas = fd::rows_tiles(B, total_q, Hq / Hkv, max_k, true) * Hkv;
+    const long long ctas = fd::rows_tiles(B, total_q, Hq / Hkv, -1, true) * Hkv;
     if (ctas * (num_splits > 0 ? num_splits : 1) > 0x7fffffffLL) return FD_ERR_UNSUPPORTED;
     return FD_OK;
 }
@@ -406,11 +406,11 @@ int check_rows(int B, int total_q, int Hq, int Hkv, int max_k, int d, int num_sp
 // tokens behind 8192 cached ones 95 us in one, 64 us in two, 82 us in three; 2 x 64
 // behind 32K 339 us in one, 65 us in nine, 78 us in sixteen; 16 x 8 behind 16K to 64K
 // (64 query heads) 458 us in one, 344 us in three, 332 us in seven, 346 us in sixteen.
-RowsPlan prefill_plan(int B, int total_q, int Hq, int Hkv, int max_k, int num_splits) {
+RowsPlan prefill_plan(int B, int total_q, int Hq, int Hkv, int max_k, int num_splits, int packed_k = -1) {
     RowsPlan pl;
     pl.splits = num_splits > 0 ? num_splits : 1;
     pl.chunk = num_splits > 0 ? 128 : 512;
-    const int sms = num_splits > 0 ? 0 : current_sm_count(), per = fd::rows_tokens(B, total_q, Hq / Hkv, max_k);
+    const int sms = num_splits > 0 ? 0 : current_sm_count(), per = fd::rows_tokens(B, total_q, Hq / Hkv, packed_k);
     const long long mean = B > 0 ? (total_q + B - 1) / B : 0;  // tokens of a sequence
     const long long ctas = (long long)B * ((mean + per - 1) / per) * Hkv;
     if (sms <= 0 || ctas <= 0 || ctas >= 2LL * sms) return pl;
@@ -434,6 +434,14 @@ RowsPlan prefill_plan(int B, int total_q, int Hq, int Hkv, int max_k, int num_sp
     return pl;
 }
 
+// The plan of a packed call.  The queries (fd_prefill_num_splits and the workspace
+// size) are not told that a call is packed: it takes no more parts than they say.
+RowsPlan packed_plan(int B, int total_q, int Hq, int Hkv, int total_k, int num_splits) {
+    RowsPlan pl = prefill_plan(B, total_q, Hq, Hkv, total_k, num_splits);
+    pl.splits = std::min(pl.splits, prefill_plan(B, total_q, Hq, Hkv, total_k, num_splits, total_k).splits);
+    return pl;
+}
+
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // A token stride covers the token's heads and keeps 16-byte rows.
@@ -452,7 +460,8 @@ int prefill_entry(fd::RowsArgs& a, int num_splits, int out_dtype, void* workspac
     if (!aligned4(a.lse) || !aligned4(a.cu_q) || !aligned4(a.cu_k) || !aligned4(a.seq_lens) ||
         !aligned4(a.page_table))
         return FD_ERR_INVALID_ARG;
-    const RowsPlan pl = prefill_plan(a.B, a.total_q, a.Hq, a.Hkv, a.max_k, num_splits);
+    const RowsPlan pl = a.cu_k ? packed_plan(a.B, a.total_q, a.Hq, a.Hkv, a.total_k, num_splits)
+                               : prefill_plan(a.B, a.total_q, a.Hq, a.Hkv, a.max_k, num_splits);
     const size_t need = fd::decode_workspace_bytes(a.total_q, a.Hq, a.D, pl.splits);
     if (need > 0) {
         if (!workspace || workspace_bytes < need) return FD_ERR_WORKSPACE_TOO_SMALL;
@@ -493,7 +502,7 @@ struct SharedPlan {
 
 SharedPlan shared_plan_uncached(int B, int Hq, int Hkv, int prefix_len, int L_own, int d, int num_splits) {
     SharedPlan s;
-    s.together = fd::rows_single(1, B, Hq / Hkv, prefix_len);
+    s.together = fd::rows_single(1, B, Hq / Hkv, -1);
     const int blocks = (L_own + 127) / 128;
     // own tokens in pieces of up to 16 blocks, 16 pieces at most (32 sequences, 8 KV heads,
     // up to 4096 own tokens behind 32K: 82 us, 87 us with 8 blocks, 95 us with 32)
@@ -504,7 +513,7 @@ SharedPlan shared_plan_uncached(int B, int Hq, int Hkv, int prefix_len, int L_ow
     const bool short_own = (long long)B * Hkv >= current_sm_count() && L_own <= 32 * kTile;
     s.own = decode_plan(B, Hq, Hkv, L_own, d, short_own ? 1 : 0, true);
     const long long own = s.together && L_own > 0 ? (long long)B * Hkv * s.own_rows.splits : 0;
-    s.shared = shared_rows_plan(fd::rows_tiles(1, B, Hq / Hkv, prefix_len, false) * Hkv, prefix_len, num_splits,
+    s.shared = shared_rows_plan(fd::rows_tiles(1, B, Hq / Hkv, -1, false) * Hkv, prefix_len, num_splits,
                                 s.together ? 4.0 : 14.0, own,
                                 0.5 * blocks / s.own_rows.splits);
     s.list = s.shared.splits + (L_own > 0 ? s.own_splits() : 0);

@@ -166,8 +166,8 @@ struct RowsArgs {
     float* part_ml;           // and [total_q, Hq, rec_stride, 2]
     int rec0, rec_stride;     // (every record of a query row is written, empty ones with m = -inf)
     int direct;               // write out/lse instead of records
-    // Own tokens of a shared-prefix decode, beside the work of single tiles: query token b also attends own_lens[b] - own_skip tokens of its own, in
-    // chunks written to the records own_rec0 + chunk.
+    // Own tokens of a shared-prefix decode, beside the work of single tiles: query token b also attends
+    // own_lens[b] - own_skip tokens of its own, in chunks written to the records own_rec0 + chunk.
     const void* own_k;        // contiguous [total_q, Hkv, own_max, D]; paged: the pools above
     const void* own_v;
     const int32_t* own_lens;  // [total_q] or null (own_max)
@@ -177,11 +177,12 @@ struct RowsArgs {
     int own_splits, own_chunk, own_rec0;  // own_splits == 0: they are someone else's
 };
 // Whether the tokens of this call take one tile per CTA (own tokens are then part of its work).
-bool rows_single(int B, int total_q, int G, int max_k);
+// packed_k: the keys of a packed call (RowsArgs::cu_k given), -1 for others.
+bool rows_single(int B, int total_q, int G, int packed_k);
 // Tiles of `total_q` tokens: how many tokens one takes, and how many tiles there are at most
 // (B sequences by offsets) or exactly (one sequence).
-int rows_tokens(int B, int total_q, int G, int max_k);
-long long rows_tiles(int B, int total_q, int G, int max_k, bool offsets);
+int rows_tokens(int B, int total_q, int G, int packed_k);
+long long rows_tiles(int B, int total_q, int G, int packed_k, bool offsets);
 cudaError_t launch_rows(const RowsArgs& a, cudaStream_t stream);
 cudaError_t rows_status_read(unsigned* bits, bool clear);
 // Merge of n records per row, all of them written (m = -inf: nothing attended).

@@ -1081,12 +1081,13 @@ int rows_tok(int G) { return kRows / G; }
 
 // Two tiles per CTA when the sequences fill more than one on average (64 x 128 tokens
 // behind 2048: 207 us in two, 287 us in one; 64 x 24: 113 and 100 us; between one tile
-// and two within 12% of each other), or when whole prompts (as many keys as queries)
-// have a block of keys on average, which a single tile would leave to one of its
-// pipelines (64 x 24 tokens alone: 19.8 us in two, 24.0 us in one).
-bool rows_dual(int B, int total_q, int G, long long max_k) {
+// and two within 12% of each other), or when packed sequences have a block of keys on
+// average, which a single tile would leave to one of its pipelines (64 x 24 tokens
+// alone: 17.8 us in two, 21.9 us in one; 256 x 16 on 100 keys 51 and 60 us).  packed_k:
+// the keys of a packed call, -1 else.
+bool rows_dual(int B, int total_q, int G, long long packed_k) {
     if (B <= 0) return false;
-    return total_q / B > rows_tok(G) || (max_k == total_q && max_k <= (long long)kBlock * B);
+    return total_q / B > rows_tok(G) || (packed_k >= 0 && packed_k <= (long long)kBlock * B);
 }
 
 template <int D, bool PAGED, bool DUAL>
@@ -1112,14 +1113,14 @@ cudaError_t launch_kernel(const RowsMaps& maps, const RowsParams& p, dim3 grid, 
 
 }  // namespace
 
-bool rows_single(int B, int total_q, int G, int max_k) { return !rows_dual(B, total_q, G, max_k); }
+bool rows_single(int B, int total_q, int G, int packed_k) { return !rows_dual(B, total_q, G, packed_k); }
 
-int rows_tokens(int B, int total_q, int G, int max_k) {
-    return rows_tok(G) * (rows_dual(B, total_q, G, max_k) ? 2 : 1);
+int rows_tokens(int B, int total_q, int G, int packed_k) {
+    return rows_tok(G) * (rows_dual(B, total_q, G, packed_k) ? 2 : 1);
 }
 
-long long rows_tiles(int B, int total_q, int G, int max_k, bool offsets) {
-    const int per = rows_tokens(B, total_q, G, max_k);
+long long rows_tiles(int B, int total_q, int G, int packed_k, bool offsets) {
+    const int per = rows_tokens(B, total_q, G, packed_k);
     return offsets ? (long long)total_q / per + B : ((long long)total_q + per - 1) / per;
 }
 
@@ -1175,7 +1176,8 @@ cudaError_t launch_rows(const RowsArgs& a, cudaStream_t stream) {
         m.k = m.v = m.q;
     }
     m.own_q = m.own_k = m.own_v = m.q;
-    const bool dual = rows_dual(a.B, a.total_q, p.G, a.max_k);
+    const int packed_k = a.cu_k ? a.total_k : -1;
+    const bool dual = rows_dual(a.B, a.total_q, p.G, packed_k);
     const long long own_work = a.own_max > 0 ? (long long)a.total_q * a.Hkv * a.own_splits : 0;
     if (own_work > 0) {
         if (dual) return cudaErrorInvalidValue;
@@ -1195,7 +1197,7 @@ cudaError_t launch_rows(const RowsArgs& a, cudaStream_t stream) {
     p.own_splits = a.own_splits;
     p.own_chunk = a.own_chunk;
     p.own_rec0 = a.own_rec0;
-    const long long tiles = rows_tiles(a.B, a.total_q, p.G, a.max_k, a.cu_q != nullptr);
+    const long long tiles = rows_tiles(a.B, a.total_q, p.G, packed_k, a.cu_q != nullptr);
     p.tiles = (int)tiles;
     // one sequence of keys for all tiles: those of a chunk read it from L2 together
     p.side_by_side = a.cu_q == nullptr;

@@ -1,0 +1,29 @@
+"""Plans of the prompt and shared-prefix calls, as their workspace sizes show them."""
+import pytest
+
+import long_context_decode_split_gb300 as fd
+from long_context_decode_split_gb300 import _build
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    _build.build()
+
+
+def records(B, Hq, Hkv, prefix_len, L_own, d, num_splits=0):
+    """Partial results of a (sequence, query head)."""
+    n = fd.fd_shared_prefix_workspace_size(B, Hq, Hkv, prefix_len, L_own, d, num_splits) - 256
+    assert n > 0 and n % (B * Hq * (d + 2) * 4) == 0
+    return n // (B * Hq * (d + 2) * 4)
+
+
+@pytest.mark.parametrize("prefix_len", [64, 128])
+@pytest.mark.parametrize("G", [1, 2])
+def test_a_batch_as_large_as_the_prefix_is_nothing_special(prefix_len, G):
+    # the own tokens go with the prefix while a tile holds the batch, whatever the prefix's length
+    most = 128 // G
+    for B in range(prefix_len - 1, prefix_len + 2):
+        if B <= most:
+            assert records(B, 2 * G, 2, prefix_len, 1 << 16, 64, 1) == records(B, 2 * G, 2, 1000, 1 << 16, 64, 1) == 17
+        else:
+            assert records(B, 2 * G, 2, prefix_len, 1 << 16, 64, 1) == records(B, 2 * G, 2, 1000, 1 << 16, 64, 1)
