@@ -503,19 +503,26 @@ struct SharedPlan {
 SharedPlan shared_plan_uncached(int B, int Hq, int Hkv, int prefix_len, int L_own, int d, int num_splits) {
     SharedPlan s;
     s.together = fd::rows_single(1, B, Hq / Hkv, -1);
-    const int blocks = (L_own + 127) / 128;
     // own tokens in pieces of up to 16 blocks, 16 pieces at most (32 sequences, 8 KV heads,
     // up to 4096 own tokens behind 32K: 82 us, 87 us with 8 blocks, 95 us with 32)
-    s.own_rows = rows_chunks(L_own, blocks <= 16 ? 1 : blocks < 256 ? (blocks + 15) / 16 : 16, false);
+    const auto own_pieces = [](int L) {
+        const int blocks = (L + 127) / 128;
+        return rows_chunks(L, blocks <= 16 ? 1 : blocks < 256 ? (blocks + 15) / 16 : 16, false);
+    };
+    s.own_rows = own_pieces(L_own);
     // one chunk each while the sequences fill the SMs and are short (128 sequences
     // of up to 1024 own tokens, 8 KV heads: 46.5 us, 60.5 us in the decode's
     // 14-tile chunks)
     const bool short_own = (long long)B * Hkv >= current_sm_count() && L_own <= 32 * kTile;
     s.own = decode_plan(B, Hq, Hkv, L_own, d, short_own ? 1 : 0, true);
-    const long long own = s.together && L_own > 0 ? (long long)B * Hkv * s.own_rows.splits : 0;
+    // L_own is the room of a table, which may be many times what the sequences hold: the
+    // prefix is cut as if they held half of 4096 tokens at most (32 sequences of up to 2048
+    // behind 128K, in a table for 128K more each: 132 us; 1013 us when its whole room counted,
+    // since the prefix then stayed in one part)
+    const int likely = std::min(L_own, 4096), pieces = own_pieces(likely).splits;
     s.shared = shared_rows_plan(fd::rows_tiles(1, B, Hq / Hkv, -1, false) * Hkv, prefix_len, num_splits,
-                                s.together ? 4.0 : 14.0, own,
-                                0.5 * blocks / s.own_rows.splits);
+                                s.together ? 4.0 : 14.0, s.together && L_own > 0 ? (long long)B * Hkv * pieces : 0,
+                                0.5 * ((likely + 127) / 128) / pieces);
     s.list = s.shared.splits + (L_own > 0 ? s.own_splits() : 0);
     return s;
 }
