@@ -503,11 +503,18 @@ struct SharedPlan {
 SharedPlan shared_plan_uncached(int B, int Hq, int Hkv, int prefix_len, int L_own, int d, int num_splits) {
     SharedPlan s;
     s.together = fd::rows_single(1, B, Hq / Hkv, -1);
-    // own tokens in pieces of up to 16 blocks, 16 pieces at most (32 sequences, 8 KV heads,
-    // up to 4096 own tokens behind 32K: 82 us, 87 us with 8 blocks, 95 us with 32)
-    const auto own_pieces = [](int L) {
+    // Own tokens in pieces of up to 16 blocks, 16 pieces at most (32 sequences, 8 KV heads,
+    // up to 4096 own tokens behind 32K: 82 us, 87 us with 8 blocks, 95 us with 32), and no
+    // more than eight for every SM: the kernel cuts what a sequence really holds, and where a
+    // table has room for much more each piece without tokens costs about a microsecond of an
+    // SM (the same with room for 256K each: 78 us, 94 us with 16 pieces; 32 sequences that do
+    // hold 50K on average behind 8K: 932 us, 922 us with 16).
+    const int sms = current_sm_count();
+    const long long units = (long long)B * Hkv;
+    const int most = sms > 0 && units > 0 ? (int)std::min(16LL, std::max(2LL, (8LL * sms + units - 1) / units)) : 16;
+    const auto own_pieces = [most](int L) {
         const int blocks = (L + 127) / 128;
-        return rows_chunks(L, blocks <= 16 ? 1 : blocks < 256 ? (blocks + 15) / 16 : 16, false);
+        return rows_chunks(L, std::max(1, std::min((blocks + 15) / 16, most)), false);
     };
     s.own_rows = own_pieces(L_own);
     // one chunk each while the sequences fill the SMs and are short (128 sequences
@@ -515,11 +522,11 @@ SharedPlan shared_plan_uncached(int B, int Hq, int Hkv, int prefix_len, int L_ow
     // 14-tile chunks)
     const bool short_own = (long long)B * Hkv >= current_sm_count() && L_own <= 32 * kTile;
     s.own = decode_plan(B, Hq, Hkv, L_own, d, short_own ? 1 : 0, true);
-    // L_own is the room of a table, which may be many times what the sequences hold: the
-    // prefix is cut as if they held half of 4096 tokens at most (32 sequences of up to 2048
-    // behind 128K, in a table for 128K more each: 132 us; 1013 us when its whole room counted,
-    // since the prefix then stayed in one part)
-    const int likely = std::min(L_own, 4096), pieces = own_pieces(likely).splits;
+    // L_own is the room of a table, which may be many times what the sequences hold: beyond
+    // 4096 the prefix is cut as if they held 1024 tokens on average (32 sequences of up to 2048
+    // behind 128K, in a table for 128K more each: 1013 us when its whole room counted, since
+    // the prefix then stayed in one part; 112 us, 110 us in a tight table)
+    const int likely = L_own <= 4096 ? L_own : 2048, pieces = own_pieces(likely).splits;
     s.shared = shared_rows_plan(fd::rows_tiles(1, B, Hq / Hkv, -1, false) * Hkv, prefix_len, num_splits,
                                 s.together ? 4.0 : 14.0, s.together && L_own > 0 ? (long long)B * Hkv * pieces : 0,
                                 0.5 * ((likely + 127) / 128) / pieces);
@@ -606,7 +613,7 @@ int shared_entry(fd::RowsArgs& r, fd::DecodeArgs& o, int prefix_len, int L_own, 
         r.own_max = L_own;
         r.own_skip = o.skip_tokens;
         r.own_splits = pl.own_rows.splits;
-        r.own_chunk = pl.own_rows.chunk;
+        r.own_chunk = std::min(pl.own_rows.chunk, 16 * 128);
         r.own_rec0 = pl.shared.splits;
     }
     cudaError_t e = fd::launch_rows(r, s);

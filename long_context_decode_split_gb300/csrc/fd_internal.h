@@ -164,7 +164,7 @@ struct RowsArgs {
     float* lse;
     float* part_o;            // else record rec0 + chunk of rec_stride: [total_q, Hq, rec_stride, D]
     float* part_ml;           // and [total_q, Hq, rec_stride, 2]
-    int rec0, rec_stride;     // (every record of a query row is written, empty ones with m = -inf)
+    int rec0, rec_stride;     // (every record of a query row is written; empty ones get l = 0 and may lack O)
     int direct;               // write out/lse instead of records
     // Own tokens of a shared-prefix decode, beside the work of single tiles: query token b also attends
     // own_lens[b] - own_skip tokens of its own, in chunks written to the records own_rec0 + chunk.
@@ -174,7 +174,7 @@ struct RowsArgs {
     const int32_t* own_table; // paged: [total_q, own_table_stride]
     long long own_table_stride;
     int own_max, own_skip;    // own_max: most own tokens of a sequence
-    int own_splits, own_chunk, own_rec0;  // own_splits == 0: they are someone else's
+    int own_splits, own_chunk, own_rec0;  // equal parts of at least own_chunk; own_splits == 0: they are someone else's
 };
 // Whether the tokens of this call take one tile per CTA (own tokens are then part of its work).
 // packed_k: the keys of a packed call (RowsArgs::cu_k given), -1 for others.
@@ -185,7 +185,7 @@ int rows_tokens(int B, int total_q, int G, int packed_k);
 long long rows_tiles(int B, int total_q, int G, int packed_k, bool offsets);
 cudaError_t launch_rows(const RowsArgs& a, cudaStream_t stream);
 cudaError_t rows_status_read(unsigned* bits, bool clear);
-// Merge of n records per row, all of them written (m = -inf: nothing attended).
+// Merge of n records per row, all of them written (l = 0: nothing attended).
 // cu (or null: all): only the tokens cu[0] .. cu[B] - 1 have records and results.
 cudaError_t launch_merge_list(const float* part_o, const float* part_ml, const int32_t* cu, int B, int tokens, int Hq,
                               int D, int n, void* out, int out_bf16, float* lse, cudaStream_t stream);

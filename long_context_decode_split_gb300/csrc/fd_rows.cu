@@ -357,6 +357,17 @@ __device__ __forceinline__ void store32(void* at, const uint32_t* x, bool wide) 
     }
 }
 
+// A warp writes l = 0 to record `rec` of `tokens` query tokens times a group's
+// heads.  (Unrolled, the loop's code cost long pieces 2%.)
+__device__ __forceinline__ void mark_empty(float* part_ml, int token, int tokens, int G, int h, int Hq, int rec_stride,
+                                        int rec) {
+#pragma unroll 1
+    for (int x = threadIdx.x & 31; x < tokens * G; x += 32) {
+        const size_t row = (size_t)(token + x / G) * Hq + h * G + x % G;
+        reinterpret_cast<float2*>(part_ml)[row * rec_stride + rec] = make_float2(-INFINITY, 0.f);
+    }
+}
+
 // ---- the pass -------------------------------------------------------------------
 //
 // S = Q K^T and O += P V run on tcgen05 with S, P and O in tensor memory.  Two
@@ -490,13 +501,11 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
                     }
                     w.it = own ? own_item(p, place) : find_item(p, p.tiles - 1 - place, TILES * p.tok);
                     some = w.it.t0 >= 0 && w.it.t0 < w.it.Lq;
-                    int chunk = p.own_chunk;
-                    if (!own) {  // equal parts of what the tiles see
-                        int seen = w.it.Lk;
-                        if (p.causal) seen -= w.it.Lq - min(w.it.Lq, w.it.t0 + TILES * p.tok);
-                        const int blocks = (max(seen, 0) + kBlock - 1) / kBlock;
-                        chunk = max(p.chunk, (blocks + splits - 1) / splits * kBlock);
-                    }
+                    // equal parts of what the tiles (or the query token) see
+                    int seen = w.it.Lk;
+                    if (!own && p.causal) seen -= w.it.Lq - min(w.it.Lq, w.it.t0 + TILES * p.tok);
+                    const int blocks = (max(seen, 0) + kBlock - 1) / kBlock;
+                    const int chunk = max(own ? p.own_chunk : p.chunk, (blocks + splits - 1) / splits * kBlock);
                     w.c0 = split * chunk;
                     w.c1 = min(w.it.Lk, w.c0 + chunk);
                     w.rec = (own ? p.own_rec0 : p.rec0) + split;
@@ -508,6 +517,13 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
                         if (p.causal) most = min(most, w.it.Lk - w.it.Lq + first + ntok);
                         most -= w.c0;
                         w.nb[i] = ntok > 0 && most > 0 ? (most + kBlock - 1) / kBlock : 0;
+                    }
+                    // A part behind the end of the keys (a short context in a wide table has many) gets
+                    // l = 0 in its records here; the merge then skips their O.
+                    if (some && (own || split > 0) && w.nb[0] == 0 && w.nb[1] == 0) {
+                        mark_empty(p.part_ml, w.it.q0 + w.it.t0, own ? 1 : min(TILES * p.tok, w.it.Lq - w.it.t0), p.G,
+                                   w.h, p.Hq, p.rec_stride, w.rec);
+                        some = false;
                     }
                 }
                 if (some) {
@@ -978,8 +994,8 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
     }
 }
 
-// Merge of a list of n partials per row (every record written; l = 0 where
-// nothing was attended): out = sum_i w_i O_i / sum_i w_i, w_i = 2^(m_i - M) l_i.
+// Merge of a list of n partials per row (every (m, l) written; l = 0 where
+// nothing was attended, and O then need not be): out = sum_i w_i O_i / sum_i w_i, w_i = 2^(m_i - M) l_i.
 // A NaN l (a NaN score, m = -inf where it saw no other) makes the row NaN.
 // W warps per row (1: eight rows per CTA; 8: one row, the warps taking every
 // eighth record and joining through shared memory), eight records in flight.
@@ -1031,7 +1047,7 @@ merge_list_kernel(const float* __restrict__ part_o, const float* __restrict__ pa
             const float2 x = ml[w0 + W * (base + lane)];
             if (x.y != 0.f) w = exp2_approx(x.x - top) * x.y;
         }
-        const int cnt = min(32, mine - base);
+        const int cnt = 32 - __clz(__ballot_sync(0xffffffffu, w != 0.f));  // up to the last one that counts
         for (int j = 0; j < cnt; j += AHEAD) {
             if (base + j > 0) {
 #pragma unroll

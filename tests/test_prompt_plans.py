@@ -34,12 +34,14 @@ def test_a_batch_as_large_as_the_prefix_is_nothing_special(prefix_len, G):
                                                  (16, 64, 8, 65536)])
 def test_room_in_the_table_does_not_change_the_prefix_plan(B, Hq, Hkv, prefix_len):
     # beyond 4096 tokens a table's room says nothing about the lengths: the prefix keeps its parts
+    import torch
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+
     def own_pieces(L):
-        blocks = -(-L // 128)
-        n = 1 if blocks <= 16 else -(-blocks // 16) if blocks < 256 else 16
+        n = max(1, min(-(-L // 2048), 16, max(2, -(-8 * sms // (B * Hkv)))))
         chunk = -(-(-(-L // n)) // 128) * 128
         return -(-L // chunk)
 
-    want = records(B, Hq, Hkv, prefix_len, 4096, 128) - own_pieces(4096)
-    for room in (8192, 1 << 15, 100032, 1 << 17, 1 << 20):
-        assert records(B, Hq, Hkv, prefix_len, room, 128) - own_pieces(room) == want, room
+    parts = [records(B, Hq, Hkv, prefix_len, room, 128) - own_pieces(room)
+             for room in (4160, 8192, 1 << 15, 100032, 1 << 17, 1 << 20)]
+    assert parts[0] > 1 and len(set(parts)) == 1, parts
