@@ -398,8 +398,9 @@ FD_API int fd_decode_paged_fp4(const void* q, const uint8_t* k_pages, const uint
  *                > 0: the keys that a tile of query tokens sees are cut into
  *                that many equal parts (whole blocks of 128), merged at the end
  *   workspace    fd_prefill_workspace_size(...) bytes, may be NULL when 0
- * max_k is total_k for fd_prefill_packed and max_pages * 64 for
- * fd_prefill_paged. */
+ * max_k is total_k for fd_prefill_packed, which may take fewer parts than
+ * fd_prefill_num_splits says (its sequences share those keys), and max_pages *
+ * 64 for fd_prefill_paged. */
 FD_API int fd_prefill_num_splits(int B, int total_q, int Hq, int Hkv, int max_k, int d, int num_splits);
 FD_API size_t fd_prefill_workspace_size(int B, int total_q, int Hq, int Hkv, int max_k, int d, int num_splits);
 

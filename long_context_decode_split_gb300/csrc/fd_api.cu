@@ -406,11 +406,11 @@ int check_rows(int B, int total_q, int Hq, int Hkv, int max_k, int d, int num_sp
 // tokens behind 8192 cached ones 95 us in one, 64 us in two, 82 us in three; 2 x 64
 // behind 32K 339 us in one, 65 us in nine, 78 us in sixteen; 16 x 8 behind 16K to 64K
 // (64 query heads) 458 us in one, 344 us in three, 332 us in seven, 346 us in sixteen.
-RowsPlan prefill_plan(int B, int total_q, int Hq, int Hkv, int max_k, int num_splits, int packed_k = -1) {
+RowsPlan prefill_plan(int B, int total_q, int Hq, int Hkv, int max_k, int num_splits) {
     RowsPlan pl;
     pl.splits = num_splits > 0 ? num_splits : 1;
     pl.chunk = num_splits > 0 ? 128 : 512;
-    const int sms = num_splits > 0 ? 0 : current_sm_count(), per = fd::rows_tokens(B, total_q, Hq / Hkv, packed_k);
+    const int sms = num_splits > 0 ? 0 : current_sm_count(), per = fd::rows_tokens(B, total_q, Hq / Hkv, -1);
     const long long mean = B > 0 ? (total_q + B - 1) / B : 0;  // tokens of a sequence
     const long long ctas = (long long)B * ((mean + per - 1) / per) * Hkv;
     if (sms <= 0 || ctas <= 0 || ctas >= 2LL * sms) return pl;
@@ -434,11 +434,15 @@ RowsPlan prefill_plan(int B, int total_q, int Hq, int Hkv, int max_k, int num_sp
     return pl;
 }
 
-// The plan of a packed call.  The queries (fd_prefill_num_splits and the workspace
-// size) are not told that a call is packed: it takes no more parts than they say.
+// The plan of a packed call, whose sequences share total_k: no more parts than a
+// sequence of 1.6 times the mean fills (the longest one, if lengths run from a quarter of
+// it up; 6 prompts of 256 tokens, 4 query heads: 9.4 us in the one part that this gives,
+// 15.6 us in three).  The queries (fd_prefill_num_splits and the workspace size) are not
+// told that a call is packed, so it never takes more parts than they say.
 RowsPlan packed_plan(int B, int total_q, int Hq, int Hkv, int total_k, int num_splits) {
     RowsPlan pl = prefill_plan(B, total_q, Hq, Hkv, total_k, num_splits);
-    pl.splits = std::min(pl.splits, prefill_plan(B, total_q, Hq, Hkv, total_k, num_splits, total_k).splits);
+    if (pl.splits > 1 && num_splits == 0)
+        pl.splits = std::min(pl.splits, std::max(1, (int)(1.6 * total_k / B) / pl.chunk));
     return pl;
 }
 

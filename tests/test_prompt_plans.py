@@ -45,3 +45,22 @@ def test_room_in_the_table_does_not_change_the_prefix_plan(B, Hq, Hkv, prefix_le
     parts = [records(B, Hq, Hkv, prefix_len, room, 128) - own_pieces(room)
              for room in (4160, 8192, 1 << 15, 100032, 1 << 17, 1 << 20)]
     assert parts[0] > 1 and len(set(parts)) == 1, parts
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,n,Hq,Hkv", [(6, 256, 4, 1), (4, 400, 4, 1), (3, 512, 2, 1), (10, 300, 1, 1)])
+def test_packed_prompts_shorter_than_a_part_take_one(B, n, Hq, Hkv):
+    # no sequence fills more than one part of 512 keys: the call needs no workspace
+    import ctypes
+    import torch
+    x = torch.randn((B * n, Hq, 64), device="cuda").to(torch.bfloat16)
+    k = x[:, :Hkv].contiguous()
+    cu = torch.arange(B + 1, device="cuda", dtype=torch.int32) * n
+    out = torch.empty_like(x)
+    p = [ctypes.c_void_p(t.data_ptr()) for t in (x, k, cu, out)]
+    st = fd.load().fd_prefill_packed(p[0], p[1], p[1], Hq * 64, Hkv * 64, Hkv * 64, p[2], p[2], B, B * n, B * n, Hq, Hkv,
+                                     64, 0.125, 1, 0, p[3], fd.FD_OUT_BF16, None, None, 0, None)
+    torch.cuda.synchronize()
+    assert st == fd.FD_OK
+    want, _ = fd.fd_prefill_packed(x, k, k, cu, num_splits=1)
+    assert torch.equal(out, want)
