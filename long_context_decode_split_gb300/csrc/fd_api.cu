@@ -604,10 +604,6 @@ int shared_entry(fd::RowsArgs& r, fd::DecodeArgs& o, int prefix_len, int L_own, 
     r.part_ml = ml;
     r.rec0 = 0;
     r.rec_stride = pl.list;
-    if (L_own == 0) {  // nobody else looks at the lengths
-        r.check_lens = o.seq_lens;
-        r.check_most = o.L_max;
-    }
     if (L_own > 0 && pl.together) {
         r.own_k = o.k;
         r.own_v = o.v;
@@ -633,7 +629,9 @@ int shared_entry(fd::RowsArgs& r, fd::DecodeArgs& o, int prefix_len, int L_own, 
         e = fd::launch_decode(o, s);
         if (e != cudaSuccess) return to_status(e);
     }
-    return to_status(fd::launch_merge_list(ws, ml, nullptr, 0, o.B, o.Hq, o.D, pl.list, o.out, out_bf16, o.lse, s));
+    // without own tokens nobody else looks at the lengths
+    return to_status(fd::launch_merge_list(ws, ml, nullptr, 0, o.B, o.Hq, o.D, pl.list, o.out, out_bf16, o.lse, s,
+                                           L_own == 0 ? o.seq_lens : nullptr, o.L_max));
 }
 
 }  // namespace

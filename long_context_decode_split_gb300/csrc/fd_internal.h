@@ -149,8 +149,6 @@ struct RowsArgs {
     const int32_t* cu_k;      // contiguous keys: [B + 1] or null (sequence 0 has all total_k)
     const int32_t* seq_lens;  // pages: [B] keys of each sequence or null (max_pages * 64)
     const int32_t* row_lens;  // [total_q] or null: a further limit on the keys of a query
-    const int32_t* check_lens;// [total_q] or null: reported where outside [0, check_most]
-    int check_most;
     const int32_t* page_table;// [B, table_stride] when paged, else null
     int max_pages, num_pages; // entries of a row that may be read; pages in the pool
     long long table_stride;
@@ -186,9 +184,11 @@ long long rows_tiles(int B, int total_q, int G, int packed_k, bool offsets);
 cudaError_t launch_rows(const RowsArgs& a, cudaStream_t stream);
 cudaError_t rows_status_read(unsigned* bits, bool clear);
 // Merge of n records per row, all of them written (l = 0: nothing attended).
+// lens (or null): [tokens], an entry outside [0, len_most] is recorded in the device status.
 // cu (or null: all): only the tokens cu[0] .. cu[B] - 1 have records and results.
 cudaError_t launch_merge_list(const float* part_o, const float* part_ml, const int32_t* cu, int B, int tokens, int Hq,
-                              int D, int n, void* out, int out_bf16, float* lse, cudaStream_t stream);
+                              int D, int n, void* out, int out_bf16, float* lse, cudaStream_t stream,
+                              const int32_t* lens = nullptr, int len_most = 0);
 
 // Page assignment and cache append (fd_pages.cu).
 struct AssignArgs {

@@ -28,8 +28,6 @@ struct RowsParams {
     const int32_t* cu_k;
     const int32_t* seq_lens;
     const int32_t* row_lens;
-    const int32_t* check_lens;
-    int check_most;
     const int32_t* page_table;
     int max_pages, num_pages;
     long long table_stride;
@@ -141,10 +139,6 @@ __device__ __forceinline__ int visible_keys(const RowsParams& p, const RowsItem&
     if (it.own) return n;
     if (p.causal) n = min(n, it.Lk - it.Lq + t + 1);
     if (p.row_lens) n = min(n, p.row_lens[it.q0 + t]);
-    if (p.check_lens) {
-        const int len = p.check_lens[it.q0 + t];
-        if (len < 0 || len > p.check_most) atomicOr(&g_status_rows, kStatusBadSeqLen);
-    }
     return max(n, 0);
 }
 
@@ -1004,7 +998,8 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
 template <int D, int W>
 __global__ void __launch_bounds__(256)
 merge_list_kernel(const float* __restrict__ part_o, const float* __restrict__ part_ml, const int32_t* __restrict__ cu,
-                  int B, long long rows, int Hq, int n, void* __restrict__ out, int out_bf16, float* __restrict__ lse) {
+                  int B, long long rows, int Hq, int n, void* __restrict__ out, int out_bf16, float* __restrict__ lse,
+                  const int32_t* __restrict__ lens, int len_most) {
     constexpr int E = D / 32;  // channels per lane
     constexpr int AHEAD = 8;
     __shared__ float part[W > 1 ? W : 1][D + 1];
@@ -1017,6 +1012,10 @@ merge_list_kernel(const float* __restrict__ part_o, const float* __restrict__ pa
     if (cu) {
         const int token = (int)(row / Hq);
         if (token < cu[0] || token >= cu[B]) return;
+    }
+    if (lens && lane == 0) {  // lengths that no other part of the call looks at
+        const int len = lens[row / Hq];
+        if (len < 0 || len > len_most) atomicOr(&g_status_rows, kStatusBadSeqLen);
     }
     const float2* ml = reinterpret_cast<const float2*>(part_ml) + row * n;
     const float* po = part_o + row * n * D + lane * E;
@@ -1147,8 +1146,6 @@ cudaError_t launch_rows(const RowsArgs& a, cudaStream_t stream) {
     p.cu_k = a.cu_k;
     p.seq_lens = a.seq_lens;
     p.row_lens = a.row_lens;
-    p.check_lens = a.check_lens;
-    p.check_most = a.check_most;
     p.page_table = a.page_table;
     p.max_pages = a.max_pages;
     p.num_pages = a.num_pages;
@@ -1233,7 +1230,8 @@ cudaError_t launch_rows(const RowsArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_merge_list(const float* part_o, const float* part_ml, const int32_t* cu, int B, int tokens, int Hq,
-                              int D, int n, void* out, int out_bf16, float* lse, cudaStream_t stream) {
+                              int D, int n, void* out, int out_bf16, float* lse, cudaStream_t stream,
+                              const int32_t* lens, int len_most) {
     const long long rows = (long long)tokens * Hq;
     // few rows with long lists leave most of the GPU idle with a warp each (the whole
     // call, 256 rows: 14 records 17.0 us with a warp each, 15.1 us with eight, 9 records 16.9
@@ -1243,7 +1241,8 @@ cudaError_t launch_merge_list(const float* part_o, const float* part_ml, const i
     const dim3 grid((unsigned)(wide ? rows : (rows + 7) / 8));
     const auto kernel = D == 128 ? (wide ? merge_list_kernel<128, 8> : merge_list_kernel<128, 1>)
                                  : (wide ? merge_list_kernel<64, 8> : merge_list_kernel<64, 1>);
-    return launch_pdl(kernel, grid, dim3(256), 0, stream, part_o, part_ml, cu, B, rows, Hq, n, out, out_bf16, lse);
+    return launch_pdl(kernel, grid, dim3(256), 0, stream, part_o, part_ml, cu, B, rows, Hq, n, out, out_bf16, lse,
+                      lens, len_most);
 }
 
 cudaError_t rows_status_read(unsigned* bits, bool clear) {
