@@ -381,10 +381,11 @@ FD_API int fd_decode_paged_fp4(const void* q, const uint8_t* k_pages, const uint
  * that sees no key gets out = 0, lse = -inf.  A visible score that is NaN or
  * +inf makes its row NaN (out and lse); one of -inf weighs nothing.  scale must
  * be finite and > 0.
- * Scores, maxima, sums and outputs are binary32; the weights e^(s - m) enter
- * the product with V as bf16 (relative rounding at most 2^-8), so out carries up to
- * 2^-8 of the weighted mean of |v| in error even as float32; lse does not (its sum takes the
- * weights before that rounding).
+ * Scores, maxima, sums and outputs are binary32.  The weights e^(s - m) enter
+ * the product with V as bf16, and out_dtype chooses how: for FD_OUT_F32 in two
+ * terms (2^-16 relative at most), for FD_OUT_BF16 in one (2^-8), so that bf16
+ * results carry up to 2^-8 of the weighted mean of |v| beside their own rounding.
+ * The sum and lse take the weights before that rounding.
  *   q            [total_q, Hq, d] bf16, tokens q_stride elements apart (a
  *                multiple of 8, at least Hq * d: a slice of a fused projection
  *                works); k_stride, v_stride likewise for k, v
@@ -423,7 +424,8 @@ FD_API int fd_prefill_packed(const void* q, const void* k, const void* v,
  * (fd_append_kv_paged): sequence b has seq_lens[b] keys, its queries are the
  * last ones.  k_pages, v_pages, page_table, seq_lens and page_size as in
  * fd_decode_paged; a bad page's tokens are skipped and reported the same way.
- * One query token per sequence gives fd_decode_paged's result. */
+ * One query token per sequence gives fd_decode_paged's result, to the accuracy
+ * of out_dtype (see above). */
 FD_API int fd_prefill_paged(const void* q, const void* k_pages, const void* v_pages, long long q_stride,
                             const int32_t* page_table, int max_pages, int num_pages,
                             const int32_t* cu_seqlens_q, const int32_t* seq_lens, int page_size,
@@ -437,9 +439,10 @@ FD_API int fd_prefill_paged(const void* q, const void* k_pages, const void* v_pa
  * (every query of the batch against them as one matrix product), each
  * sequence's own tokens apart, and all partial results are joined exactly.
  * The result is that of fd_decode_paged / fd_decode_dense over the whole
- * sequences; weights are bf16, and a NaN or +inf score makes its row NaN (see
- * the prompts above; the other decode calls leave a chunk that holds such a
- * score out).  scale must be finite and > 0.
+ * sequences, weights in two bf16 terms for FD_OUT_F32 and in one for
+ * FD_OUT_BF16 (see the prompts above; the other decode calls always take two).
+ * A NaN or +inf score makes its row NaN (they leave a chunk that holds one
+ * out).  scale must be finite and > 0.
  *   num_splits  chunks of the shared tokens, 0 = planner
  *   workspace   fd_shared_prefix_workspace_size(B, Hq, Hkv, prefix_len, L_own,
  *               d, num_splits) bytes (never 0): prefix_len = prefix_pages * 64

@@ -477,6 +477,7 @@ int prefill_entry(fd::RowsArgs& a, int num_splits, int out_dtype, void* workspac
     a.chunk = pl.chunk;
     a.out_bf16 = out_dtype == FD_OUT_BF16;
     a.direct = pl.splits == 1;
+    a.fine = !a.out_bf16;
     a.rec0 = 0;
     a.rec_stride = pl.splits;
     a.part_o = static_cast<float*>(workspace);
@@ -604,6 +605,7 @@ int shared_entry(fd::RowsArgs& r, fd::DecodeArgs& o, int prefix_len, int L_own, 
     r.part_ml = ml;
     r.rec0 = 0;
     r.rec_stride = pl.list;
+    r.fine = !out_bf16;
     if (L_own > 0 && pl.together) {
         r.own_k = o.k;
         r.own_v = o.v;

@@ -164,6 +164,7 @@ struct RowsArgs {
     float* part_ml;           // and [total_q, Hq, rec_stride, 2]
     int rec0, rec_stride;     // (every record of a query row is written; empty ones get l = 0 and may lack O)
     int direct;               // write out/lse instead of records
+    int fine;                 // weights in two bf16 terms (float32 results)
     // Own tokens of a shared-prefix decode, beside the work of single tiles: query token b also attends
     // own_lens[b] - own_skip tokens of its own, in chunks written to the records own_rec0 + chunk.
     const void* own_k;        // contiguous [total_q, Hkv, own_max, D]; paged: the pools above

@@ -9,9 +9,11 @@
 //   lse = ln sum_j e^(s_j)
 // (no visible key, or none of weight: out = 0, lse = -inf) in one pass over the keys: m is the running maximum, l the running sum of
 // 2^(s_j log2e - m), and O is rescaled when m moves.  Scores, m, l and O are
-// binary32; the weights are rounded to bf16 (2^-8 relative at most) for the
-// product with V, whose operands have one type, and l takes them unrounded.
+// binary32, and l takes the weights unrounded.  The product with V wants both
+// operands of one type, so the weights enter it as bf16: as one term for bf16 results
+// (2^-8 relative at most), as hi + lo for float32 results (2^-16).
 #include <cmath>
+#include <type_traits>
 
 #include "fd_device.cuh"
 #include "fd_internal.h"
@@ -407,7 +409,13 @@ __device__ __forceinline__ void mark_empty(float* part_ml, int token, int tokens
 //     longer.
 //   * few query rows (drafts, a shared prefix): HBM.  16 x 8 drafted tokens of 64
 //     query heads on 16K-64K cached ones 332 us, 6.4 TB/s.
-template <int D, bool PAGED, bool DUAL>
+//
+// FINE (float32 results): weights as hi + lo, both in tensor memory over their S, and a
+// second pass of the same V for lo.  8000 tokens, 32 and 8 heads: 423 us, 318 us with one
+// term; 16 tokens on 16000 keys 133 and 101 us.  bf16 results take one term, whose error is
+// like that of their own rounding; as hi + lo their single tiles would take 372 us
+// instead of 337 (16 x 8 drafted tokens on 16K-64K) and 118 instead of 108 (shared 128K x 32).
+template <int D, bool PAGED, bool DUAL, bool FINE>
 __global__ void __launch_bounds__(kThreads, 1)
 rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
     using Geo = RowsGeo<D, DUAL>;
@@ -677,8 +685,8 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
                 const uint32_t va = desc_cols(ring_at + stage * TILE);
                 if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < kBlock / 16; ++kk)
-                        mma_ts(o_tm, s_tm + kk * 8, va + (kk * 16 * 128 >> 4), IPV, !first || kk > 0);
+                    for (int kk = 0; kk < (FINE ? 2 : 1) * kBlock / 16; ++kk)  // (lo lies behind hi)
+                        mma_ts(o_tm, s_tm + kk * 8, va + (kk % (kBlock / 16) * 16 * 128 >> 4), IPV, !first || kk > 0);
                     mma_commit(&empty[stage]);
                 }
             };
@@ -850,16 +858,18 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
                 const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nb2 = make_float2(-base, -base);
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
-                    uint32_t w[32];
+                    uint32_t w[32], lo[32];
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
                         const int c = 2 * half + e / 16, x = 2 * (e % 16);
                         float2 f = f2fma(make_float2(__uint_as_float(s[c][x]), __uint_as_float(s[c][x + 1])), sc2, nb2);
                         f = make_float2(exp2_approx(f.x), exp2_approx(f.y));
                         l2 = __fadd2_rn(l2, f);
-                        w[e] = pack_bf16(f.x, f.y);
+                        if (FINE) split_bf16(f.x, f.y, w[e], lo[e]);
+                        else w[e] = pack_bf16(f.x, f.y);
                     }
                     tmem_st32(s_at + 32 * half, w);
+                    if (FINE) tmem_st32(s_at + 64 + 32 * half, lo);
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -1105,9 +1115,9 @@ bool rows_dual(int B, int total_q, int G, long long packed_k) {
     return total_q / B > rows_tok(G) || (packed_k >= 0 && packed_k <= (long long)kBlock * B);
 }
 
-template <int D, bool PAGED, bool DUAL>
+template <int D, bool PAGED, bool DUAL, bool FINE>
 cudaError_t launch_kernel(const RowsMaps& maps, const RowsParams& p, dim3 grid, cudaStream_t stream) {
-    constexpr auto kernel = rows_kernel<D, PAGED, DUAL>;
+    constexpr auto kernel = rows_kernel<D, PAGED, DUAL, FINE>;
     constexpr int SMEM = RowsGeo<D, DUAL>::SMEM;
     static bool done[64] = {};
     int dev = 0;
@@ -1217,16 +1227,19 @@ cudaError_t launch_rows(const RowsArgs& a, cudaStream_t stream) {
     injected_timeout(&p.wait_limit_ns, &p.withhold_tile);
     p.shared_work = (int)(tiles * a.Hkv * a.splits);
     const dim3 grid((unsigned)(p.shared_work + own_work));
-    if (a.D == 128) {
-        if (paged) return dual ? launch_kernel<128, true, true>(m, p, grid, stream)
-                               : launch_kernel<128, true, false>(m, p, grid, stream);
-        return dual ? launch_kernel<128, false, true>(m, p, grid, stream)
-                    : launch_kernel<128, false, false>(m, p, grid, stream);
-    }
-    if (paged) return dual ? launch_kernel<64, true, true>(m, p, grid, stream)
-                           : launch_kernel<64, true, false>(m, p, grid, stream);
-    return dual ? launch_kernel<64, false, true>(m, p, grid, stream)
-                : launch_kernel<64, false, false>(m, p, grid, stream);
+    const auto launch = [&](auto d, auto pages) {
+        constexpr int D = decltype(d)::value;
+        constexpr bool P = decltype(pages)::value;
+        if (dual) return a.fine ? launch_kernel<D, P, true, true>(m, p, grid, stream)
+                                : launch_kernel<D, P, true, false>(m, p, grid, stream);
+        return a.fine ? launch_kernel<D, P, false, true>(m, p, grid, stream)
+                      : launch_kernel<D, P, false, false>(m, p, grid, stream);
+    };
+    using std::integral_constant;
+    if (a.D == 128) return paged ? launch(integral_constant<int, 128>(), std::true_type())
+                                 : launch(integral_constant<int, 128>(), std::false_type());
+    return paged ? launch(integral_constant<int, 64>(), std::true_type())
+                 : launch(integral_constant<int, 64>(), std::false_type());
 }
 
 cudaError_t launch_merge_list(const float* part_o, const float* part_ml, const int32_t* cu, int B, int tokens, int Hq,
