@@ -1131,14 +1131,15 @@ int fd_debug_inject_wait_timeout(unsigned long long wait_limit_ns, int withhold_
 
 int fd_device_status(int clear, void* stream) {
     if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return FD_ERR_CUDA;
-    unsigned a = 0, b = 0, c = 0, e = 0, r = 0, g = 0;
+    unsigned a = 0, b = 0, c = 0, e = 0, r = 0, m = 0, g = 0;
     if (fd::decode_status_read(&a, clear != 0) != cudaSuccess) return FD_ERR_CUDA;
     if (fd::topdelta_status_read(&b, clear != 0) != cudaSuccess) return FD_ERR_CUDA;
     if (fd::fp8_status_read(&c, clear != 0) != cudaSuccess) return FD_ERR_CUDA;
     if (fd::fp4_status_read(&e, clear != 0) != cudaSuccess) return FD_ERR_CUDA;
     if (fd::rows_status_read(&r, clear != 0) != cudaSuccess) return FD_ERR_CUDA;
+    if (fd::merge_status_read(&m, clear != 0) != cudaSuccess) return FD_ERR_CUDA;
     if (fd::pages_status_read(&g, clear != 0) != cudaSuccess) return FD_ERR_CUDA;
-    const unsigned bits = a | b | c | e | r | g;
+    const unsigned bits = a | b | c | e | r | m | g;
     if (bits & 2u) return FD_ERR_DEVICE_TIMEOUT;
     if (bits & 1u) return FD_ERR_BAD_PAGE_TABLE;
     if (bits & 8u) return FD_ERR_OUT_OF_PAGES;

@@ -184,12 +184,13 @@ int rows_tokens(int B, int total_q, int G, int packed_k);
 long long rows_tiles(int B, int total_q, int G, int packed_k, bool offsets);
 cudaError_t launch_rows(const RowsArgs& a, cudaStream_t stream);
 cudaError_t rows_status_read(unsigned* bits, bool clear);
-// Merge of n records per row, all of them written (l = 0: nothing attended).
+// Merge (fd_merge.cu) of n records per row, all of them written (l = 0: nothing attended).
 // lens (or null): [tokens], an entry outside [0, len_most] is recorded in the device status.
 // cu (or null: all): only the tokens cu[0] .. cu[B] - 1 have records and results.
 cudaError_t launch_merge_list(const float* part_o, const float* part_ml, const int32_t* cu, int B, int tokens, int Hq,
                               int D, int n, void* out, int out_bf16, float* lse, cudaStream_t stream,
                               const int32_t* lens = nullptr, int len_most = 0);
+cudaError_t merge_status_read(unsigned* bits, bool clear);
 
 // Page assignment and cache append (fd_pages.cu).
 struct AssignArgs {
