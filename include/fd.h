@@ -441,8 +441,8 @@ FD_API int fd_prefill_paged(const void* q, const void* k_pages, const void* v_pa
  * The result is that of fd_decode_paged / fd_decode_dense over the whole
  * sequences, weights in two bf16 terms for FD_OUT_F32 and in one for
  * FD_OUT_BF16 (see the prompts above; the other decode calls always take two).
- * A NaN or +inf score makes its row NaN (they leave a chunk that holds one
- * out).  scale must be finite and > 0.
+ * A NaN or +inf score makes its row NaN (they leave that key, or the chunk that
+ * holds it, out).  scale must be finite and > 0.
  *   num_splits  chunks of the shared tokens, 0 = planner
  *   workspace   fd_shared_prefix_workspace_size(B, Hq, Hkv, prefix_len, L_own,
  *               d, num_splits) bytes (never 0): prefix_len = prefix_pages * 64

@@ -143,7 +143,7 @@ __device__ __forceinline__ void mma_consume_tile_unified(TokAcc<D>& ac, bool& un
 
 // LISTED: the chunks of a shared-prefix decode's own tokens.  They are records of a
 // longer list (StoreTarget::listed), and a NaN score makes the result NaN; the other
-// passes answer as they always did (a NaN score attends nothing).
+// passes leave that key, or the whole chunk, out.
 template <int D, int GP, int CW, int STAGES, bool PAGED, bool MMA, bool UMAX, bool LISTED>
 __global__ void __launch_bounds__((CW + 1) * 32, (MMA || GP < 8) ? 2 : 1)
 partial_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,

@@ -521,8 +521,9 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
                         w.nb[i] = ntok > 0 && most > 0 ? (most + kBlock - 1) / kBlock : 0;
                     }
                     // A part behind the end of the keys (a short context in a wide table has many) gets
-                    // l = 0 in its records here; the merge then skips their O.
-                    if (some && (own || split > 0) && w.nb[0] == 0 && w.nb[1] == 0) {
+                    // l = 0 in its records here; the merge then skips their O.  (Every 256th is handed on:
+                    // the other warps wait for work with a time limit.)
+                    if (some && (own || split > 0) && w.nb[0] == 0 && w.nb[1] == 0 && (asked & 255) != 255) {
                         mark_empty(p.part_ml, w.it.q0 + w.it.t0, own ? 1 : min(TILES * p.tok, w.it.Lq - w.it.t0), p.G,
                                    w.h, p.Hq, p.rec_stride, w.rec);
                         some = false;

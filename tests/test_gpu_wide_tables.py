@@ -62,3 +62,22 @@ def test_shared_prefix(fd, lens, G, d):
         check_rows(out[b:b + 1], lse[b:b + 1], attend64(q[b:b + 1], k, v, torch.tensor([n]), 1 / math.sqrt(d)),
                    f"sequence {b} of {n} tokens")
     assert fd.fd_device_status(clear=True) == fd.FD_OK
+
+
+def test_a_long_run_of_empty_parts_is_no_time_out(fd):
+    # 8 heads x 65535 parts, one of each with keys: some 3400 empty parts in a row on every SM take about 3 ms.  The
+    # warps that wait for work meanwhile hear from the copy warp often enough for a limit of 1 ms.
+    g = generator(3)
+    T, H, d = 4, 8, 64
+    q, k, v = randn(g, T, H, d), randn(g, T, H, d), randn(g, T, H, d)
+    cu = offsets([T])
+    ws = torch.empty(fd.fd_prefill_workspace_size(1, T, H, H, T, d, 65535), dtype=torch.uint8, device="cuda")
+    fd.fd_prefill_packed(q, k, v, cu, num_splits=65535, workspace=ws)
+    assert fd.fd_device_status(clear=True) == fd.FD_OK
+    try:
+        fd.fd_debug_inject_wait_timeout(1_000_000, -1)
+        out, lse = fd.fd_prefill_packed(q, k, v, cu, num_splits=65535, workspace=ws)
+        assert fd.fd_device_status(clear=True) == fd.FD_OK
+    finally:
+        fd.fd_debug_inject_wait_timeout(0, -1)
+    check_rows(out, lse, attend64(q, k, v, limits(T, T, True), 1 / math.sqrt(d)))
