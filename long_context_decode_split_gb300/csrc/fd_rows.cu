@@ -522,8 +522,9 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
                     }
                     // A part behind the end of the keys (a short context in a wide table has many) gets
                     // l = 0 in its records here; the merge then skips their O.  (Every 256th is handed on:
-                    // the other warps wait for work with a time limit.)
-                    if (some && (own || split > 0) && w.nb[0] == 0 && w.nb[1] == 0 && (asked & 255) != 255) {
+                    // the other warps wait for work with a time limit.  So are those of two tiles, whose
+                    // contexts have fewer parts: the code alone cost 512 tokens 0.3 of 11.8 us.)
+                    if (!DUAL && some && (own || split > 0) && w.nb[0] == 0 && w.nb[1] == 0 && (asked & 255) != 255) {
                         mark_empty(p.part_ml, w.it.q0 + w.it.t0, own ? 1 : min(TILES * p.tok, w.it.Lq - w.it.t0), p.G,
                                    w.h, p.Hq, p.rec_stride, w.rec);
                         some = false;
@@ -974,11 +975,13 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
                 }
             } else {
                 float* dst = p.direct ? static_cast<float*>(p.out) + row * D : p.part_o + rec * D;
+                // the merge skips records with l = 0 (of a single tile, only pipeline 0 knows the joined l)
+                const bool wanted = live && (p.direct || (DUAL ? l != 0.f : f0 != 0.f || f1 != 0.f));
 #pragma unroll 1
                 for (int c = c_mine; c < c_mine + MINE; c += 32) {
                     float f[32];
                     channels(c, f);
-                    if (!live) continue;
+                    if (!wanted) continue;
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         store32(dst + c + 8 * e, reinterpret_cast<uint32_t*>(f) + 8 * e, p.wide);
