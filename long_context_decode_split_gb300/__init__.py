@@ -681,7 +681,10 @@ def fd_prefill_packed(q, k, v, cu_seqlens_q, cu_seqlens_k=None, scale=None, caus
     """Attention of whole prompts packed one behind the other.  q [Tq,Hq,d],
     k, v [Tk,Hkv,d] bf16 (tokens may be strided), cu_seqlens_q [B+1] int32,
     cu_seqlens_k [B+1] or None (= cu_seqlens_q).  Returns (out [Tq,Hq,d],
-    lse [Tq,Hq] or None); rows of no sequence are not written."""
+    lse [Tq,Hq] or None); rows of no sequence are not written.  The weights
+    enter the product with v in one bf16 term (2^-8) for bf16 outputs, in two
+    (2^-16) for float32 ones; so in fd_prefill_paged and the shared-prefix
+    decodes."""
     return _binding().prefill_packed(q, k, v, cu_seqlens_q, cu_seqlens_k, scale, causal, num_splits, out, lse,
                                      _code(out_dtype), want_lse, workspace, stream)
 

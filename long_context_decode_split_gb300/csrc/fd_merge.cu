@@ -12,7 +12,8 @@ __device__ unsigned int g_status_merge;
 namespace {
 
 // Merge of a list of n partials per row (every (m, l) written; l = 0 where
-// nothing was attended, and O then need not be): out = sum_i w_i O_i / sum_i w_i, w_i = 2^(m_i - M) l_i.
+// nothing was attended, and O then need not be): out = sum_i w_i O_i / sum_i w_i,
+// w_i = 2^(m_i - M) l_i.
 // A NaN l (a NaN score, m = -inf where it saw no other) makes the row NaN.
 // W warps per row (1: eight rows per CTA; 8: one row, the warps taking every
 // eighth record and joining through shared memory), eight records in flight.

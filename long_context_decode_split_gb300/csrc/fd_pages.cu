@@ -354,9 +354,10 @@ __device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi) {
 // The kernel carries -q, whose remainder steps keep the sign of a zero, and
 // flips the codes' signs.  The maximum skips NaN, as the encoder's does (finite
 // scale, NaN codes where the NaNs are); a lane that holds one divides, since a
-// flipped sign would show in the NaN's code.  C lanes hold a row, 16 channels each: with 8 the
-// pass was bound by its instructions (77 us against the 29 us that the bytes of
-// 31K tokens x 8 heads x 128 need).
+// flipped sign would show in the NaN's code (the whole test moved into the dividing
+// branch: 31.3 us).  C lanes hold a row, 16 channels each: with 8 the pass was bound
+// by its instructions (77 us against the 29 us that the bytes of 31K tokens x 8
+// heads x 128 need).
 template <int C>
 __device__ __forceinline__ void encode_row(const uint32_t (&w)[8], uint8_t* codes, float* scale, bool live, int c) {
     // magnitudes of bf16 order like unsigned integers
@@ -407,8 +408,8 @@ __device__ __forceinline__ void load16(uint32_t (&w)[8], const uint16_t* x) {
     w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
 }
 
-// HBM bounds it: 31K tokens x 8 heads x 128 in 29.8 us, 6.5 TB/s (35.5 us with the
-// rows loaded after their slots).
+// HBM bounds it: 31K tokens x 8 heads x 128 in 30.4 us, 6.4 TB/s (29.9 us before it
+// looked for NaN; 35.5 us with the rows loaded after their slots).
 template <int D>
 __global__ void __launch_bounds__(256) append_fp8_kernel(const AppendParams p) {
     constexpr int C = D / 16;
@@ -451,10 +452,11 @@ constexpr int kSlotsHere = 32768;
 constexpr int kPagesAlone = 2048, kSlotsAlone = 2048;
 // Otherwise a CTA per so many tokens and pages, a thread each, up to one CTA per SM
 // (131072 tokens: 4.0 us, 5.6 us with 4096 and 4.0 us with 512 per CTA).  512 prompts
-// with a million new tokens take 8.2 us, 11.5 us in the two launches of a call in place;
-// their 8.8 MB would pass HBM in 1.3 us; searches and page look-ups take 3.5 us of it,
-// the stores 1 us, the launch, lengths and sums 3.7 us (two tokens a thread 9.15 us; a
-// run of tokens per CTA that keeps its sequence 9.6 us).
+// with a million new tokens take 8.2 us on the GPU (a run of calls in a graph; 8.4 us a
+// call into given outputs, 11.7 to 12.2 us when the call allocates them), 11.5 us in the
+// two launches of a call in place; their 8.8 MB would pass HBM in 1.3 us; searches and
+// page look-ups take 3.5 us of it, the stores 1 us, the launch, lengths and sums 3.7 us
+// (two tokens a thread 9.15 us; a run of tokens per CTA that keeps its sequence 9.6 us).
 constexpr int kPerCta = 1024;
 
 cudaError_t launch_assign(const AssignArgs& a, cudaStream_t stream) {

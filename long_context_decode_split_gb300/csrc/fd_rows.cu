@@ -7,11 +7,12 @@
 // For a row with the visible keys [0, n):
 //   s_j = scale <q, k_j>,  out = sum_j e^(s_j) v_j / sum_j e^(s_j),
 //   lse = ln sum_j e^(s_j)
-// (no visible key, or none of weight: out = 0, lse = -inf) in one pass over the keys: m is the running maximum, l the running sum of
-// 2^(s_j log2e - m), and O is rescaled when m moves.  Scores, m, l and O are
-// binary32, and l takes the weights unrounded.  The product with V wants both
-// operands of one type, so the weights enter it as bf16: as one term for bf16 results
-// (2^-8 relative at most), as hi + lo for float32 results (2^-16).
+// (no visible key, or none of weight: out = 0, lse = -inf) in one pass over the
+// keys: m is the running maximum, l the running sum of 2^(s_j log2e - m), and O is
+// rescaled when m moves.  Scores, m, l and O are binary32, and l takes the weights
+// unrounded.  The product with V wants both operands of one type, so the weights
+// enter it as bf16: as one term for bf16 results (2^-8 relative at most), as
+// hi + lo for float32 results (2^-16).
 #include <cmath>
 #include <type_traits>
 
@@ -1088,7 +1089,8 @@ cudaError_t launch_rows(const RowsArgs& a, cudaStream_t stream) {
     if (!make_token_map(&m.q, a.q, a.D, a.Hq, a.total_q, a.D, a.q_stride, p.G, p.tok)) return cudaErrorInvalidValue;
     bool ok = true;
     if (paged && pool_rows > 0) {
-        ok = make_row_map(&m.k, a.k, pool_rows, (uint32_t)a.D * 2) && make_row_map(&m.v, a.v, pool_rows, (uint32_t)a.D * 2);
+        ok = make_row_map(&m.k, a.k, pool_rows, (uint32_t)a.D * 2) &&
+             make_row_map(&m.v, a.v, pool_rows, (uint32_t)a.D * 2);
     } else if (paged) {  // an empty pool: nothing is read, any well-formed map will do
         ok = make_row_map(&m.k, a.q, 1, (uint32_t)a.D * 2);
         m.v = m.k;

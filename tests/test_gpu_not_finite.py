@@ -177,8 +177,9 @@ def test_append_fp8_writes_the_encoders_bytes(fd, d):
     rows = randn(g, T, Hkv, d)
     neg = torch.tensor(-64, dtype=torch.int16, device="cuda").view(torch.bfloat16)  # 0xffc0
     assert torch.isnan(neg) and torch.signbit(neg)
-    for t, (at, x) in enumerate(((5, NAN), (0, NAN), (d - 1, neg), (16, INF), (3, -INF), (slice(None), NAN), (slice(1, None), NAN),
-                                 (slice(None), INF), (slice(0, 8), neg), (slice(None, None, 2), NAN))):
+    for t, (at, x) in enumerate(((5, NAN), (0, NAN), (d - 1, neg), (16, INF), (3, -INF), (slice(None), NAN),
+                                 (slice(1, None), NAN), (slice(None), INF), (slice(0, 8), neg),
+                                 (slice(None, None, 2), NAN))):
         rows[t, 1, at] = x
     rows[10], rows[10, :, 7] = 0.0, NAN
     rows[11, 0, 2], rows[11, 0, 9] = INF, NAN

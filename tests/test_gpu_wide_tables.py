@@ -18,8 +18,9 @@ def widen(table, room):
 
 
 @pytest.mark.parametrize("causal", [True, False])
-@pytest.mark.parametrize("new,ctx,Hq,Hkv,d", [([16, 3, 0, 1], [1000, 0, 70, 2000], 8, 2, 128), ([1] * 8, [2000] * 8, 32, 8, 128),
-                                              ([100, 90], [500, 40], 8, 2, 64), ([300], [4000], 6, 2, 128)], ids=str)
+@pytest.mark.parametrize("new,ctx,Hq,Hkv,d", [([16, 3, 0, 1], [1000, 0, 70, 2000], 8, 2, 128),
+                                              ([1] * 8, [2000] * 8, 32, 8, 128), ([100, 90], [500, 40], 8, 2, 64),
+                                              ([300], [4000], 6, 2, 128)], ids=str)
 def test_paged_prompts(fd, new, ctx, Hq, Hkv, d, causal):
     g = generator(len(new))
     total = [n + c for n, c in zip(new, ctx)]

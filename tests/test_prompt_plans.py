@@ -30,8 +30,8 @@ def test_a_batch_as_large_as_the_prefix_is_nothing_special(prefix_len, G):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("B,Hq,Hkv,prefix_len", [(8, 32, 8, 8192), (32, 32, 8, 131072), (32, 32, 8, 32768), (4, 8, 2, 2048),
-                                                 (16, 64, 8, 65536)])
+@pytest.mark.parametrize("B,Hq,Hkv,prefix_len", [(8, 32, 8, 8192), (32, 32, 8, 131072), (32, 32, 8, 32768),
+                                                 (4, 8, 2, 2048), (16, 64, 8, 65536)])
 def test_room_in_the_table_does_not_change_the_prefix_plan(B, Hq, Hkv, prefix_len):
     # beyond 4096 tokens a table's room says nothing about the lengths: the prefix keeps its parts
     import torch
@@ -58,8 +58,8 @@ def test_packed_prompts_shorter_than_a_part_take_one(B, n, Hq, Hkv):
     cu = torch.arange(B + 1, device="cuda", dtype=torch.int32) * n
     out = torch.empty_like(x)
     p = [ctypes.c_void_p(t.data_ptr()) for t in (x, k, cu, out)]
-    st = fd.load().fd_prefill_packed(p[0], p[1], p[1], Hq * 64, Hkv * 64, Hkv * 64, p[2], p[2], B, B * n, B * n, Hq, Hkv,
-                                     64, 0.125, 1, 0, p[3], fd.FD_OUT_BF16, None, None, 0, None)
+    st = fd.load().fd_prefill_packed(p[0], p[1], p[1], Hq * 64, Hkv * 64, Hkv * 64, p[2], p[2], B, B * n, B * n, Hq,
+                                     Hkv, 64, 0.125, 1, 0, p[3], fd.FD_OUT_BF16, None, None, 0, None)
     torch.cuda.synchronize()
     assert st == fd.FD_OK
     want, _ = fd.fd_prefill_packed(x, k, k, cu, num_splits=1)
