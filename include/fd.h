@@ -516,6 +516,121 @@ FD_API int fd_append_kv_paged_fp8(const void* k, const void* v, long long k_stri
                                   uint8_t* k_pages, float* k_page_scales, uint8_t* v_pages, float* v_page_scales,
                                   int num_pages, int page_size, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Norms and rotation of query and key heads, and the same on the way into the
+ * paged cache.  For a head x of n channels at position t:
+ *   y = x / sqrt(mean(x^2) + norm_eps) * w         (with a weight w; else y = x)
+ *   (y_a, y_b) <- (y_a cos_i - y_b sin_i, y_b cos_i + y_a sin_i)
+ * for the pairs i = 0 .. rot/2 - 1 of its first `rot` channels: a = i, b = i +
+ * rot/2, or with `interleaved` a = 2i, b = 2i + 1.  All of it in binary32, rounded
+ * once at the end. */
+typedef struct fd_rope {
+    const float* cos_sin;       /* [max_pos, rot]: row t holds the rot/2 cosines, then the sines; 16-byte aligned */
+    int max_pos;
+    int rot;                    /* a multiple of 16, at most a head's channels */
+    int interleaved;
+    int halves;                 /* != 0: each half of a row of d is a head of its own (differential attention) */
+    const int32_t* positions;   /* [T]: token t's row of the table, < 0: the token is left out; or NULL, then */
+    const int32_t* cu_seqlens;  /* [B + 1] and */
+    const int32_t* seq_lens;    /* [B], as fd_assign_pages returns them: the last new token of sequence b is at
+                                   seq_lens[b] - 1; tokens of no sequence are left out */
+    int B;
+    const float* q_weight;      /* [d] (halves: [d/2]), 16-byte aligned, or NULL: queries without norm */
+    const float* k_weight;      /* the same for the keys */
+    float norm_eps;             /* > 0 where there is a weight */
+} fd_rope;
+
+/* Rows to rows: q [T, Hq, d] to q_out, k [T, Hkv, d] to k_out, bf16, tokens the
+ * strides apart (elements, multiples of 8: slices of a fused projection work).
+ * Hkv = 0: queries alone.  q_out may be q itself (the same address and stride),
+ * k_out k; any other overlap is refused (FD_ERR_INVALID_ARG), but slices of the same
+ * rows with columns of their own do not count as one.  Tokens left out
+ * are not written.  A position outside the table takes its nearest row and is
+ * recorded in the device status (FD_ERR_INVALID_ARG), like offsets that run
+ * backwards or out of [0, T].  d must be 64 or 128, rot a multiple of 16
+ * (FD_ERR_UNSUPPORTED). */
+FD_API int fd_norm_rope(const void* q, const void* k, long long q_stride, long long k_stride,
+                        int T, int Hq, int Hkv, int d, const fd_rope* rope,
+                        void* q_out, void* k_out, long long q_out_stride, long long k_out_stride, void* stream);
+
+/* fd_append_kv_paged with that on the way: queries to q_out, keys turned to their
+ * slots, values as they are to theirs, in one launch.  slots, pools and
+ * page_size as fd_append_kv_paged; a token left out, or with a negative slot,
+ * leaves its cache rows as they were (with a negative slot its query is turned all the
+ * same).  Hq = 0: keys and values alone. */
+FD_API int fd_append_kv_paged_rope(const void* q, const void* k, const void* v,
+                                   long long q_stride, long long k_stride, long long v_stride,
+                                   const int64_t* slots, int T, int Hq, int Hkv, int d, const fd_rope* rope,
+                                   void* q_out, long long q_out_stride,
+                                   void* k_pages, void* v_pages, int num_pages, int page_size, void* stream);
+
+/* The same into the paged fp8 cache: value rows as fd_append_kv_paged_fp8 encodes
+ * them, key rows from their turned binary32 values by the same rule, s = max |y| / 448
+ * and e4m3(y / s): one rounding. */
+FD_API int fd_append_kv_paged_rope_fp8(const void* q, const void* k, const void* v,
+                                       long long q_stride, long long k_stride, long long v_stride,
+                                       const int64_t* slots, int T, int Hq, int Hkv, int d, const fd_rope* rope,
+                                       void* q_out, long long q_out_stride,
+                                       uint8_t* k_pages, float* k_page_scales, uint8_t* v_pages,
+                                       float* v_page_scales, int num_pages, int page_size, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Differential attention: the difference of two softmax maps.  A query or key
+ * row of d channels is [first half | second half]; with
+ *   s1_j = scale * <q1, k1_j>,  s2_j = scale * <q2, k2_j>   (halves of d/2 channels)
+ *   o = sum_j softmax(s1)_j v_j - lambda * sum_j softmax(s2)_j v_j
+ *   y = o / sqrt(mean(o^2) + norm_eps) * norm_weight    (with a weight; else y = o)
+ * over value rows of d channels: the caches and pools are those of the other
+ * calls (bf16), and so are their page tables, lengths and offsets.
+ *   scale         finite and > 0 (usually 1 / sqrt(d/2))
+ *   lambda        float32: of token t (decode: sequence t) and query head h
+ *                 lambda[t * lambda_stride + h]; lambda_stride 0 = one value per
+ *                 head for all tokens, else at least Hq
+ *   norm_weight   [d] float32, 16-byte aligned, or NULL; norm_eps > 0 with it
+ *   out           as the calls without _diff
+ *   lse           [tokens, Hq, 2] float32 or NULL: of either map
+ * A query that sees no key gets out = 0 and lse = -inf.  A visible score that is NaN
+ * or +inf makes its row NaN; one of -inf weighs nothing.  Values that a query sees
+ * have to be finite.
+ * Scores, maxima, sums, the maps' outputs, their difference and its norm are
+ * binary32.  The weights of either map enter the product with V as the other calls'
+ * do: in two bf16 terms in the decode (2^-16), and in the prompt calls in two
+ * for FD_OUT_F32 and one for FD_OUT_BF16 (2^-8).  Where the maps nearly cancel,
+ * such errors of either map are large beside what is left of them, and the norm
+ * scales both: float32 results keep them small.
+ * Workspace: fd_decode_diff_workspace_size and fd_prefill_diff_workspace_size, with
+ * the arguments of fd_decode_workspace_size and fd_prefill_workspace_size. */
+FD_API int fd_num_splits_diff(int B, int Hq, int Hkv, int L_max, int d, int num_splits, int ragged);
+FD_API size_t fd_decode_diff_workspace_size(int B, int Hq, int Hkv, int L_max, int d, int num_splits, int ragged);
+FD_API int fd_decode_dense_diff(const void* q, const void* k, const void* v, const int32_t* seq_lens,
+                                int B, int Hq, int Hkv, int L_max, int d, float scale,
+                                const float* lambda, long long lambda_stride, const float* norm_weight, float norm_eps,
+                                int num_splits, void* out, int out_dtype, float* lse,
+                                void* workspace, size_t workspace_bytes, void* stream);
+FD_API int fd_decode_paged_diff(const void* q, const void* k_pages, const void* v_pages,
+                                const int32_t* page_table, int max_pages, int num_pages,
+                                const int32_t* seq_lens, int page_size,
+                                int B, int Hq, int Hkv, int d, float scale,
+                                const float* lambda, long long lambda_stride, const float* norm_weight, float norm_eps,
+                                int num_splits, void* out, int out_dtype, float* lse,
+                                void* workspace, size_t workspace_bytes, void* stream);
+FD_API int fd_prefill_diff_num_splits(int B, int total_q, int Hq, int Hkv, int max_k, int d, int num_splits);
+FD_API size_t fd_prefill_diff_workspace_size(int B, int total_q, int Hq, int Hkv, int max_k, int d, int num_splits);
+FD_API int fd_prefill_packed_diff(const void* q, const void* k, const void* v,
+                                  long long q_stride, long long k_stride, long long v_stride,
+                                  const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,
+                                  int B, int total_q, int total_k, int Hq, int Hkv, int d, float scale, int causal,
+                                  const float* lambda, long long lambda_stride, const float* norm_weight,
+                                  float norm_eps, int num_splits, void* out, int out_dtype, float* lse,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+FD_API int fd_prefill_paged_diff(const void* q, const void* k_pages, const void* v_pages, long long q_stride,
+                                 const int32_t* page_table, int max_pages, int num_pages,
+                                 const int32_t* cu_seqlens_q, const int32_t* seq_lens, int page_size,
+                                 int B, int total_q, int Hq, int Hkv, int d, float scale, int causal,
+                                 const float* lambda, long long lambda_stride, const float* norm_weight,
+                                 float norm_eps, int num_splits, void* out, int out_dtype, float* lse,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+
 /* Size of the fixed device scratch array used by fd_decode_dense_noalloc. */
 #define FD_NOALLOC_SCRATCH_BYTES (4u << 20)
 
@@ -548,7 +663,7 @@ FD_API int fd_decode_dense_noalloc(const void* q, const void* k, const void* v,
  * Applies to the bf16 dense and paged decode (fd_decode_dense,
  * fd_decode_paged, their unified-max variants and fd_decode_dense_noalloc),
  * the prompt attention and the shared-prefix decode (fd_prefill_packed,
- * fd_prefill_paged, fd_decode_*_shared_prefix) launched afterwards from this
+ * fd_prefill_paged, fd_decode_*_shared_prefix) and the differential calls launched afterwards from this
  * process:
  *   wait_limit_ns  > 0: the time limit of every pipeline wait (default 2 s;
  *                  0 restores it)

@@ -5,8 +5,8 @@ shapes, devices and contiguity, allocates outputs and workspace with torch
 when the caller did not pass them, and calls the C entry point of the same
 name (declared in include/fd.h) on the current CUDA stream.  All arithmetic
 runs in the library's CUDA kernels; there is no fallback.  A missing or
-unloadable libfd.so raises an error.  The prompt, shared-prefix, page and
-append calls do these steps in the compiled module _marshal
+unloadable libfd.so raises an error.  The prompt, shared-prefix, page, append,
+rotation and differential calls do these steps in the compiled module _marshal
 (csrc/fd_binding.cpp), the others in Python.
 """
 from __future__ import annotations
@@ -31,6 +31,9 @@ __all__ = [
     "fd_prefill_num_splits", "fd_prefill_workspace_size", "fd_prefill_packed", "fd_prefill_paged",
     "fd_shared_prefix_workspace_size", "fd_decode_paged_shared_prefix", "fd_decode_dense_shared_prefix",
     "fd_assign_pages", "fd_append_kv_paged", "fd_append_kv_paged_fp8",
+    "fd_norm_rope", "fd_append_kv_paged_rope", "fd_append_kv_paged_rope_fp8", "fd_num_splits_diff",
+    "fd_decode_diff_workspace_size", "fd_decode_dense_diff", "fd_decode_paged_diff", "fd_prefill_diff_num_splits",
+    "fd_prefill_diff_workspace_size", "fd_prefill_packed_diff", "fd_prefill_paged_diff",
     "FD_OK", "FD_ERR_INVALID_ARG", "FD_ERR_UNSUPPORTED", "FD_ERR_WORKSPACE_TOO_SMALL",
     "FD_ERR_BAD_PAGE_TABLE", "FD_ERR_CUDA", "FD_ERR_DEVICE_TIMEOUT", "FD_ERR_OUT_OF_PAGES", "FD_OUT_F32", "FD_OUT_BF16",
 ]
@@ -114,6 +117,19 @@ def open_library(path: str):
         "fd_assign_pages": (I, [P, P, I, P, I, I, P, I, P, I, P, P, P, P, P]),
         "fd_append_kv_paged": (I, [P, P, N, N, P, I, I, I, P, P, I, I, P]),
         "fd_append_kv_paged_fp8": (I, [P, P, N, N, P, I, I, I, P, P, P, P, I, I, P]),
+        "fd_norm_rope": (I, [P, P, N, N, I, I, I, I, P, P, P, N, N, P]),
+        "fd_append_kv_paged_rope": (I, [P, P, P, N, N, N, P, I, I, I, I, P, P, N, P, P, I, I, P]),
+        "fd_append_kv_paged_rope_fp8": (I, [P, P, P, N, N, N, P, I, I, I, I, P, P, N, P, P, P, P, I, I, P]),
+        "fd_num_splits_diff": (I, [I, I, I, I, I, I, I]),
+        "fd_decode_diff_workspace_size": (S, [I, I, I, I, I, I, I]),
+        "fd_decode_dense_diff": (I, [P, P, P, P, I, I, I, I, I, F, P, N, P, F, I, P, I, P, P, S, P]),
+        "fd_decode_paged_diff": (I, [P, P, P, P, I, I, P, I, I, I, I, I, F, P, N, P, F, I, P, I, P, P, S, P]),
+        "fd_prefill_diff_num_splits": (I, [I, I, I, I, I, I, I]),
+        "fd_prefill_diff_workspace_size": (S, [I, I, I, I, I, I, I]),
+        "fd_prefill_packed_diff": (I, [P, P, P, N, N, N, P, P, I, I, I, I, I, I, F, I, P, N, P, F, I, P, I, P, P, S,
+                                       P]),
+        "fd_prefill_paged_diff": (I, [P, P, P, N, P, I, I, P, P, I, I, I, I, I, I, F, I, P, N, P, F, I, P, I, P, P, S,
+                                      P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -749,6 +765,105 @@ def fd_append_kv_paged_fp8(k, v, slots, k_pages, k_page_scales, v_pages, v_page_
     uint8 codes, k_page_scales, v_page_scales [P,Hkv,64] float32; rows are
     encoded as by fd_quantize_kv_fp8."""
     return _binding().append_kv_fp8(k, v, slots, k_pages, k_page_scales, v_pages, v_page_scales, stream)
+
+
+def fd_norm_rope(q, k, cos_sin, positions=None, cu_seqlens=None, seq_lens=None, q_weight=None, k_weight=None,
+                 norm_eps=1e-6, interleaved=False, halves=False, q_out=None, k_out=None, stream=None):
+    """Norms (where there is a weight) and rotation of query and key heads.
+    q [T,Hq,d], k [T,Hkv,d] bf16 (tokens may be strided; k may be None), cos_sin
+    [max_pos,rot] float32 (cosines, then sines of a position; rot a multiple of
+    16), positions [T] int32 (negative: the token is left out), or cu_seqlens
+    [B+1] and seq_lens [B] int32 as fd_assign_pages returns them; q_weight,
+    k_weight [d] float32 or None.  The channels i and i + rot/2 turn together,
+    with interleaved 2i and 2i + 1.  halves: each half of a row is a head of its
+    own (weights [d/2], rot <= d/2).  Returns (q_out, k_out); q_out may be q and
+    k_out k (in place)."""
+    return _binding().norm_rope(q, k, cos_sin, positions, cu_seqlens, seq_lens, q_weight, k_weight, norm_eps,
+                                interleaved, halves, q_out, k_out, stream)
+
+
+def fd_append_kv_paged_rope(q, k, v, slots, k_pages, v_pages, cos_sin, positions=None, cu_seqlens=None, seq_lens=None,
+                            q_weight=None, k_weight=None, norm_eps=1e-6, interleaved=False, halves=False, q_out=None,
+                            stream=None):
+    """fd_append_kv_paged with fd_norm_rope on the way: the keys go to their
+    slots turned, the values as they are, the queries to q_out (q may be None).
+    Returns (q_out, k_pages, v_pages)."""
+    return _binding().append_rope(q, k, v, slots, k_pages, v_pages, cos_sin, positions, cu_seqlens, seq_lens, q_weight,
+                                  k_weight, norm_eps, interleaved, halves, q_out, stream)
+
+
+def fd_append_kv_paged_rope_fp8(q, k, v, slots, k_pages, k_page_scales, v_pages, v_page_scales, cos_sin,
+                                positions=None, cu_seqlens=None, seq_lens=None, q_weight=None, k_weight=None,
+                                norm_eps=1e-6, interleaved=False, halves=False, q_out=None, stream=None):
+    """fd_append_kv_paged_rope into the paged fp8 cache (as
+    fd_append_kv_paged_fp8; the keys are encoded from their turned float32
+    values).  Returns (q_out, k_pages, k_page_scales, v_pages, v_page_scales)."""
+    return _binding().append_rope_fp8(q, k, v, slots, k_pages, k_page_scales, v_pages, v_page_scales, cos_sin,
+                                      positions, cu_seqlens, seq_lens, q_weight, k_weight, norm_eps, interleaved,
+                                      halves, q_out, stream)
+
+
+def fd_num_splits_diff(B, Hq, Hkv, L_max, d, num_splits=0, ragged=False) -> int:
+    r = int(load().fd_num_splits_diff(B, Hq, Hkv, L_max, d, num_splits, int(bool(ragged))))
+    if r < 0:
+        raise FdError(-r, "fd_num_splits_diff")
+    return r
+
+
+def fd_decode_diff_workspace_size(B, Hq, Hkv, L_max, d, num_splits=0, ragged=False) -> int:
+    return _remembered_size("fd_decode_diff_workspace_size", B, Hq, Hkv, L_max, d, num_splits, int(bool(ragged)))
+
+
+def fd_decode_dense_diff(q, k, v, lam, seq_lens=None, scale=None, norm_weight=None, norm_eps=1e-5, num_splits=0,
+                         out=None, lse=None, out_dtype="bf16", want_lse=True, workspace=None, stream=None):
+    """Differential decode: softmax(scale q1 k1^T) v - lam softmax(scale q2 k2^T) v
+    of one token per sequence, q1, k1 the first halves of the rows and q2, k2 the
+    second ones, then the norm where there is a norm_weight.  q [B,Hq,d], k, v
+    [B,Hkv,L_max,d] bf16, lam [Hq] or [B,Hq] float32, seq_lens [B] int32 or None,
+    norm_weight [d] float32 or None; scale None = 1/sqrt(d/2).  Returns (out
+    [B,Hq,d], lse [B,Hq,2] or None)."""
+    return _binding().dense_diff(q, k, v, lam, seq_lens, scale, norm_weight, norm_eps, num_splits, out, lse,
+                                 _code(out_dtype), want_lse, workspace, stream)
+
+
+def fd_decode_paged_diff(q, k_pages, v_pages, lam, page_table, num_pages, seq_lens, scale=None, norm_weight=None,
+                         norm_eps=1e-5, num_splits=0, out=None, lse=None, out_dtype="bf16", want_lse=True,
+                         workspace=None, stream=None):
+    """fd_decode_dense_diff over a paged cache, as fd_decode_paged: k_pages,
+    v_pages [P,Hkv,64,d] bf16, page_table [B,max_pages] int32."""
+    return _binding().paged_diff(q, k_pages, v_pages, lam, page_table, num_pages, seq_lens, scale, norm_weight,
+                                 norm_eps, num_splits, out, lse, _code(out_dtype), want_lse, workspace, stream)
+
+
+def fd_prefill_diff_num_splits(B, total_q, Hq, Hkv, max_k, d, num_splits=0) -> int:
+    r = int(load().fd_prefill_diff_num_splits(B, total_q, Hq, Hkv, max_k, d, num_splits))
+    if r < 0:
+        raise FdError(-r, "fd_prefill_diff_num_splits")
+    return r
+
+
+def fd_prefill_diff_workspace_size(B, total_q, Hq, Hkv, max_k, d, num_splits=0) -> int:
+    return _remembered_size("fd_prefill_diff_workspace_size", B, total_q, Hq, Hkv, max_k, d, num_splits)
+
+
+def fd_prefill_packed_diff(q, k, v, lam, cu_seqlens_q, cu_seqlens_k=None, scale=None, norm_weight=None, norm_eps=1e-5,
+                           causal=True, num_splits=0, out=None, lse=None, out_dtype="bf16", want_lse=True,
+                           workspace=None, stream=None):
+    """Differential attention (fd_decode_dense_diff) of whole prompts, packed as
+    for fd_prefill_packed.  lam [Hq] or [Tq,Hq] float32.  Returns (out [Tq,Hq,d],
+    lse [Tq,Hq,2] or None)."""
+    return _binding().prefill_packed_diff(q, k, v, lam, cu_seqlens_q, cu_seqlens_k, scale, norm_weight, norm_eps, causal,
+                                          num_splits, out, lse, _code(out_dtype), want_lse, workspace, stream)
+
+
+def fd_prefill_paged_diff(q, k_pages, v_pages, lam, page_table, num_pages, cu_seqlens_q, seq_lens, scale=None,
+                          norm_weight=None, norm_eps=1e-5, causal=True, num_splits=0, out=None, lse=None,
+                          out_dtype="bf16", want_lse=True, workspace=None, stream=None):
+    """Differential attention of prompt tails over a paged cache, as
+    fd_prefill_paged.  lam [Hq] or [Tq,Hq] float32."""
+    return _binding().prefill_paged_diff(q, k_pages, v_pages, lam, page_table, num_pages, cu_seqlens_q, seq_lens, scale,
+                                         norm_weight, norm_eps, causal, num_splits, out, lse, _code(out_dtype),
+                                         want_lse, workspace, stream)
 
 
 def fd_debug_inject_wait_timeout(wait_limit_ns=0, withhold_tile=-1) -> int:

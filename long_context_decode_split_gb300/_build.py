@@ -25,7 +25,7 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
               "-Xptxas", "-warn-spills", f"-I{INCLUDE}", f"-I{CSRC}"]
 SOURCES = ["fd_api.cu", "fd_decode.cu", "fd_topdelta.cu", "fd_fp8.cu", "fd_fp4.cu", "fd_noalloc.cu", "fd_rows.cu",
-           "fd_merge.cu", "fd_pages.cu"]
+           "fd_merge.cu", "fd_pages.cu", "fd_rows_diff.cu", "fd_diff.cu", "fd_rope.cu"]
 
 
 def nvcc() -> str:

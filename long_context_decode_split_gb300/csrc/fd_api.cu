@@ -406,11 +406,12 @@ int check_rows(int B, int total_q, int Hq, int Hkv, int max_k, int d, int num_sp
 // tokens behind 8192 cached ones 95 us in one, 64 us in two, 82 us in three; 2 x 64
 // behind 32K 339 us in one, 65 us in nine, 78 us in sixteen; 16 x 8 behind 16K to 64K
 // (64 query heads) 458 us in one, 344 us in three, 332 us in seven, 346 us in sixteen.
-RowsPlan prefill_plan(int B, int total_q, int Hq, int Hkv, int max_k, int num_splits) {
+// per: query tokens of a piece of work.
+RowsPlan pieces_plan(int B, int total_q, int Hq, int Hkv, int max_k, int num_splits, int per) {
     RowsPlan pl;
     pl.splits = num_splits > 0 ? num_splits : 1;
     pl.chunk = num_splits > 0 ? 128 : 512;
-    const int sms = num_splits > 0 ? 0 : current_sm_count(), per = fd::rows_tokens(B, total_q, Hq / Hkv, -1);
+    const int sms = num_splits > 0 ? 0 : current_sm_count();
     const long long mean = B > 0 ? (total_q + B - 1) / B : 0;  // tokens of a sequence
     const long long ctas = (long long)B * ((mean + per - 1) / per) * Hkv;
     if (sms <= 0 || ctas <= 0 || ctas >= 2LL * sms) return pl;
@@ -434,6 +435,10 @@ RowsPlan prefill_plan(int B, int total_q, int Hq, int Hkv, int max_k, int num_sp
     return pl;
 }
 
+RowsPlan prefill_plan(int B, int total_q, int Hq, int Hkv, int max_k, int num_splits) {
+    return pieces_plan(B, total_q, Hq, Hkv, max_k, num_splits, fd::rows_tokens(B, total_q, Hq / Hkv, -1));
+}
+
 // The plan of a packed call, whose sequences share total_k: no more parts than a
 // sequence of 1.6 times the mean fills (the longest one, if lengths run from a quarter of
 // it up; 6 prompts of 256 tokens, 4 query heads: 9.4 us in the one part that this gives,
@@ -451,8 +456,7 @@ bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 // A token stride covers the token's heads and keeps 16-byte rows.
 bool stride_ok(long long s, int H, int d) { return s >= (long long)H * d && s % 8 == 0 && s <= (1LL << 32); }
 
-int prefill_entry(fd::RowsArgs& a, int num_splits, int out_dtype, void* workspace, size_t workspace_bytes,
-                  void* stream) {
+int check_prefill(const fd::RowsArgs& a, int num_splits, int out_dtype) {
     const int st = check_rows(a.B, a.total_q, a.Hq, a.Hkv, a.max_k, a.D, num_splits);
     if (st != FD_OK) return st;
     if (out_dtype != FD_OUT_F32 && out_dtype != FD_OUT_BF16) return FD_ERR_INVALID_ARG;
@@ -464,15 +468,50 @@ int prefill_entry(fd::RowsArgs& a, int num_splits, int out_dtype, void* workspac
     if (!aligned4(a.lse) || !aligned4(a.cu_q) || !aligned4(a.cu_k) || !aligned4(a.seq_lens) ||
         !aligned4(a.page_table))
         return FD_ERR_INVALID_ARG;
-    const RowsPlan pl = a.cu_k ? packed_plan(a.B, a.total_q, a.Hq, a.Hkv, a.total_k, num_splits)
-                               : prefill_plan(a.B, a.total_q, a.Hq, a.Hkv, a.max_k, num_splits);
-    const size_t need = fd::decode_workspace_bytes(a.total_q, a.Hq, a.D, pl.splits);
+    return FD_OK;
+}
+
+// A differential call: a piece of work has one tile, and either map its own records.
+RowsPlan prefill_diff_plan(int B, int total_q, int Hq, int Hkv, int max_k, int num_splits, bool packed) {
+    RowsPlan pl = pieces_plan(B, total_q, Hq, Hkv, max_k, num_splits, fd::rows_diff_tokens(Hq / Hkv));
+    if (packed && pl.splits > 1 && num_splits == 0)  // (as packed_plan)
+        pl.splits = std::min(pl.splits, std::max(1, (int)(1.6 * max_k / B) / pl.chunk));
+    return pl;
+}
+
+int check_diff_rows(int B, int total_q, int Hq, int Hkv, int max_k, int d, int num_splits) {
+    const int st = check_rows(B, total_q, Hq, Hkv, max_k, d, num_splits);
+    if (st != FD_OK) return st;
+    const long long ctas = fd::rows_diff_tiles(B, total_q, Hq / Hkv) * Hkv;
+    return ctas * (num_splits > 0 ? num_splits : 1) > 0x7fffffffLL ? FD_ERR_UNSUPPORTED : FD_OK;
+}
+
+int check_mix(const fd::DiffMix& m, int Hq, bool some) {
+    if (some && !m.lambda) return FD_ERR_INVALID_ARG;
+    if (m.lambda_stride != 0 && (m.lambda_stride < Hq || m.lambda_stride > (1LL << 32))) return FD_ERR_INVALID_ARG;
+    if (!aligned4(m.lambda) || !aligned16(m.weight)) return FD_ERR_INVALID_ARG;
+    if (m.weight && !(m.eps > 0.f && std::isfinite(m.eps))) return FD_ERR_INVALID_ARG;
+    return FD_OK;
+}
+
+// mix: the two maps of differential attention, or null.
+int prefill_entry(fd::RowsArgs& a, const fd::DiffMix* mix, int num_splits, int out_dtype, void* workspace,
+                  size_t workspace_bytes, void* stream) {
+    int st = check_prefill(a, num_splits, out_dtype);
+    if (st == FD_OK && mix) st = check_diff_rows(a.B, a.total_q, a.Hq, a.Hkv, a.max_k, a.D, num_splits);
+    if (st == FD_OK && mix) st = check_mix(*mix, a.Hq, a.B > 0 && a.total_q > 0);
+    if (st != FD_OK) return st;
+    const RowsPlan pl = mix      ? prefill_diff_plan(a.B, a.total_q, a.Hq, a.Hkv, a.max_k, num_splits, a.cu_k != nullptr)
+                        : a.cu_k ? packed_plan(a.B, a.total_q, a.Hq, a.Hkv, a.total_k, num_splits)
+                                 : prefill_plan(a.B, a.total_q, a.Hq, a.Hkv, a.max_k, num_splits);
+    const int rows = mix ? 2 * a.Hq : a.Hq;  // of records, a token
+    const size_t need = fd::decode_workspace_bytes(a.total_q, rows, a.D, pl.splits);
     if (need > 0) {
         if (!workspace || workspace_bytes < need) return FD_ERR_WORKSPACE_TOO_SMALL;
         if (!aligned16(workspace)) return FD_ERR_INVALID_ARG;
         if ((long long)a.total_q * a.Hq > 0x7fffffffLL) return FD_ERR_UNSUPPORTED;  // the merge's grid
     }
-    if (!some) return FD_OK;
+    if (a.B == 0 || a.total_q == 0) return FD_OK;
     a.splits = pl.splits;
     a.chunk = pl.chunk;
     a.out_bf16 = out_dtype == FD_OUT_BF16;
@@ -481,10 +520,13 @@ int prefill_entry(fd::RowsArgs& a, int num_splits, int out_dtype, void* workspac
     a.rec0 = 0;
     a.rec_stride = pl.splits;
     a.part_o = static_cast<float*>(workspace);
-    a.part_ml = need ? a.part_o + (size_t)a.total_q * a.Hq * pl.splits * a.D : nullptr;
+    a.part_ml = need ? a.part_o + (size_t)a.total_q * rows * pl.splits * a.D : nullptr;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = fd::launch_rows(a, s);
+    const cudaError_t e = mix ? fd::launch_rows_diff(a, *mix, s) : fd::launch_rows(a, s);
     if (e != cudaSuccess || a.direct) return to_status(e);
+    if (mix)
+        return to_status(fd::launch_merge_diff(a.part_o, a.part_ml, a.cu_q, a.B, a.total_q, a.Hq, a.D, pl.splits,
+                                               nullptr, 0, 0, a.out, a.out_bf16, a.lse, *mix, s));
     return to_status(fd::launch_merge_list(a.part_o, a.part_ml, a.cu_q, a.B, a.total_q, a.Hq, a.D, pl.splits, a.out,
                                            a.out_bf16, a.lse, s));
 }
@@ -636,22 +678,7 @@ int shared_entry(fd::RowsArgs& r, fd::DecodeArgs& o, int prefix_len, int L_own, 
                                            L_own == 0 ? o.seq_lens : nullptr, o.L_max));
 }
 
-}  // namespace
-
-extern "C" {
-
-int fd_prefill_num_splits(int B, int total_q, int Hq, int Hkv, int max_k, int d, int num_splits) {
-    const int st = check_rows(B, total_q, Hq, Hkv, max_k, d, num_splits);
-    if (st != FD_OK) return -st;
-    return prefill_plan(B, total_q, Hq, Hkv, max_k, num_splits).splits;
-}
-
-size_t fd_prefill_workspace_size(int B, int total_q, int Hq, int Hkv, int max_k, int d, int num_splits) {
-    if (check_rows(B, total_q, Hq, Hkv, max_k, d, num_splits) != FD_OK) return 0;
-    return fd::decode_workspace_bytes(total_q, Hq, d, prefill_plan(B, total_q, Hq, Hkv, max_k, num_splits).splits);
-}
-
-int fd_prefill_packed(const void* q, const void* k, const void* v, long long q_stride, long long k_stride,
+int packed_entry(const fd::DiffMix* mix, const void* q, const void* k, const void* v, long long q_stride, long long k_stride,
                       long long v_stride, const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int B,
                       int total_q, int total_k, int Hq, int Hkv, int d, float scale, int causal, int num_splits,
                       void* out, int out_dtype, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
@@ -681,10 +708,10 @@ int fd_prefill_packed(const void* q, const void* k, const void* v, long long q_s
     a.causal = causal != 0;
     a.out = out;
     a.lse = lse;
-    return prefill_entry(a, num_splits, out_dtype, workspace, workspace_bytes, stream);
+    return prefill_entry(a, mix, num_splits, out_dtype, workspace, workspace_bytes, stream);
 }
 
-int fd_prefill_paged(const void* q, const void* k_pages, const void* v_pages, long long q_stride,
+int paged_rows_entry(const fd::DiffMix* mix, const void* q, const void* k_pages, const void* v_pages, long long q_stride,
                      const int32_t* page_table, int max_pages, int num_pages, const int32_t* cu_seqlens_q,
                      const int32_t* seq_lens, int page_size, int B, int total_q, int Hq, int Hkv, int d, float scale,
                      int causal, int num_splits, void* out, int out_dtype, float* lse, void* workspace,
@@ -717,7 +744,75 @@ int fd_prefill_paged(const void* q, const void* k_pages, const void* v_pages, lo
     a.causal = causal != 0;
     a.out = out;
     a.lse = lse;
-    return prefill_entry(a, num_splits, out_dtype, workspace, workspace_bytes, stream);
+    return prefill_entry(a, mix, num_splits, out_dtype, workspace, workspace_bytes, stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+int fd_prefill_num_splits(int B, int total_q, int Hq, int Hkv, int max_k, int d, int num_splits) {
+    const int st = check_rows(B, total_q, Hq, Hkv, max_k, d, num_splits);
+    if (st != FD_OK) return -st;
+    return prefill_plan(B, total_q, Hq, Hkv, max_k, num_splits).splits;
+}
+
+size_t fd_prefill_workspace_size(int B, int total_q, int Hq, int Hkv, int max_k, int d, int num_splits) {
+    if (check_rows(B, total_q, Hq, Hkv, max_k, d, num_splits) != FD_OK) return 0;
+    return fd::decode_workspace_bytes(total_q, Hq, d, prefill_plan(B, total_q, Hq, Hkv, max_k, num_splits).splits);
+}
+
+int fd_prefill_packed(const void* q, const void* k, const void* v, long long q_stride, long long k_stride,
+                      long long v_stride, const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int B,
+                      int total_q, int total_k, int Hq, int Hkv, int d, float scale, int causal, int num_splits,
+                      void* out, int out_dtype, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+    return packed_entry(nullptr, q, k, v, q_stride, k_stride, v_stride, cu_seqlens_q, cu_seqlens_k, B, total_q, total_k,
+                        Hq, Hkv, d, scale, causal, num_splits, out, out_dtype, lse, workspace, workspace_bytes, stream);
+}
+
+int fd_prefill_paged(const void* q, const void* k_pages, const void* v_pages, long long q_stride,
+                     const int32_t* page_table, int max_pages, int num_pages, const int32_t* cu_seqlens_q,
+                     const int32_t* seq_lens, int page_size, int B, int total_q, int Hq, int Hkv, int d, float scale,
+                     int causal, int num_splits, void* out, int out_dtype, float* lse, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+    return paged_rows_entry(nullptr, q, k_pages, v_pages, q_stride, page_table, max_pages, num_pages, cu_seqlens_q,
+                            seq_lens, page_size, B, total_q, Hq, Hkv, d, scale, causal, num_splits, out, out_dtype, lse,
+                            workspace, workspace_bytes, stream);
+}
+
+int fd_prefill_diff_num_splits(int B, int total_q, int Hq, int Hkv, int max_k, int d, int num_splits) {
+    const int st = check_diff_rows(B, total_q, Hq, Hkv, max_k, d, num_splits);
+    if (st != FD_OK) return -st;
+    return prefill_diff_plan(B, total_q, Hq, Hkv, max_k, num_splits, false).splits;
+}
+
+size_t fd_prefill_diff_workspace_size(int B, int total_q, int Hq, int Hkv, int max_k, int d, int num_splits) {
+    if (check_diff_rows(B, total_q, Hq, Hkv, max_k, d, num_splits) != FD_OK) return 0;
+    return fd::decode_workspace_bytes(total_q, 2 * Hq, d,
+                                      prefill_diff_plan(B, total_q, Hq, Hkv, max_k, num_splits, false).splits);
+}
+
+int fd_prefill_packed_diff(const void* q, const void* k, const void* v, long long q_stride, long long k_stride,
+                           long long v_stride, const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int B,
+                           int total_q, int total_k, int Hq, int Hkv, int d, float scale, int causal,
+                           const float* lambda, long long lambda_stride, const float* norm_weight, float norm_eps,
+                           int num_splits, void* out, int out_dtype, float* lse, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+    const fd::DiffMix mix = {lambda, lambda_stride, norm_weight, norm_eps};
+    return packed_entry(&mix, q, k, v, q_stride, k_stride, v_stride, cu_seqlens_q, cu_seqlens_k, B, total_q, total_k, Hq,
+                        Hkv, d, scale, causal, num_splits, out, out_dtype, lse, workspace, workspace_bytes, stream);
+}
+
+int fd_prefill_paged_diff(const void* q, const void* k_pages, const void* v_pages, long long q_stride,
+                          const int32_t* page_table, int max_pages, int num_pages, const int32_t* cu_seqlens_q,
+                          const int32_t* seq_lens, int page_size, int B, int total_q, int Hq, int Hkv, int d,
+                          float scale, int causal, const float* lambda, long long lambda_stride,
+                          const float* norm_weight, float norm_eps, int num_splits, void* out, int out_dtype,
+                          float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+    const fd::DiffMix mix = {lambda, lambda_stride, norm_weight, norm_eps};
+    return paged_rows_entry(&mix, q, k_pages, v_pages, q_stride, page_table, max_pages, num_pages, cu_seqlens_q, seq_lens,
+                            page_size, B, total_q, Hq, Hkv, d, scale, causal, num_splits, out, out_dtype, lse,
+                            workspace, workspace_bytes, stream);
 }
 
 size_t fd_shared_prefix_workspace_size(int B, int Hq, int Hkv, int prefix_len, int L_own, int d, int num_splits) {
@@ -792,6 +887,119 @@ int fd_decode_paged_shared_prefix(const void* q, const void* k_pages, const void
     o.out = out;
     o.lse = lse;
     return shared_entry(r, o, prefix_len, L_own, num_splits, out_dtype, workspace, workspace_bytes, stream);
+}
+
+// ---------------------------------------------------------------------------
+// Differential attention of single tokens.
+
+}  // extern "C"
+
+namespace {
+
+// The columns of both maps share a pass over the cache; its chunks are those of the plain decode, by
+// the bytes.
+Plan diff_plan(int B, int Hq, int Hkv, int L_max, int d, int requested, bool ragged) {
+    const int sms = current_sm_count();
+    const int occ = requested > 0 ? 1 : fd::diff_ctas_per_sm(d, Hq / Hkv, ragged);
+    return plan(B, Hkv, L_max, requested, ragged, occ, sms, saturating_ctas(d, sms), true);
+}
+
+int diff_decode_entry(fd::DecodeArgs& a, const fd::DiffMix& mix, int num_splits, int out_dtype, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+    const bool ragged = a.seq_lens != nullptr;
+    if (out_dtype != FD_OUT_F32 && out_dtype != FD_OUT_BF16) return FD_ERR_INVALID_ARG;
+    if (num_splits < 0 || !(a.scale > 0.f) || !std::isfinite(a.scale)) return FD_ERR_INVALID_ARG;
+    if (a.B > 0 && (!a.q || !a.out)) return FD_ERR_INVALID_ARG;
+    const long long cache_rows = a.page_table ? (long long)a.num_pages * a.Hkv * kTile
+                                              : (long long)a.B * a.Hkv * a.L_max;
+    if (cache_rows > 0 && (!a.k || !a.v)) return FD_ERR_INVALID_ARG;
+    if (!aligned16(a.q) || !aligned16(a.k) || !aligned16(a.v) || !aligned16(a.out)) return FD_ERR_INVALID_ARG;
+    if (!aligned4(a.lse) || !aligned4(a.seq_lens) || !aligned4(a.page_table)) return FD_ERR_INVALID_ARG;
+    const int st = check_mix(mix, a.Hq, a.B > 0);
+    if (st != FD_OK) return st;
+    if (cache_rows > 0x7fffffffLL) return FD_ERR_UNSUPPORTED;  // 32-bit row coordinates
+    const Plan pl = diff_plan(a.B, a.Hq, a.Hkv, a.L_max, a.D, num_splits, ragged);
+    const size_t need = fd::decode_workspace_bytes(a.B, 2 * a.Hq, a.D, pl.splits);
+    if (need > 0) {
+        if (!workspace || workspace_bytes < need) return FD_ERR_WORKSPACE_TOO_SMALL;
+        if (!aligned16(workspace)) return FD_ERR_INVALID_ARG;
+        if ((long long)a.B * a.Hq > 0x7fffffffLL) return FD_ERR_UNSUPPORTED;  // the merge's grid
+    }
+    a.splits = pl.splits;
+    a.chunk_fixed = pl.chunk_fixed;
+    a.out_bf16 = out_dtype == FD_OUT_BF16;
+    a.part_o = static_cast<float*>(workspace);
+    a.part_ml = need ? a.part_o + (size_t)a.B * 2 * a.Hq * pl.splits * a.D : nullptr;
+    return to_status(fd::launch_decode_diff(a, mix, static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+int fd_num_splits_diff(int B, int Hq, int Hkv, int L_max, int d, int num_splits, int ragged) {
+    const int st = check_shape(B, Hq, Hkv, L_max, d);
+    if (st != FD_OK) return -st;
+    if (num_splits < 0) return -FD_ERR_INVALID_ARG;
+    return diff_plan(B, Hq, Hkv, L_max, d, num_splits, ragged != 0).splits;
+}
+
+size_t fd_decode_diff_workspace_size(int B, int Hq, int Hkv, int L_max, int d, int num_splits, int ragged) {
+    if (check_shape(B, Hq, Hkv, L_max, d) != FD_OK || num_splits < 0) return 0;
+    return fd::decode_workspace_bytes(B, 2 * Hq, d, diff_plan(B, Hq, Hkv, L_max, d, num_splits, ragged != 0).splits);
+}
+
+int fd_decode_dense_diff(const void* q, const void* k, const void* v, const int32_t* seq_lens, int B, int Hq, int Hkv,
+                         int L_max, int d, float scale, const float* lambda, long long lambda_stride,
+                         const float* norm_weight, float norm_eps, int num_splits, void* out, int out_dtype, float* lse,
+                         void* workspace, size_t workspace_bytes, void* stream) {
+    const int st = check_shape(B, Hq, Hkv, L_max, d);
+    if (st != FD_OK) return st;
+    fd::DecodeArgs a = {};
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.seq_lens = seq_lens;
+    a.B = B;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.L_max = L_max;
+    a.D = d;
+    a.scale = scale;
+    a.out = out;
+    a.lse = lse;
+    return diff_decode_entry(a, {lambda, lambda_stride, norm_weight, norm_eps}, num_splits, out_dtype, workspace,
+                             workspace_bytes, stream);
+}
+
+int fd_decode_paged_diff(const void* q, const void* k_pages, const void* v_pages, const int32_t* page_table,
+                         int max_pages, int num_pages, const int32_t* seq_lens, int page_size, int B, int Hq, int Hkv,
+                         int d, float scale, const float* lambda, long long lambda_stride, const float* norm_weight,
+                         float norm_eps, int num_splits, void* out, int out_dtype, float* lse, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+    if (page_size != kTile) return page_size > 0 ? FD_ERR_UNSUPPORTED : FD_ERR_INVALID_ARG;
+    if (max_pages <= 0 || num_pages < 0 || max_pages > (1 << 24)) return FD_ERR_INVALID_ARG;
+    const int st = check_shape(B, Hq, Hkv, max_pages * kTile, d);
+    if (st != FD_OK) return st;
+    if (B > 0 && (!page_table || !seq_lens)) return FD_ERR_INVALID_ARG;
+    fd::DecodeArgs a = {};
+    a.q = q;
+    a.k = k_pages;
+    a.v = v_pages;
+    a.seq_lens = seq_lens;
+    a.page_table = page_table;
+    a.max_pages = max_pages;
+    a.num_pages = num_pages;
+    a.B = B;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.L_max = max_pages * kTile;
+    a.D = d;
+    a.scale = scale;
+    a.out = out;
+    a.lse = lse;
+    return diff_decode_entry(a, {lambda, lambda_stride, norm_weight, norm_eps}, num_splits, out_dtype, workspace,
+                             workspace_bytes, stream);
 }
 
 // ---------------------------------------------------------------------------
@@ -870,6 +1078,156 @@ int fd_append_kv_paged_fp8(const void* k, const void* v, long long k_stride, lon
     fd::AppendArgs a = {k, v, k_stride, v_stride, slots, T, Hkv, d, num_pages, k_pages, v_pages, k_page_scales,
                         v_page_scales};
     return append_entry(a, page_size, true, stream);
+}
+
+}  // extern "C"
+
+namespace {
+
+// T rows of `bytes` bytes, `step` bytes apart.
+struct Strided {
+    const void* at;
+    long long T, bytes, step;
+};
+bool overlap(const Strided& a, const Strided& b) {
+    if (!a.at || !b.at || a.T <= 0 || b.T <= 0 || a.bytes <= 0 || b.bytes <= 0) return false;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+    if (x >= y + (uintptr_t)((b.T - 1) * b.step + b.bytes) || y >= x + (uintptr_t)((a.T - 1) * a.step + a.bytes))
+        return false;
+    if (a.step != b.step) return true;
+    // slices of the same rows (a fused projection): apart where their columns are
+    const long long d = (long long)(y - x) % a.step, shift = d < 0 ? d + a.step : d;
+    return !(a.bytes <= shift && shift + b.bytes <= a.step);
+}
+
+// The arguments that norms and rotation share.  a: the tensors; paged: keys and values go to the cache.
+int rope_entry(fd::RopeArgs& a, const fd_rope* r, bool paged, bool fp8, int page_size, void* stream) {
+    if (paged && page_size != kTile) return page_size > 0 ? FD_ERR_UNSUPPORTED : FD_ERR_INVALID_ARG;
+    if (!r || a.T < 0 || a.Hq < 0 || a.Hkv < 0 || a.Hq > 65535 || a.Hkv > 65535 || a.num_pages < 0)
+        return FD_ERR_INVALID_ARG;
+    if (a.Hq + a.Hkv == 0 || (paged && a.Hkv == 0)) return FD_ERR_INVALID_ARG;
+    if (a.D != 64 && a.D != 128) return FD_ERR_UNSUPPORTED;
+    const int dh = r->halves ? a.D / 2 : a.D;
+    if (r->rot <= 0 || r->rot > dh || r->max_pos <= 0 || r->B < 0) return FD_ERR_INVALID_ARG;
+    if (r->rot % 16 != 0) return FD_ERR_UNSUPPORTED;
+    if ((long long)a.T * std::max(a.Hq, a.Hkv) > 0x7fffffffLL) return FD_ERR_UNSUPPORTED;
+    const bool q = a.Hq > 0, k = a.Hkv > 0, some = a.T > 0;
+    if ((q && (!stride_ok(a.q_stride, a.Hq, a.D) || !stride_ok(a.q_out_stride, a.Hq, a.D))) ||
+        (k && !stride_ok(a.k_stride, a.Hkv, a.D)) || (k && paged && !stride_ok(a.v_stride, a.Hkv, a.D)) ||
+        (k && !paged && !stride_ok(a.k_out_stride, a.Hkv, a.D)))
+        return FD_ERR_INVALID_ARG;
+    if (some && ((q && (!a.q || !a.q_out)) || (k && !a.k) || (k && !paged && !a.k_out) || (paged && (!a.v || !a.slots))))
+        return FD_ERR_INVALID_ARG;
+    if (some && paged && a.num_pages > 0 && (!a.k_pages || !a.v_pages || (fp8 && (!a.k_scales || !a.v_scales))))
+        return FD_ERR_INVALID_ARG;
+    if (some && (!r->cos_sin || (!r->positions && (!r->cu_seqlens || (r->B > 0 && !r->seq_lens)))))
+        return FD_ERR_INVALID_ARG;
+    if ((r->q_weight || r->k_weight) && !(r->norm_eps > 0.f && std::isfinite(r->norm_eps))) return FD_ERR_INVALID_ARG;
+    if (!aligned16(a.q) || !aligned16(a.k) || !aligned16(a.v) || !aligned16(a.q_out) || !aligned16(a.k_out) ||
+        !aligned16(a.k_pages) || !aligned16(a.v_pages) || !aligned16(r->cos_sin) || !aligned16(r->q_weight) ||
+        !aligned16(r->k_weight) || !aligned4(r->positions) || !aligned4(r->cu_seqlens) || !aligned4(r->seq_lens) ||
+        !aligned4(a.k_scales) || !aligned4(a.v_scales) || (reinterpret_cast<uintptr_t>(a.slots) & 7u))
+        return FD_ERR_INVALID_ARG;
+    // outputs share no memory with anything but, in place, the very rows that they replace
+    const auto rows = [&](const void* at, int H, long long stride) {
+        return Strided{at, a.T, 2LL * H * a.D, 2 * stride};
+    };
+    const Strided qo = rows(a.q_out, a.Hq, a.q_out_stride), ko = rows(a.k_out, a.Hkv, a.k_out_stride);
+    const Strided qi = rows(a.q, a.Hq, a.q_stride), ki = rows(a.k, a.Hkv, a.k_stride), vi = rows(a.v, a.Hkv, a.v_stride);
+    const auto same = [](const Strided& x, const Strided& y) {
+        return x.at == y.at && (x.step == y.step || x.T == 1) && x.bytes == y.bytes;
+    };
+    if (q && ((overlap(qo, qi) && !same(qo, qi)) || overlap(qo, ki) || overlap(qo, vi) || overlap(qo, ko)))
+        return FD_ERR_INVALID_ARG;
+    if (k && !paged && ((overlap(ko, ki) && !same(ko, ki)) || overlap(ko, qi))) return FD_ERR_INVALID_ARG;
+    const auto whole = [](const void* at, long long bytes) { return Strided{at, 1, bytes, bytes}; };
+    const long long pool = (long long)a.num_pages * a.Hkv * kTile * a.D * (fp8 ? 1 : 2);
+    const Strided others[] = {whole(a.k_pages, pool), whole(a.v_pages, pool),
+                              whole(r->cos_sin, 4LL * r->max_pos * r->rot), whole(r->q_weight, 4LL * dh),
+                              whole(r->k_weight, 4LL * dh)};
+    for (const Strided& o : others)
+        if ((q && overlap(qo, o)) || (k && !paged && overlap(ko, o))) return FD_ERR_INVALID_ARG;
+    a.cos_sin = r->cos_sin;
+    a.max_pos = r->max_pos;
+    a.rot = r->rot;
+    a.interleaved = r->interleaved != 0;
+    a.halves = r->halves != 0;
+    a.positions = r->positions;
+    a.cu = r->cu_seqlens;
+    a.lens = r->seq_lens;
+    a.B = r->B;
+    a.q_weight = r->q_weight;
+    a.k_weight = r->k_weight;
+    a.eps = r->norm_eps;
+    return to_status(fd::launch_rope(a, static_cast<cudaStream_t>(stream)));
+}
+
+const uint16_t* bits16(const void* p) { return static_cast<const uint16_t*>(p); }
+
+int append_rope(const void* q, const void* k, const void* v, long long q_stride, long long k_stride,
+                long long v_stride, const int64_t* slots, int T, int Hq, int Hkv, int d, const fd_rope* rope,
+                void* q_out, long long q_out_stride, void* k_pages, float* k_scales, void* v_pages, float* v_scales,
+                int num_pages, int page_size, bool fp8, void* stream) {
+    fd::RopeArgs a = {};
+    a.q = bits16(q);
+    a.k = bits16(k);
+    a.v = bits16(v);
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.slots = slots;
+    a.T = T;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.D = d;
+    a.q_out = static_cast<uint16_t*>(q_out);
+    a.q_out_stride = q_out_stride;
+    a.k_pages = k_pages;
+    a.v_pages = v_pages;
+    a.k_scales = k_scales;
+    a.v_scales = v_scales;
+    a.num_pages = num_pages;
+    return rope_entry(a, rope, true, fp8, page_size, stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+int fd_norm_rope(const void* q, const void* k, long long q_stride, long long k_stride, int T, int Hq, int Hkv, int d,
+                 const fd_rope* rope, void* q_out, void* k_out, long long q_out_stride, long long k_out_stride,
+                 void* stream) {
+    fd::RopeArgs a = {};
+    a.q = bits16(q);
+    a.k = bits16(k);
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.T = T;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.D = d;
+    a.q_out = static_cast<uint16_t*>(q_out);
+    a.k_out = static_cast<uint16_t*>(k_out);
+    a.q_out_stride = q_out_stride;
+    a.k_out_stride = k_out_stride;
+    return rope_entry(a, rope, false, false, kTile, stream);
+}
+
+int fd_append_kv_paged_rope(const void* q, const void* k, const void* v, long long q_stride, long long k_stride,
+                            long long v_stride, const int64_t* slots, int T, int Hq, int Hkv, int d,
+                            const fd_rope* rope, void* q_out, long long q_out_stride, void* k_pages, void* v_pages,
+                            int num_pages, int page_size, void* stream) {
+    return append_rope(q, k, v, q_stride, k_stride, v_stride, slots, T, Hq, Hkv, d, rope, q_out, q_out_stride,
+                           k_pages, nullptr, v_pages, nullptr, num_pages, page_size, false, stream);
+}
+
+int fd_append_kv_paged_rope_fp8(const void* q, const void* k, const void* v, long long q_stride, long long k_stride,
+                                long long v_stride, const int64_t* slots, int T, int Hq, int Hkv, int d,
+                                const fd_rope* rope, void* q_out, long long q_out_stride, uint8_t* k_pages,
+                                float* k_page_scales, uint8_t* v_pages, float* v_page_scales, int num_pages,
+                                int page_size, void* stream) {
+    return append_rope(q, k, v, q_stride, k_stride, v_stride, slots, T, Hq, Hkv, d, rope, q_out, q_out_stride,
+                           k_pages, k_page_scales, v_pages, v_page_scales, num_pages, page_size, true, stream);
 }
 
 int fd_abi_version(void) { return FD_ABI_VERSION; }
@@ -1131,7 +1489,7 @@ int fd_debug_inject_wait_timeout(unsigned long long wait_limit_ns, int withhold_
 
 int fd_device_status(int clear, void* stream) {
     if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return FD_ERR_CUDA;
-    unsigned a = 0, b = 0, c = 0, e = 0, r = 0, m = 0, g = 0;
+    unsigned a = 0, b = 0, c = 0, e = 0, r = 0, m = 0, g = 0, x = 0, y = 0, z = 0;
     if (fd::decode_status_read(&a, clear != 0) != cudaSuccess) return FD_ERR_CUDA;
     if (fd::topdelta_status_read(&b, clear != 0) != cudaSuccess) return FD_ERR_CUDA;
     if (fd::fp8_status_read(&c, clear != 0) != cudaSuccess) return FD_ERR_CUDA;
@@ -1139,7 +1497,10 @@ int fd_device_status(int clear, void* stream) {
     if (fd::rows_status_read(&r, clear != 0) != cudaSuccess) return FD_ERR_CUDA;
     if (fd::merge_status_read(&m, clear != 0) != cudaSuccess) return FD_ERR_CUDA;
     if (fd::pages_status_read(&g, clear != 0) != cudaSuccess) return FD_ERR_CUDA;
-    const unsigned bits = a | b | c | e | r | m | g;
+    if (fd::diff_status_read(&x, clear != 0) != cudaSuccess) return FD_ERR_CUDA;
+    if (fd::rows_diff_status_read(&y, clear != 0) != cudaSuccess) return FD_ERR_CUDA;
+    if (fd::rope_status_read(&z, clear != 0) != cudaSuccess) return FD_ERR_CUDA;
+    const unsigned bits = a | b | c | e | r | m | g | x | y | z;
     if (bits & 2u) return FD_ERR_DEVICE_TIMEOUT;
     if (bits & 1u) return FD_ERR_BAD_PAGE_TABLE;
     if (bits & 8u) return FD_ERR_OUT_OF_PAGES;

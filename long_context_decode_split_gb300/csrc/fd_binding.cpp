@@ -1,5 +1,5 @@
 // fd_binding.cpp -- the Python binding's compiled half for the prompt, shared-
-// prefix, page and append calls: the checks of their tensors, the allocation of
+// prefix, page, append, rotation and differential calls: the checks of their tensors, the allocation of
 // outputs and workspace on the stream that uses them, and the call of the C
 // entry point.  The same steps in Python cost 12-15 us a call beside 2-6 us of
 // GPU time (a decode step's page assignment: 18.9 us a call in Python, 6.4 us
@@ -37,6 +37,15 @@ struct Library {
     decltype(&fd_assign_pages) assign_pages;
     decltype(&fd_append_kv_paged) append;
     decltype(&fd_append_kv_paged_fp8) append_fp8;
+    decltype(&fd_norm_rope) norm_rope;
+    decltype(&fd_append_kv_paged_rope) append_rope;
+    decltype(&fd_append_kv_paged_rope_fp8) append_rope_fp8;
+    decltype(&fd_decode_diff_workspace_size) decode_diff_workspace_size;
+    decltype(&fd_decode_dense_diff) dense_diff;
+    decltype(&fd_decode_paged_diff) paged_diff;
+    decltype(&fd_prefill_diff_workspace_size) prefill_diff_workspace_size;
+    decltype(&fd_prefill_packed_diff) prefill_packed_diff;
+    decltype(&fd_prefill_paged_diff) prefill_paged_diff;
 };
 Library lib = {};
 PyObject* fd_error = nullptr;  // the class FdError(status, where)
@@ -66,11 +75,14 @@ bool truth(PyObject* o) {
     return r != 0;
 }
 
-float scale_of(PyObject* o, int64_t d) {
-    if (o == Py_None) return (float)(1.0 / std::sqrt((double)d));
+float number(PyObject* o) {
     const double v = PyFloat_AsDouble(o);
     if (v == -1.0 && PyErr_Occurred()) throw python_error();
     return (float)v;
+}
+
+float scale_of(PyObject* o, int64_t d) {
+    return o == Py_None ? (float)(1.0 / std::sqrt((double)d)) : number(o);
 }
 
 void on_device(const Tensor& t, const char* name, c10::Device dev) {
@@ -157,9 +169,9 @@ struct Place {
     }
 };
 
-c10::Device first_device(PyObject* o, const char* call) {
-    TORCH_CHECK_VALUE(THPVariable_Check(o) && THPVariable_Unpack(o).is_cuda(), call,
-                      ": the first argument must be a CUDA tensor");
+c10::Device first_device(PyObject* o, const char* call, const char* which = "the first argument") {
+    TORCH_CHECK_VALUE(THPVariable_Check(o) && THPVariable_Unpack(o).is_cuda(), call, ": ", which,
+                      " must be a CUDA tensor");
     return THPVariable_Unpack(o).device();
 }
 
@@ -172,13 +184,17 @@ struct Outputs {
     Tensor out, lse;  // lse may be undefined: none wanted
     int code;
 
-    Outputs(int64_t T, int64_t Hq, int64_t d, PyObject* o, PyObject* l, int out_code, bool want_lse, c10::Device dev)
+    // maps: an lse for each of so many maps, [T, Hq, maps] (0: [T, Hq])
+    Outputs(int64_t T, int64_t Hq, int64_t d, PyObject* o, PyObject* l, int out_code, bool want_lse, c10::Device dev,
+            int64_t maps = 0)
         : code(out_code) {
         const at::ScalarType type = out_code == FD_OUT_BF16 ? at::kBFloat16 : at::kFloat;
         if (o == Py_None) out = fresh_tensor({T, Hq, d}, type, dev);
         else out = check(tensor(o, "out"), "out", dev, type, {{T, Hq, d}});
-        if (l != Py_None) lse = check(tensor(l, "lse"), "lse", dev, at::kFloat, {{T, Hq}});
-        else if (want_lse) lse = fresh_tensor({T, Hq}, at::kFloat, dev);
+        const int64_t sizes[3] = {T, Hq, maps};
+        const at::IntArrayRef shape(sizes, maps ? 3 : 2);
+        if (l != Py_None) lse = check(tensor(l, "lse"), "lse", dev, at::kFloat, shape);
+        else if (want_lse) lse = fresh_tensor(shape, at::kFloat, dev);
     }
     float* lse_data() const { return lse.defined() ? lse.mutable_data_ptr<float>() : nullptr; }
 };
@@ -450,6 +466,25 @@ PyObject* append_kv(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// (k_pages, k_page_scales, v_pages, v_page_scales) for rows of r
+struct Fp8Pool {
+    uint8_t *k, *v;
+    float *k_scales, *v_scales;
+    int pages, page;
+    Fp8Pool(PyObject* const* a, const NewRows& r, c10::Device dev) {
+        const Tensor& kp = check(tensor(a[0], "k_pages"), "k_pages", dev, at::kByte);
+        TORCH_CHECK_VALUE(kp.dim() == 4 && kp.size(1) == r.Hkv && kp.size(3) == r.d, "k_pages must be [P, Hkv, page, d]");
+        const Tensor& vp = check(tensor(a[2], "v_pages"), "v_pages", dev, at::kByte, kp.sizes());
+        const at::IntArrayRef rows = kp.sizes().slice(0, 3);
+        k_scales = check(tensor(a[1], "k_page_scales"), "k_page_scales", dev, at::kFloat, rows).mutable_data_ptr<float>();
+        v_scales = check(tensor(a[3], "v_page_scales"), "v_page_scales", dev, at::kFloat, rows).mutable_data_ptr<float>();
+        k = kp.mutable_data_ptr<uint8_t>();
+        v = vp.mutable_data_ptr<uint8_t>();
+        pages = size_of(kp.size(0), "k_pages");
+        page = (int)kp.size(2);
+    }
+};
+
 // (k, v, slots, k_pages, k_page_scales, v_pages, v_page_scales, stream)
 PyObject* append_kv_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
@@ -458,17 +493,315 @@ PyObject* append_kv_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Place place(dev, a[7]);
     const Tensor &k = tensor(a[0], "k"), &v = tensor(a[1], "v");
     const NewRows r(k, v, a[2], dev);
-    const Tensor& kp = check(tensor(a[3], "k_pages"), "k_pages", dev, at::kByte);
-    TORCH_CHECK_VALUE(kp.dim() == 4 && kp.size(1) == r.Hkv && kp.size(3) == r.d, "k_pages must be [P, Hkv, page, d]");
-    const Tensor& vp = check(tensor(a[5], "v_pages"), "v_pages", dev, at::kByte, kp.sizes());
-    const at::IntArrayRef rows = kp.sizes().slice(0, 3);
-    const Tensor& ks = check(tensor(a[4], "k_page_scales"), "k_page_scales", dev, at::kFloat, rows);
-    const Tensor& vs = check(tensor(a[6], "v_page_scales"), "v_page_scales", dev, at::kFloat, rows);
-    expect(lib.append_fp8(k.const_data_ptr(), v.const_data_ptr(), r.ks, r.vs, r.slots, r.T, r.Hkv, r.d,
-                          kp.mutable_data_ptr<uint8_t>(), ks.mutable_data_ptr<float>(), vp.mutable_data_ptr<uint8_t>(),
-                          vs.mutable_data_ptr<float>(), size_of(kp.size(0), "k_pages"), (int)kp.size(2), place.stream),
+    const Fp8Pool pool(a + 3, r, dev);
+    expect(lib.append_fp8(k.const_data_ptr(), v.const_data_ptr(), r.ks, r.vs, r.slots, r.T, r.Hkv, r.d, pool.k,
+                          pool.k_scales, pool.v, pool.v_scales, pool.pages, pool.page, place.stream),
            "fd_append_kv_paged_fp8");
     return same({a[3], a[4], a[5], a[6]});
+    END_HANDLE_TH_ERRORS
+}
+
+// ---- rotation -----------------------------------------------------------------------
+
+// The rotation's arguments: (cos_sin, positions, cu_seqlens, seq_lens, q_weight, k_weight, norm_eps, interleaved, halves)
+fd_rope rope_of(PyObject* const* a, int T, int d, c10::Device dev) {
+    fd_rope r = {};
+    const Tensor& table = check(tensor(a[0], "cos_sin"), "cos_sin", dev, at::kFloat);
+    TORCH_CHECK_VALUE(table.dim() == 2, "cos_sin must be [max_pos, rot]");
+    r.cos_sin = table.const_data_ptr<float>();
+    r.max_pos = size_of(table.size(0), "cos_sin");
+    r.rot = size_of(table.size(1), "cos_sin");
+    TORCH_CHECK_VALUE((a[1] == Py_None) != (a[2] == Py_None) && (a[2] == Py_None) == (a[3] == Py_None),
+                      "give positions, or cu_seqlens and seq_lens");
+    if (a[1] != Py_None) {
+        r.positions = check(tensor(a[1], "positions"), "positions", dev, at::kInt, {{(int64_t)T}}).const_data_ptr<int>();
+    } else {
+        const Tensor& cu = tensor(a[2], "cu_seqlens");
+        r.B = check_offsets(cu, "cu_seqlens", dev);
+        r.cu_seqlens = cu.const_data_ptr<int>();
+        r.seq_lens = check(tensor(a[3], "seq_lens"), "seq_lens", dev, at::kInt, {{(int64_t)r.B}}).const_data_ptr<int>();
+    }
+    r.halves = truth(a[8]);
+    const int64_t n = r.halves ? d / 2 : d;
+    const auto weight = [&](PyObject* o, const char* name) {
+        return o == Py_None ? nullptr : check(tensor(o, name), name, dev, at::kFloat, {{n}}).const_data_ptr<float>();
+    };
+    r.q_weight = weight(a[4], "q_weight");
+    r.k_weight = weight(a[5], "k_weight");
+    r.norm_eps = number(a[6]);
+    r.interleaved = truth(a[7]);
+    return r;
+}
+
+// Rows like `like` (or fresh and contiguous ones): the tensor and its token stride.
+struct RowsOut {
+    Tensor t;
+    int64_t stride;
+    RowsOut(PyObject* o, const char* name, const Tensor& like, c10::Device dev) {
+        if (o == Py_None) {
+            t = fresh_tensor(like.sizes(), at::kBFloat16, dev);
+            stride = like.size(1) * like.size(2);
+        } else {
+            t = tensor(o, name);
+            stride = check_tokens(t, name, dev, like.size(1), like.size(2));
+            TORCH_CHECK_VALUE(t.size(0) == like.size(0), name, " must have the tokens of its input");
+        }
+    }
+    RowsOut() : stride(0) {}
+};
+
+PyObject* wrap(const Tensor& t) { return t.defined() ? THPVariable_Wrap(t) : none(); }
+
+// (q, k, [cos_sin .. halves: 9], q_out, k_out, stream)
+PyObject* norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    ready(n, 14);
+    const c10::Device dev = first_device(a[0], "fd_norm_rope");
+    const Place place(dev, a[13]);
+    const Tensor& q = tensor(a[0], "q");
+    const int64_t qs = check_tokens(q, "q", dev);
+    const int T = size_of(q.size(0), "q"), Hq = size_of(q.size(1), "q"), d = size_of(q.size(2), "q");
+    const bool keys = a[1] != Py_None;
+    TORCH_CHECK_VALUE(keys || a[12] == Py_None, "k_out without k");
+    int64_t ks = 0;
+    int Hkv = 0;
+    const void* kp = nullptr;
+    RowsOut ko;
+    if (keys) {
+        const Tensor& k = tensor(a[1], "k");
+        ks = check_tokens(k, "k", dev, -1, d);
+        TORCH_CHECK_VALUE(k.size(0) == T, "q and k must have the same number of tokens");
+        Hkv = size_of(k.size(1), "k");
+        kp = k.const_data_ptr();
+        ko = RowsOut(a[12], "k_out", k, dev);
+    }
+    const fd_rope r = rope_of(a + 2, T, d, dev);
+    const RowsOut qo(a[11], "q_out", q, dev);
+    expect(lib.norm_rope(q.const_data_ptr(), kp, qs, ks, T, Hq, Hkv, d, &r, qo.t.mutable_data_ptr(),
+                         keys ? ko.t.mutable_data_ptr() : nullptr, qo.stride, ko.stride, place.stream),
+           "fd_norm_rope");
+    THPObjectPtr t(PyTuple_New(2));
+    if (!t) throw python_error();
+    PyTuple_SET_ITEM(t.get(), 0, wrap(qo.t));
+    PyTuple_SET_ITEM(t.get(), 1, wrap(ko.t));
+    return t.release();
+    END_HANDLE_TH_ERRORS
+}
+
+// The queries of an append: rows, or none.
+struct Queries {
+    int64_t stride = 0;
+    int Hq = 0;
+    const void* data = nullptr;
+    RowsOut out;
+    Queries(PyObject* o, PyObject* to, const NewRows& r, c10::Device dev) {
+        TORCH_CHECK_VALUE(o != Py_None || to == Py_None, "q_out without q");
+        if (o == Py_None) return;
+        const Tensor& q = tensor(o, "q");
+        stride = check_tokens(q, "q", dev, -1, r.d);
+        TORCH_CHECK_VALUE(q.size(0) == r.T, "q and k must have the same number of tokens");
+        Hq = size_of(q.size(1), "q");
+        data = q.const_data_ptr();
+        out = RowsOut(to, "q_out", q, dev);
+    }
+    void* to() const { return out.t.defined() ? out.t.mutable_data_ptr() : nullptr; }
+};
+
+PyObject* with_queries(const Queries& q, std::initializer_list<PyObject*> items) {
+    THPObjectPtr t(PyTuple_New((Py_ssize_t)items.size() + 1));
+    if (!t) throw python_error();
+    PyTuple_SET_ITEM(t.get(), 0, wrap(q.out.t));
+    Py_ssize_t i = 1;
+    for (PyObject* o : items) {
+        Py_INCREF(o);
+        PyTuple_SET_ITEM(t.get(), i++, o);
+    }
+    return t.release();
+}
+
+// (q, k, v, slots, k_pages, v_pages, [cos_sin .. halves: 9], q_out, stream)
+PyObject* append_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    ready(n, 17);
+    const c10::Device dev = first_device(a[1], "fd_append_kv_paged_rope", "k");
+    const Place place(dev, a[16]);
+    const Tensor &k = tensor(a[1], "k"), &v = tensor(a[2], "v");
+    const NewRows r(k, v, a[3], dev);
+    const Tensor &kp = tensor(a[4], "k_pages"), &vp = tensor(a[5], "v_pages");
+    check_pool(kp, vp, r.d, dev);
+    TORCH_CHECK_VALUE(kp.size(1) == r.Hkv, "k_pages must have the heads of k");
+    const fd_rope rope = rope_of(a + 6, r.T, r.d, dev);
+    const Queries q(a[0], a[15], r, dev);
+    expect(lib.append_rope(q.data, k.const_data_ptr(), v.const_data_ptr(), q.stride, r.ks, r.vs, r.slots, r.T, q.Hq,
+                           r.Hkv, r.d, &rope, q.to(), q.out.stride, kp.mutable_data_ptr(), vp.mutable_data_ptr(),
+                           size_of(kp.size(0), "k_pages"), (int)kp.size(2), place.stream),
+           "fd_append_kv_paged_rope");
+    return with_queries(q, {a[4], a[5]});
+    END_HANDLE_TH_ERRORS
+}
+
+// (q, k, v, slots, k_pages, k_page_scales, v_pages, v_page_scales, [cos_sin .. halves: 9], q_out, stream)
+PyObject* append_rope_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    ready(n, 19);
+    const c10::Device dev = first_device(a[1], "fd_append_kv_paged_rope_fp8", "k");
+    const Place place(dev, a[18]);
+    const Tensor &k = tensor(a[1], "k"), &v = tensor(a[2], "v");
+    const NewRows r(k, v, a[3], dev);
+    const Fp8Pool pool(a + 4, r, dev);
+    const fd_rope rope = rope_of(a + 8, r.T, r.d, dev);
+    const Queries q(a[0], a[17], r, dev);
+    expect(lib.append_rope_fp8(q.data, k.const_data_ptr(), v.const_data_ptr(), q.stride, r.ks, r.vs, r.slots, r.T, q.Hq,
+                               r.Hkv, r.d, &rope, q.to(), q.out.stride, pool.k, pool.k_scales, pool.v, pool.v_scales,
+                               pool.pages, pool.page, place.stream),
+           "fd_append_kv_paged_rope_fp8");
+    return with_queries(q, {a[4], a[5], a[6], a[7]});
+    END_HANDLE_TH_ERRORS
+}
+
+// ---- differential attention -----------------------------------------------------------
+
+// (lam, norm_weight, norm_eps) of T tokens
+struct Mix {
+    const float* lambda;
+    int64_t stride = 0;
+    const float* weight = nullptr;
+    float eps;
+    Mix(PyObject* l, PyObject* w, PyObject* e, int64_t T, int64_t Hq, int64_t d, c10::Device dev) {
+        const Tensor& t = tensor(l, "lam");
+        on_device(t, "lam", dev);
+        TORCH_CHECK_VALUE(t.scalar_type() == at::kFloat, "lam must be ", at::kFloat, ", got ", t.scalar_type());
+        TORCH_CHECK_VALUE((t.dim() == 1 && t.size(0) == Hq) || (t.dim() == 2 && t.size(0) == T && t.size(1) == Hq),
+                          "lam must be [Hq] or [tokens, Hq], got ", t.sizes());
+        TORCH_CHECK_VALUE(Hq == 1 || t.stride(-1) == 1, "lam: the heads of a token must be contiguous");
+        if (t.dim() == 2) {
+            stride = T > 1 ? t.stride(0) : Hq;
+            TORCH_CHECK_VALUE(stride == 0 || stride >= Hq, "lam: tokens must not overlap");
+        }
+        lambda = t.const_data_ptr<float>();
+        if (w != Py_None)
+            weight = check(tensor(w, "norm_weight"), "norm_weight", dev, at::kFloat, {{d}}).const_data_ptr<float>();
+        eps = number(e);
+    }
+};
+
+// (q, k, v, lam, seq_lens, scale, norm_weight, norm_eps, num_splits, out, lse, out_code, want_lse, workspace, stream)
+PyObject* dense_diff(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    ready(n, 15);
+    const c10::Device dev = first_device(a[0], "fd_decode_dense_diff");
+    const Place place(dev, a[14]);
+    const Tensor& q = check_queries(a[0], dev);
+    const int B = (int)q.size(0), Hq = size_of(q.size(1), "q"), d = size_of(q.size(2), "q");
+    const Tensor& k = check(tensor(a[1], "k"), "k", dev, at::kBFloat16);
+    TORCH_CHECK_VALUE(k.dim() == 4 && k.size(0) == B && k.size(3) == d, "k must be [B, Hkv, L_max, d]");
+    const Tensor& v = check(tensor(a[2], "v"), "v", dev, at::kBFloat16, k.sizes());
+    const int Hkv = size_of(k.size(1), "k"), L = size_of(k.size(2), "k");
+    const int* lens = nullptr;
+    if (a[4] != Py_None)
+        lens = check(tensor(a[4], "seq_lens"), "seq_lens", dev, at::kInt, {{(int64_t)B}}).const_data_ptr<int>();
+    const Mix mix(a[3], a[6], a[7], B, Hq, d, dev);
+    const int splits = integer(a[8], "num_splits");
+    const Outputs o(B, Hq, d, a[9], a[10], integer(a[11], "out_dtype"), truth(a[12]), dev, 2);
+    const Workspace ws(lib.decode_diff_workspace_size(B, Hq, Hkv, L, d, splits, lens != nullptr), a[13], dev);
+    expect(lib.dense_diff(q.const_data_ptr(), k.const_data_ptr(), v.const_data_ptr(), lens, B, Hq, Hkv, L, d,
+                          scale_of(a[5], d / 2), mix.lambda, mix.stride, mix.weight, mix.eps, splits,
+                          o.out.mutable_data_ptr(), o.code, o.lse_data(), ws.data(), ws.bytes(), place.stream),
+           "fd_decode_dense_diff");
+    return pair(o);
+    END_HANDLE_TH_ERRORS
+}
+
+// (q, k_pages, v_pages, lam, page_table, num_pages, seq_lens, scale, norm_weight, norm_eps, num_splits, out, lse,
+//  out_code, want_lse, workspace, stream)
+PyObject* paged_diff(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    ready(n, 17);
+    const c10::Device dev = first_device(a[0], "fd_decode_paged_diff");
+    const Place place(dev, a[16]);
+    const Tensor& q = check_queries(a[0], dev);
+    const int B = (int)q.size(0), Hq = size_of(q.size(1), "q"), d = size_of(q.size(2), "q");
+    const Tensor &kp = tensor(a[1], "k_pages"), &vp = tensor(a[2], "v_pages");
+    check_pool(kp, vp, d, dev);
+    const int num_pages = check_num_pages(a[5], kp), Hkv = (int)kp.size(1), page = (int)kp.size(2);
+    const Tensor& table = tensor(a[4], "page_table");
+    const int max_pages = check_table(table, B, dev);
+    const Tensor& lens = check(tensor(a[6], "seq_lens"), "seq_lens", dev, at::kInt, {{(int64_t)B}});
+    const Mix mix(a[3], a[8], a[9], B, Hq, d, dev);
+    const int splits = integer(a[10], "num_splits");
+    const Outputs o(B, Hq, d, a[11], a[12], integer(a[13], "out_dtype"), truth(a[14]), dev, 2);
+    const int64_t L = (int64_t)max_pages * page;
+    const Workspace ws(L > INT_MAX ? 0 : lib.decode_diff_workspace_size(B, Hq, Hkv, (int)L, d, splits, 1), a[15], dev);
+    expect(lib.paged_diff(q.const_data_ptr(), kp.const_data_ptr(), vp.const_data_ptr(), table.const_data_ptr<int>(),
+                          max_pages, num_pages, lens.const_data_ptr<int>(), page, B, Hq, Hkv, d, scale_of(a[7], d / 2),
+                          mix.lambda, mix.stride, mix.weight, mix.eps, splits, o.out.mutable_data_ptr(), o.code,
+                          o.lse_data(), ws.data(), ws.bytes(), place.stream),
+           "fd_decode_paged_diff");
+    return pair(o);
+    END_HANDLE_TH_ERRORS
+}
+
+// (q, k, v, lam, cu_seqlens_q, cu_seqlens_k, scale, norm_weight, norm_eps, causal, num_splits, out, lse, out_code,
+//  want_lse, workspace, stream)
+PyObject* prefill_packed_diff(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    ready(n, 17);
+    const c10::Device dev = first_device(a[0], "fd_prefill_packed_diff");
+    const Place place(dev, a[16]);
+    const Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v");
+    const int64_t qs = check_tokens(q, "q", dev), d = q.size(2);
+    const int Hq = size_of(q.size(1), "q");
+    const int64_t ks = check_tokens(k, "k", dev, -1, d);
+    const int Hkv = size_of(k.size(1), "k");
+    const int64_t vs = check_tokens(v, "v", dev, Hkv, d);
+    TORCH_CHECK_VALUE(v.size(0) == k.size(0), "k and v must have the same number of tokens");
+    const Tensor& cq = tensor(a[4], "cu_seqlens_q");
+    const int B = check_offsets(cq, "cu_seqlens_q", dev);
+    const Tensor& ck = a[5] == Py_None ? cq : tensor(a[5], "cu_seqlens_k");
+    if (a[5] != Py_None) check(ck, "cu_seqlens_k", dev, at::kInt, {{(int64_t)B + 1}});
+    const int tq = size_of(q.size(0), "q"), tk = size_of(k.size(0), "k"), splits = integer(a[10], "num_splits");
+    const Mix mix(a[3], a[7], a[8], tq, Hq, d, dev);
+    const Outputs o(tq, Hq, d, a[11], a[12], integer(a[13], "out_dtype"), truth(a[14]), dev, 2);
+    const Workspace ws(lib.prefill_diff_workspace_size(B, tq, Hq, Hkv, tk, (int)d, splits), a[15], dev);
+    expect(lib.prefill_packed_diff(q.const_data_ptr(), k.const_data_ptr(), v.const_data_ptr(), qs, ks, vs,
+                                   cq.const_data_ptr<int>(), ck.const_data_ptr<int>(), B, tq, tk, Hq, Hkv, (int)d,
+                                   scale_of(a[6], d / 2), truth(a[9]), mix.lambda, mix.stride, mix.weight, mix.eps,
+                                   splits, o.out.mutable_data_ptr(), o.code, o.lse_data(), ws.data(), ws.bytes(),
+                                   place.stream),
+           "fd_prefill_packed_diff");
+    return pair(o);
+    END_HANDLE_TH_ERRORS
+}
+
+// (q, k_pages, v_pages, lam, page_table, num_pages, cu_seqlens_q, seq_lens, scale, norm_weight, norm_eps, causal,
+//  num_splits, out, lse, out_code, want_lse, workspace, stream)
+PyObject* prefill_paged_diff(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    ready(n, 19);
+    const c10::Device dev = first_device(a[0], "fd_prefill_paged_diff");
+    const Place place(dev, a[18]);
+    const Tensor &q = tensor(a[0], "q"), &kp = tensor(a[1], "k_pages"), &vp = tensor(a[2], "v_pages");
+    const int64_t qs = check_tokens(q, "q", dev), d = q.size(2);
+    const int Hq = size_of(q.size(1), "q"), tq = size_of(q.size(0), "q");
+    check_pool(kp, vp, d, dev);
+    const int num_pages = check_num_pages(a[5], kp), Hkv = (int)kp.size(1), page = (int)kp.size(2);
+    const Tensor &cq = tensor(a[6], "cu_seqlens_q"), &table = tensor(a[4], "page_table");
+    const int B = check_offsets(cq, "cu_seqlens_q", dev);
+    const int max_pages = check_table(table, B, dev);
+    const Tensor& lens = check(tensor(a[7], "seq_lens"), "seq_lens", dev, at::kInt, {{(int64_t)B}});
+    const int splits = integer(a[12], "num_splits");
+    const Mix mix(a[3], a[9], a[10], tq, Hq, d, dev);
+    const Outputs o(tq, Hq, d, a[13], a[14], integer(a[15], "out_dtype"), truth(a[16]), dev, 2);
+    const int64_t L = (int64_t)max_pages * page;
+    const Workspace ws(L > INT_MAX ? 0 : lib.prefill_diff_workspace_size(B, tq, Hq, Hkv, (int)L, (int)d, splits), a[17],
+                       dev);
+    expect(lib.prefill_paged_diff(q.const_data_ptr(), kp.const_data_ptr(), vp.const_data_ptr(), qs,
+                                  table.const_data_ptr<int>(), max_pages, num_pages, cq.const_data_ptr<int>(),
+                                  lens.const_data_ptr<int>(), page, B, tq, Hq, Hkv, (int)d, scale_of(a[8], d / 2),
+                                  truth(a[11]), mix.lambda, mix.stride, mix.weight, mix.eps, splits,
+                                  o.out.mutable_data_ptr(), o.code, o.lse_data(), ws.data(), ws.bytes(), place.stream),
+           "fd_prefill_paged_diff");
+    return pair(o);
     END_HANDLE_TH_ERRORS
 }
 
@@ -492,7 +825,14 @@ PyObject* bind(PyObject*, PyObject* args) {
           get(l.shared_workspace_size, "fd_shared_prefix_workspace_size") &&
           get(l.paged_shared, "fd_decode_paged_shared_prefix") &&
           get(l.dense_shared, "fd_decode_dense_shared_prefix") && get(l.assign_pages, "fd_assign_pages") &&
-          get(l.append, "fd_append_kv_paged") && get(l.append_fp8, "fd_append_kv_paged_fp8"))) {
+          get(l.append, "fd_append_kv_paged") && get(l.append_fp8, "fd_append_kv_paged_fp8") &&
+          get(l.norm_rope, "fd_norm_rope") && get(l.append_rope, "fd_append_kv_paged_rope") &&
+          get(l.append_rope_fp8, "fd_append_kv_paged_rope_fp8") &&
+          get(l.decode_diff_workspace_size, "fd_decode_diff_workspace_size") &&
+          get(l.dense_diff, "fd_decode_dense_diff") && get(l.paged_diff, "fd_decode_paged_diff") &&
+          get(l.prefill_diff_workspace_size, "fd_prefill_diff_workspace_size") &&
+          get(l.prefill_packed_diff, "fd_prefill_packed_diff") &&
+          get(l.prefill_paged_diff, "fd_prefill_paged_diff"))) {
         PyErr_Format(PyExc_ImportError, "%s lacks an entry point of this binding", path);
         return nullptr;
     }
@@ -510,6 +850,13 @@ PyMethodDef methods[] = {FD_FAST(prefill_packed),
                          FD_FAST(assign_pages),
                          FD_FAST(append_kv),
                          FD_FAST(append_kv_fp8),
+                         FD_FAST(norm_rope),
+                         FD_FAST(append_rope),
+                         FD_FAST(append_rope_fp8),
+                         FD_FAST(dense_diff),
+                         FD_FAST(paged_diff),
+                         FD_FAST(prefill_packed_diff),
+                         FD_FAST(prefill_paged_diff),
                          {"bind", bind, METH_VARARGS, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", "compiled half of the binding", -1, methods,

@@ -192,6 +192,60 @@ cudaError_t launch_merge_list(const float* part_o, const float* part_ml, const i
                               const int32_t* lens = nullptr, int len_most = 0);
 cudaError_t merge_status_read(unsigned* bits, bool clear);
 
+// Differential attention (fd_diff.cu, fd_rows_diff.cu): what joins a head's two maps.
+struct DiffMix {
+    const float* lambda;      // of token t, query head h: lambda[t * lambda_stride + h]
+    long long lambda_stride;  // 0: the same for all tokens
+    const float* weight;      // [D] norm of the difference, or null
+    float eps;
+};
+// Decode with DecodeArgs as above (bf16 cache, lse [B, Hq, 2]); records of both maps:
+// part_o [B, Hq, 2, splits, D], part_ml [B, Hq, 2, splits, 2].
+int diff_ctas_per_sm(int D, int G, bool paged);
+cudaError_t launch_decode_diff(const DecodeArgs& a, const DiffMix& mix, cudaStream_t stream);
+// Prompts with RowsArgs as above (sequences by offsets; no row_lens, no own tokens); lse and records
+// [total_q, Hq, 2, ..].  A tile has rows_diff_tokens tokens.
+int rows_diff_tokens(int G);
+long long rows_diff_tiles(int B, int total_q, int G);
+cudaError_t launch_rows_diff(const RowsArgs& a, const DiffMix& mix, cudaStream_t stream);
+// Merge of `splits` records per row and map.  cu given: prompts, every record of the tokens
+// cu[0] .. cu[B] - 1 is written.  cu null: a decode's chunks, as many as the lengths have.
+cudaError_t launch_merge_diff(const float* part_o, const float* part_ml, const int32_t* cu, int B, int tokens, int Hq,
+                              int D, int splits, const int32_t* lens, int L_max, int chunk_fixed, void* out,
+                              int out_bf16, float* lse, const DiffMix& mix, cudaStream_t stream);
+cudaError_t diff_status_read(unsigned* bits, bool clear);
+cudaError_t rows_diff_status_read(unsigned* bits, bool clear);
+
+// Norms and rotation (fd_rope.cu): of rows to rows, or (slots given) with the keys and values on
+// their way into the pages, which hold bf16, or e4m3 codes with the row scales.
+struct RopeArgs {
+    const uint16_t* q;        // [T, Hq, D], tokens the stride apart (elements); likewise the others
+    const uint16_t* k;
+    const uint16_t* v;
+    long long q_stride, k_stride, v_stride;
+    int T, Hq, Hkv, D;
+    const float* cos_sin;     // [max_pos, rot]: cosines, then sines
+    int max_pos, rot, interleaved, halves;
+    const int32_t* positions; // [T], or null: from cu [B + 1] and lens [B]
+    const int32_t* cu;
+    const int32_t* lens;
+    int B;
+    const float* q_weight;    // [D], or [D / 2] with halves; or null
+    const float* k_weight;
+    float eps;
+    uint16_t* q_out;
+    uint16_t* k_out;
+    long long q_out_stride, k_out_stride;
+    const int64_t* slots;     // [T]
+    int num_pages;
+    void* k_pages;
+    void* v_pages;
+    float* k_scales;
+    float* v_scales;
+};
+cudaError_t launch_rope(const RopeArgs& a, cudaStream_t stream);
+cudaError_t rope_status_read(unsigned* bits, bool clear);
+
 // Page assignment and cache append (fd_pages.cu).
 struct AssignArgs {
     const int32_t* cached_lens;
