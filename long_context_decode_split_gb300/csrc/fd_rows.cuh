@@ -149,10 +149,7 @@ __device__ __forceinline__ int visible_keys(const RowsParams& p, const RowsItem&
 
 constexpr int kRows = 128;    // rows of a tile: the lanes of an accumulator in tensor memory
 constexpr int kBlock = 128;   // keys per step
-constexpr int kThreads = 384; // two softmax warpgroups, then the copy warp, two MMA warps and an idle one
-constexpr int kCopyWarp = 8, kMmaWarp = 9;  // (kMmaWarp + i issues pipeline i's products)
-// Registers per thread after the split: 168 x 384 at launch = 216 x 256 + 72 x 128.
-constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
+constexpr int kUnit = 64;     // keys per step of a map
 
 // A running maximum is replaced only when a row exceeds it by more than this
 // (log2 units): the weights then stay below 2^8, far inside binary32 and bf16
@@ -166,6 +163,11 @@ constexpr float kRescaleAt = 8.f;
 //              the query and key rows, and both the same values
 enum RowsMode { kOneTile, kTwoTiles, kTwoMaps };
 
+constexpr int kThreads = 384; // two softmax warpgroups, then the copy warp, two MMA warps and an idle one
+constexpr int kCopyWarp = 8, kMmaWarp = 9;  // (kMmaWarp + i issues pipeline i's products)
+// Registers per thread after the split: 168 x 384 at launch = 216 x 256 + 72 x 128.
+constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;
+
 template <int D, RowsMode MODE>
 struct RowsGeo {
     static constexpr bool SHARED = MODE != kOneTile;  // every block is for both pipelines
@@ -178,7 +180,8 @@ struct RowsGeo {
     // (Every consumer of a ring waits for every tile of it: a barrier's parity
     // tells only two phases apart.)
     static constexpr int RING = SHARED ? STAGES : STAGES / 2;
-    static constexpr int SMEM = 1024 + (TILES + STAGES) * TILE + (2 * STAGES + 18) * 8 + 16 + 2 * 64 + 16 + 2 * 128 * 4;
+    static constexpr int SMEM = 1024 + (TILES + STAGES) * TILE + (2 * STAGES + 18) * 8 + 16 + 2 * 64 + 16 + 2 * 128 * 4 +
+                                (MODE == kTwoMaps ? D * 4 : 0);
     static_assert(SMEM <= 232448, "shared memory of a CTA");
 };
 
@@ -224,6 +227,28 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
         "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
         "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+// The same of 16 columns.
+__device__ __forceinline__ void tmem_ld16(uint32_t (&r)[16], uint32_t addr) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr));
+}
+__device__ __forceinline__ void tie16(uint32_t (&r)[16]) {
+    asm volatile(""
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15]));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+            addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -343,12 +368,12 @@ __device__ __forceinline__ int pages_of(const RowsParams& p, const RowsItem& it)
 
 // A piece of work as the copy warp hands it to the others.
 struct Work {
-    int valid;  // 0: there is no more
+    int valid;  // 0: there is no more; 2 (maps): once more, with care
     RowsItem it;
     int h;
     int c0, c1;  // its keys [c0, c1)
     int rec;     // its record
-    int nb[2];   // blocks of keys of each pipeline
+    int nb[2];   // blocks of keys of each pipeline (maps: blocks, and units of kUnit keys)
 };
 
 // 32 bytes to global memory: whole sectors from one thread.  `wide`: the
@@ -377,87 +402,271 @@ __device__ __forceinline__ void mark_empty(float* part_ml, int token, int tokens
     }
 }
 
-// The end of a row whose two maps are complete: warpgroup i holds the exp-sum of map i and writes half of
-// the channels of O0 / l0 - lambda O1 / l1, normalised where there is a weight.  o_at: O of map 0 in tensor
-// memory, map 1 behind it.  A thread tells the other warpgroup its factor, then its sum of squares.
+// The end of a row whose two maps are complete: warpgroup i knows the factor of map i and writes half of the channels
+// of factor0 O0 + factor1 O1 (1 / l0 and -lambda / l1), normalised where there is a weight.  o_at: O of map 0 in
+// tensor memory, map 1 behind it.  A thread tells the other warpgroup its factor, then its sum of squares.  This code
+// runs once a piece, and fetching it takes longer than running it: one small loop for both passes over the
+// channels (32 at a time and a loop each, 32 prompts of 512: 2800 cycles a piece, 4900 with the norm).
 template <int D>
-__device__ __forceinline__ void write_difference(const RowsParams& p, float* join, int r, int i, size_t row, int token,
-                                                 int head, bool live, float l, float inv, bool some, uint32_t o_at) {
-    constexpr int MINE = D / 2;
-    const float lambda = live ? p.mix.lambda[(size_t)token * p.mix.lambda_stride + head] : 0.f;
-    join[i * 128 + r] = i ? -lambda * inv : inv;
-    // (both O are complete: each warpgroup has waited for its own); a row that saw nothing has factors 0,
-    // and lambda may be anything there
-    if (l == 0.f) join[i * 128 + r] = 0.f;
+__device__ __forceinline__ void write_difference(const RowsParams& p, float* join, int r, int i, size_t row, bool live,
+                                                 float factor, bool some, uint32_t o_at) {
+    constexpr int MINE = D / 2, STEP = 16;
+    join[i * 128 + r] = factor;
     tc_fence_before();
-    named_barrier(1, 256);
+    named_barrier(1, 256);  // (both O are complete: each warpgroup has waited for its own)
     tc_fence_after();
     const float f0 = join[r], f1 = join[128 + r];
-    const auto channels = [&](int c, float (&f)[32]) {
-        uint32_t o[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) f[e] = 0.f;
-        if (!some) return;
-        tmem_ld32(o, o_at + c);
-        tmem_wait_ld();
-        tie32(o);
-        if (f0 != 0.f) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(o[e]) * f0;
-        }
-        tmem_ld32(o, o_at + D + c);
-        tmem_wait_ld();
-        tie32(o);
-        if (f1 != 0.f) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) f[e] += __uint_as_float(o[e]) * f1;
-        }
-    };
-    float by = 1.f;
-    if (p.mix.weight) {
-        float sum = 0.f;
+    const bool weight = p.mix.weight != nullptr;
+    float sum = 0.f, by = 1.f;
 #pragma unroll 1
-        for (int c = i * MINE; c < (i + 1) * MINE; c += 32) {
-            float f[32];
-            channels(c, f);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) sum = fmaf(f[e], f[e], sum);
+    for (int x = weight ? 0 : MINE; x < 2 * MINE; x += STEP) {
+        const bool first = x < MINE;  // of two passes: the sum of squares
+        if (x == MINE && weight) {
+            named_barrier(1, 256);  // the factors are read
+            join[i * 128 + r] = sum;
+            named_barrier(1, 256);
+            by = rsqrtf((join[r] + join[128 + r]) * (1.f / D) + p.mix.eps);
         }
-        named_barrier(1, 256);  // the factors are read
-        join[i * 128 + r] = sum;
-        named_barrier(1, 256);
-        by = rsqrtf((join[r] + join[128 + r]) * (1.f / D) + p.mix.eps);
-    }
-#pragma unroll 1
-    for (int c = i * MINE; c < (i + 1) * MINE; c += 32) {
-        float f[32];
-        channels(c, f);
-        if (p.mix.weight) {
+        const int c = i * MINE + (first ? x : x - MINE);
+        float f[STEP];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float4 w = reinterpret_cast<const float4*>(p.mix.weight + c)[e];
-                f[4 * e] *= by * w.x;
-                f[4 * e + 1] *= by * w.y;
-                f[4 * e + 2] *= by * w.z;
-                f[4 * e + 3] *= by * w.w;
+        for (int e = 0; e < STEP; ++e) f[e] = 0.f;
+        if (some) {
+            uint32_t o[STEP], o2[STEP];
+            tmem_ld16(o, o_at + c);
+            tmem_ld16(o2, o_at + D + c);
+            tmem_wait_ld();
+            tie16(o);
+            tie16(o2);
+#pragma unroll
+            for (int e = 0; e < STEP; ++e) {
+                if (f0 != 0.f) f[e] = __uint_as_float(o[e]) * f0;
+                if (f1 != 0.f) f[e] = fmaf(__uint_as_float(o2[e]), f1, f[e]);
             }
         }
+        if (first) {
+#pragma unroll
+            for (int e = 0; e < STEP; ++e) sum = fmaf(f[e], f[e], sum);
+            continue;
+        }
         if (!live) continue;
+        if (weight) {
+#pragma unroll
+            for (int e = 0; e < STEP; e += 4) {
+                const float4 w = *reinterpret_cast<const float4*>(join + 256 + c + e);  // (the kernel's copy)
+                f[e] *= by * w.x;
+                f[e + 1] *= by * w.y;
+                f[e + 2] *= by * w.z;
+                f[e + 3] *= by * w.w;
+            }
+        }
         if (p.out_bf16) {
-            uint32_t x[16];
+            uint32_t y[STEP / 2];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] = pack_bf16(f[2 * e], f[2 * e + 1]);
-            store32(static_cast<uint16_t*>(p.out) + row * D + c, x, p.wide);
-            store32(static_cast<uint16_t*>(p.out) + row * D + c + 16, x + 8, p.wide);
+            for (int e = 0; e < STEP / 2; ++e) y[e] = pack_bf16(f[2 * e], f[2 * e + 1]);
+            store32(static_cast<uint16_t*>(p.out) + row * D + c, y, p.wide);
         } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                store32(static_cast<float*>(p.out) + row * D + c + 8 * e, reinterpret_cast<uint32_t*>(f) + 8 * e,
-                        p.wide);
+            float* to = static_cast<float*>(p.out) + row * D + c;
+            store32(to, reinterpret_cast<uint32_t*>(f), p.wide);
+            store32(to + 8, reinterpret_cast<uint32_t*>(f) + 8, p.wide);
         }
     }
     tc_fence_before();
     named_barrier(1, 256);  // both O and the factors are read
+}
+
+// The softmax of map i, a warpgroup each, one row a thread, in units of 64 keys.  A row's reference m is the maximum
+// of its first unit, and the others are weighed by it as they come: maxima are a fifth of a unit's instructions,
+// and the warps' time bounds the pass.  Scores may rise above m by as much as binary32 and bf16 have room
+// for; a row whose sum passes kMostSum (or whose first unit gave it no reference) marks its piece, which the
+// copy warp hands out once more, with care: then every unit raises m to its maximum, and O is rescaled.
+constexpr float kMostSum = 18446744073709551616.f;  // 2^64
+
+template <int D, bool PAGED, bool FINE>
+__device__ __forceinline__ void softmax_maps(const RowsParams& p, const Work* work, volatile int* redo,
+                                             uint64_t* work_full, uint64_t* work_empty, const unsigned char* sq, uint64_t* q_full,
+                                             uint64_t* q_empty, uint64_t* s_full, uint64_t* p_full, float* join,
+                                             uint32_t tmem) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int i = warp >> 2, r = threadIdx.x & 127;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+    const uint32_t s_at = tmem + lanes + i * 128, o_at = tmem + lanes + 256;
+    const int tk = r / p.G;
+    bool ok = true;
+    uint32_t n = 0, qn = 0;  // turns (see the products), pieces with keys
+    const auto hand_over = [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[i]);
+    };
+    for (int wn = 0;; ++wn) {
+        const int slot = wn & 1;
+        ok = ok && warp_wait(&work_full[slot], (uint32_t)(wn >> 1) & 1u, p.wait_limit_ns);
+        if (named_barrier_or(2, 256, !ok)) break;  // all of them stop, or none
+        const Work& wk = work[slot];
+        if (!wk.valid) break;
+        const bool careful = wk.valid == 2;
+        RowsItem it = wk.it;
+        it.own = 0;  // known to be
+        const int h = wk.h, c0 = wk.c0, c1 = wk.c1, rec_at = wk.rec, units = wk.nb[1];
+        const bool live = tk < p.tok && it.t0 + tk < it.Lq;
+        const int lim = live ? min(visible_keys(p, it, it.t0 + tk), c1) - c0 : 0;
+        const int least = __reduce_min_sync(0xffffffffu, lim);
+        const int head = h * p.G + r - tk * p.G, token = it.q0 + it.t0 + tk;
+        const size_t row = (size_t)token * p.Hq + head;
+        float lambda = -1.f;  // (wanted at the end)
+        if (i == 1 && live && p.direct) lambda = p.mix.lambda[(size_t)token * p.mix.lambda_stride + head];
+        const int32_t* table = PAGED ? table_of(p, it) : nullptr;
+        const int pages = PAGED ? pages_of(p, it) : 0;
+        float m = -INFINITY;
+        float2 l2 = make_float2(0.f, 0.f);
+        uint32_t s[2][32];
+        uint32_t bads = 0;  // of 32 units: pages outside the pool
+        if (units > 0) {
+            if (!FINE) {  // the row's queries to tensor memory
+                ok = warp_wait(q_full, qn & 1u, p.wait_limit_ns);
+                uint32_t q[D / 4];
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c) {
+                    const int at = D == 128 ? c : (D / 16) * i + c;  // 16-byte chunk of the row in its box
+                    const uint4 x = lds128(sq + (D == 128 ? i * (128 * 128) : 0) + r * 128 + ((at ^ (r & 7)) << 4));
+                    q[4 * c] = x.x;
+                    q[4 * c + 1] = x.y;
+                    q[4 * c + 2] = x.z;
+                    q[4 * c + 3] = x.w;
+                }
+                if constexpr (D == 128) tmem_st32(s_at + 96, q);
+                else tmem_st16(s_at + 96, q);
+                tmem_wait_st();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(q_empty);
+            }
+            ++qn;
+            hand_over();
+            ok = ok && warp_wait(&s_full[i], n & 1u, p.wait_limit_ns);
+            ++n;
+            tc_fence_after();
+            tmem_ld32(s[0], s_at);
+            tmem_ld32(s[1], s_at + 32);
+            tmem_wait_ld();
+            tie32(s[0]);
+            tie32(s[1]);
+            hand_over();
+        }
+        for (int u = 0; ok && u < units; ++u, ++n) {
+            if (PAGED && (u & 31) == 0) {  // 32 pages at a time
+                const int pi = c0 / kTile + u + lane;
+                const int pg = pi < pages ? table[pi] : 0;
+                bads = __ballot_sync(0xffffffffu, pi < pages && (pg < 0 || pg >= p.num_pages));
+            }
+            const bool bad = PAGED && (bads >> (u & 31) & 1u);
+            const int left = bad ? 0 : lim - u * kUnit;
+            if (bad || least < (u + 1) * kUnit) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int k = min(max(left - 32 * c, 0), 32);
+                    const uint32_t seen = k < 32 ? (1u << k) - 1u : 0xffffffffu;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (!(seen & 1u << e)) s[c][e] = 0xff800000u;  // -inf
+                }
+            }
+            if (u == 0 || careful) {
+                float mx[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    mx[c] = __uint_as_float(s[c / 2][16 * (c & 1)]);
+#pragma unroll
+                    for (int e = 1; e < 16; ++e) mx[c] = fmaxf(mx[c], __uint_as_float(s[c / 2][16 * (c & 1) + e]));
+                }
+                const float mn = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2);
+                const float a = mn == m ? 1.f : exp2_approx(m - mn);
+                m = mn;
+                l2 = f2mul(l2, make_float2(a, a));
+                if (u > 0) {
+                    ok = warp_wait(&s_full[i], n & 1u, p.wait_limit_ns);  // the product with the last P is in O
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 16) {
+                        uint32_t o[16];
+                        tmem_ld16(o, o_at + i * D + c);
+                        tmem_wait_ld();
+                        tie16(o);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+                        tmem_st16(o_at + i * D + c, o);
+                    }
+                }
+            }
+            const float base = m == -INFINITY ? 0.f : m;
+            const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nb2 = make_float2(-base, -base);
+            uint32_t w[32], lo[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+                const int c = e / 16, x = 2 * (e % 16);
+                float2 f = f2fma(make_float2(__uint_as_float(s[c][x]), __uint_as_float(s[c][x + 1])), sc2, nb2);
+                f = make_float2(exp2_approx(f.x), exp2_approx(f.y));
+                l2 = __fadd2_rn(l2, f);
+                if (FINE) split_bf16(f.x, f.y, w[e], lo[e]);
+                else w[e] = pack_bf16(f.x, f.y);
+            }
+            ok = warp_wait(&s_full[i], n & 1u, p.wait_limit_ns);
+            if (!ok) break;
+            tc_fence_after();
+            if (u + 1 < units) {
+                tmem_ld32(s[0], s_at);
+                tmem_ld32(s[1], s_at + 32);
+            }
+            tmem_st32(s_at + 64, w);
+            if (FINE) tmem_st32(s_at + 96, lo);
+            tmem_wait_ld();
+            tie32(s[0]);
+            tie32(s[1]);
+            tmem_wait_st();
+            hand_over();
+        }
+        // l is 0 only where nothing of weight was seen; NaN passes on
+        float l = ok ? l2.x + l2.y : 0.f;
+        float f = l != 0.f ? 1.f / l : 0.f;
+        const bool again = !careful && lim > 0 && !(l < kMostSum && m > -INFINITY);
+        if (__any_sync(0xffffffffu, again) && lane == 0) redo[slot] = 1;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&work_empty[slot]);
+        const size_t rec = (2 * row + i) * p.rec_stride + rec_at;
+        if (live && !p.direct) {
+            p.part_ml[2 * rec] = m;
+            p.part_ml[2 * rec + 1] = l;
+        } else if (live && p.lse) {
+            p.lse[2 * row + i] = l != 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
+        }
+        if (units > 0) {
+            ok = ok && warp_wait(&s_full[i], n & 1u, p.wait_limit_ns);
+            ++n;
+        }
+        tc_fence_after();
+        if (!p.direct) {
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+                uint32_t o[16];
+                if (units > 0) {
+                    tmem_ld16(o, o_at + i * D + c);
+                    tmem_wait_ld();
+                    tie16(o);
+                }
+                if (!live || f == 0.f) continue;  // (the merge skips records with l = 0)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                store32(p.part_o + rec * D + c, o, p.wide);
+                store32(p.part_o + rec * D + c + 8, o + 8, p.wide);
+            }
+            tc_fence_before();
+            continue;
+        }
+        write_difference<D>(p, join, r, i, row, live, f != 0.f ? -f * lambda : 0.f, units > 0, o_at);
+    }
+    if (!ok && lane == 0) atomicOr(&g_status_rows, kStatusTimeout);
+    tc_fence_before();
 }
 
 // ---- the pass -------------------------------------------------------------------
@@ -533,7 +742,9 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
     Work* work = reinterpret_cast<Work*>(answer + 16);                      // [2]
     static_assert(sizeof(Work) <= 64, "room for two pieces of work");
     uint32_t* tmem_at = reinterpret_cast<uint32_t*>(work + 2);
-    float* join = reinterpret_cast<float*>(tmem_at + 4);  // [2][128] what the pipelines tell each other (single)
+    volatile int* redo = reinterpret_cast<volatile int*>(tmem_at + 1);  // [2] (maps) the piece in a slot is to be done once more
+    float* join = reinterpret_cast<float*>(tmem_at + 4);  // [2][128] what the pipelines tell each other (single, maps)
+    float* norm = join + 256;  // [D] (maps) the weights of the norm
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -543,7 +754,7 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], 1);
-            mbar_init(&q_empty[i], TWO ? 1 : 2);
+            mbar_init(&q_empty[i], TWO ? 1 : MAPS && !FINE ? 8 : 2);
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 4);
             mbar_init(&o_full[i], 1);
@@ -552,6 +763,7 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
             mbar_init(&drained[i], 1);
         }
         mbar_init(next_full, 1);
+        if (MAPS) redo[0] = redo[1] = 0;
         fence_barrier_init();
     }
     if (warp == kMmaWarp) tmem_alloc(tmem_at, 512);
@@ -566,6 +778,10 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
     const uint32_t tmem = *tmem_at;
     pdl_wait_primary();  // the previous kernel in the stream may still be running
     pdl_launch_dependents();
+    if constexpr (MAPS) {
+        // (the barriers before the first result order these writes)
+        if (p.mix.weight && threadIdx.x < D) norm[threadIdx.x] = p.mix.weight[threadIdx.x];
+    }
 
     if (warp >= kCopyWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
@@ -611,7 +827,8 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
                         int most = w.c1;
                         if (p.causal) most = min(most, w.it.Lk - w.it.Lq + first + ntok);
                         most -= w.c0;
-                        w.nb[i] = ntok > 0 && most > 0 ? (most + kBlock - 1) / kBlock : 0;
+                        const int step = MAPS && i ? kUnit : kBlock;
+                        w.nb[i] = ntok > 0 && most > 0 ? (most + step - 1) / step : 0;
                     }
                     // A part behind the end of the keys (a short context in a wide table has many) gets
                     // l = 0 in its records here; the merge then skips their O.  (Every 256th is handed on:
@@ -623,18 +840,39 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
                         some = false;
                     }
                 }
-                if (some) {
+                Work later;
+                bool again = false;  // (maps) w is an earlier piece once more, `later` the one that was due
+                if (some) do {
                     // hand it on (or the end)
                     const int slot = wn & 1;
                     ok = warp_wait(&work_empty[slot], ((uint32_t)(wn >> 1) & 1u) ^ 1u, p.wait_limit_ns);
                     if (!ok) break;
+                    if constexpr (MAPS) {
+                        if (again) w = later;
+                        // the piece that had this slot, and before the end the one in the other slot
+                        int from = redo[slot] ? slot : -1;
+                        if (from < 0 && !w.valid) {
+                            ok = warp_wait(&work_empty[slot ^ 1], ((uint32_t)((wn + 1) >> 1) & 1u) ^ 1u, p.wait_limit_ns);
+                            if (!ok) break;
+                            if (redo[slot ^ 1]) from = slot ^ 1;
+                        }
+                        again = from >= 0;
+                        if (again) {
+                            later = w;
+                            w = work[from];
+                            w.valid = 2;
+                            __syncwarp();
+                            if (lane == 0) redo[from] = 0;
+                            __syncwarp();
+                        }
+                    }
                     if (lane == 0) {
                         work[slot] = w;
                         mbar_arrive(&work_full[slot]);
                     }
                     ++wn;
                     if (!w.valid) break;
-                    const int blocks = max(w.nb[0], w.nb[1]);
+                    const int blocks = MAPS ? w.nb[0] : max(w.nb[0], w.nb[1]);
                     if (blocks > 0) {
                         auto query = [&](int i) {  // tile i of the queries
                             if (TWO && w.nb[i] == 0) return;
@@ -723,7 +961,8 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
                         }
                         if (!ok) break;
                     }
-                }
+                } while (MAPS && again);
+                if (!ok || !w.valid) break;
                 // all copies of this piece are under way: ask for the next one
                 if (lane == 0) {
                     mbar_arrive_expect_tx(next_full, 16);
@@ -798,7 +1037,7 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&work_empty[slot]);
                 if (!valid) break;
-                const int blocks = max(nb0, nb1);
+                const int blocks = MAPS ? nb0 : max(nb0, nb1);
                 if (blocks == 0) continue;
                 // the pipeline's rounds: blocks 0, 1, .. or every second one from i on
                 const int nb = SHARED ? (i ? nb1 : nb0) : (blocks + 1 - (int)i) / 2;
@@ -817,6 +1056,52 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
                 };
+                if constexpr (MAPS) {
+                    // Units of half a block, U of them.  A map's columns are S | P | Q (two terms: S | P P, with Q
+                    // in shared memory), and its warpgroup and this warp take turns:
+                    //   p_full 0: Q is in place; k = 1 .. U: S of unit k - 1 is in registers and P of unit k - 2
+                    //             in place; U + 1: the last P
+                    //   s_full k: P V of unit k - 2 and S of unit k are complete
+                    // so S of the next unit and the product with the last P run while a unit is weighed.
+                    const int units = nb1;
+                    if (FINE) ok = warp_wait(q_full, qn & 1u, p.wait_limit_ns);
+                    ++qn;
+                    uint32_t sk = 0, sv = 0;
+                    for (int k = 0; ok && k < units + 2; ++k, ++rounds) {
+                        const int u = k - 2;  // of P V
+                        if (k < units && !(k & 1)) sk = arrive(n0 + k);
+                        if (ok && u >= 0 && !(u & 1)) {
+                            sv = arrive(n0 + u + 1);
+                            if (ok) clear_tail(u / 2, sv);
+                        }
+                        ok = ok && warp_wait(&p_full[i], rounds & 1u, p.wait_limit_ns);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t va = desc_cols(ring_at + sv * TILE + (u & 1) * (kUnit * 128));
+                        const uint32_t ka = desc_rows(ring_at + sk * TILE + (k & 1) * (kUnit * 128)) + half;
+                        if (elect_one()) {
+                            if (u >= 0) {
+#pragma unroll
+                                for (int kk = 0; kk < (FINE ? 2 : 1) * kUnit / 16; ++kk)  // (lo lies behind hi)
+                                    mma_ts(o_tm, s_tm + 64 + kk * 8, va + (kk % (kUnit / 16) * 16 * 128 >> 4), IPV,
+                                           u > 0 || kk > 0);
+                                if ((u & 1) || u + 1 == units) mma_commit(&empty[sv]);
+                            }
+                            if (k < units) {
+#pragma unroll
+                                for (int kk = 0; kk < D / 32; ++kk) {
+                                    if (FINE) mma_ss(s_tm, q_desc + half + kk * 2, ka + kk * 2, mma_desc(kUnit, false), kk > 0);
+                                    else mma_ts(s_tm, s_tm + 96 + kk * 8, ka + kk * 2, mma_desc(kUnit, false), kk > 0);
+                                }
+                                if ((k & 1) || k + 1 == units) mma_commit(&empty[sk]);
+                                if (FINE && k + 1 == units) mma_commit(q_empty);
+                            }
+                            mma_commit(&s_full[i]);
+                        }
+                    }
+                    n0 += 2 * blocks;
+                    continue;
+                }
                 const uint32_t qt = TWO ? i : 0;
                 if (!TWO || nb > 0) {
                     ok = warp_wait(&q_full[qt], qn & 1u, p.wait_limit_ns);
@@ -858,6 +1143,9 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
                 warp_wait(&drained[i], 0, p.wait_limit_ns);
             }
         }
+    } else if constexpr (MAPS) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        softmax_maps<D, PAGED, FINE>(p, work, redo, work_full, work_empty, sq, q_full, q_empty, s_full, p_full, join, tmem);
     } else {
         // ---------------- softmax, one row per thread ----------------
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
@@ -876,7 +1164,7 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
             const Work& wk = work[slot];
             const bool valid = wk.valid != 0;
             RowsItem it = wk.it;
-            if (SHARED) it.own = 0;  // known to be
+            if (TWO) it.own = 0;  // known to be
             const int h = wk.h, c0 = wk.c0, c1 = wk.c1, rec_at = wk.rec;
             const int nb = i ? wk.nb[1] : wk.nb[0];
             const int all = wk.nb[0];
@@ -886,13 +1174,13 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
             const int first = it.t0 + (TWO ? i : 0) * p.tok;
             const bool live = tk < p.tok && first + tk < it.Lq;
             const int lim = live ? min(visible_keys(p, it, first + tk), c1) - c0 : 0;
-            const int rounds = SHARED ? nb : (nb + 1 - i) / 2;
+            const int rounds = TWO ? nb : (nb + 1 - i) / 2;
             const int32_t* table = PAGED ? table_of(p, it) : nullptr;
             const int pages = PAGED ? pages_of(p, it) : 0;
             float m = -INFINITY;
             float2 l2 = make_float2(0.f, 0.f);
             for (int round = 0; round < rounds; ++round) {
-                const int j = SHARED ? round : 2 * round + i;
+                const int j = TWO ? round : 2 * round + i;
                 const int left = lim - j * kBlock;  // visible keys from this block on
                 bool bad[2] = {false, false};
                 if (PAGED) {
@@ -975,8 +1263,7 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
             }
             const int head = h * p.G + r - tk * p.G;
             const size_t row = (size_t)(it.q0 + first + tk) * p.Hq + head;
-            const size_t stat = MAPS ? 2 * row + i : row;  // row of the statistics, and of the records
-            const size_t rec = stat * p.rec_stride + rec_at;
+            const size_t rec = row * p.rec_stride + rec_at;
             // l is 0 only where nothing of weight was seen.  A NaN or +inf score makes it NaN (m skips NaN
             // and may still be -inf), and that has to pass on to the result: hence no test l > 0.
             float l = ok ? l2.x + l2.y : 0.f;
@@ -985,12 +1272,12 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
                     p.part_ml[2 * rec] = m;
                     p.part_ml[2 * rec + 1] = l;
                 } else if (p.lse) {
-                    p.lse[stat] = l != 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
+                    p.lse[row] = l != 0.f ? (m + __log2f(l)) * kLn2 : -INFINITY;
                 }
             };
             // what does not need O goes before the wait for it
             const float inv_own = l != 0.f ? 1.f / l : 0.f;
-            if (SHARED && live) statistics();
+            if (TWO && live) statistics();
             if (ok && rounds > 0) {
                 ok = warp_wait(&o_full[i], o_round & 1u, p.wait_limit_ns);
                 ++o_round;
@@ -1002,13 +1289,7 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
             }
             // factors of the O of pipeline 0 and 1
             float f0 = i ? 0.f : 1.f, f1 = i ? 1.f : 0.f;
-            if constexpr (MAPS) {
-                if (p.direct) {
-                    write_difference<D>(p, join, r, i, row, it.q0 + first + tk, head, live, l, inv_own, all > 0, o_at);
-                    continue;
-                }
-            }
-            if (!SHARED) {
+            if (!TWO) {
                 // pipeline 0 learns m and l of pipeline 1 and tells the factors; each
                 // warpgroup then writes half of the channels of the joined result
                 if (i == 1) {
@@ -1038,9 +1319,9 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
                 uint32_t o[32];
 #pragma unroll
                 for (int e = 0; e < 32; ++e) f[e] = 0.f;
-                if (SHARED ? rounds > 0 : all > 0) {
-                    const float by = SHARED ? inv_own : f0;
-                    tmem_ld32(o, o_at + (SHARED ? i * D : 0) + c);
+                if (TWO ? rounds > 0 : all > 0) {
+                    const float by = TWO ? inv_own : f0;
+                    tmem_ld32(o, o_at + (TWO ? i * D : 0) + c);
                     tmem_wait_ld();
                     tie32(o);
                     if (by != 0.f) {
@@ -1048,7 +1329,7 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
                         for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(o[e]) * by;
                     }
                 }
-                if (!SHARED && all > 1) {
+                if (!TWO && all > 1) {
                     tmem_ld32(o, o_at + D + c);
                     tmem_wait_ld();
                     tie32(o);
@@ -1060,8 +1341,8 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
             };
             // This code runs once a piece: fetching it takes longer than running it, so its loops are
             // rolled up (32 prompts of 512: 116 us unrolled, 100 us).
-            constexpr int MINE = SHARED ? D : D / 2;  // channels that this warpgroup writes
-            const int c_mine = SHARED ? 0 : i * MINE;
+            constexpr int MINE = TWO ? D : D / 2;  // channels that this warpgroup writes
+            const int c_mine = TWO ? 0 : i * MINE;
             if (p.direct && p.out_bf16) {
                 uint16_t* dst = static_cast<uint16_t*>(p.out) + row * D;
 #pragma unroll 1
@@ -1078,7 +1359,7 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
             } else {
                 float* dst = p.direct ? static_cast<float*>(p.out) + row * D : p.part_o + rec * D;
                 // the merge skips records with l = 0 (of a single tile, only pipeline 0 knows the joined l)
-                const bool wanted = live && (p.direct || (SHARED ? l != 0.f : f0 != 0.f || f1 != 0.f));
+                const bool wanted = live && (p.direct || (TWO ? l != 0.f : f0 != 0.f || f1 != 0.f));
 #pragma unroll 1
                 for (int c = c_mine; c < c_mine + MINE; c += 32) {
                     float f[32];
@@ -1089,9 +1370,9 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
                         store32(dst + c + 8 * e, reinterpret_cast<uint32_t*>(f) + 8 * e, p.wide);
                 }
             }
-            if (!SHARED && live && i == 0) statistics();
+            if (!TWO && live && i == 0) statistics();
             tc_fence_before();
-            if (!SHARED) named_barrier(1, 256);  // both O and the factors are read
+            if (!TWO) named_barrier(1, 256);  // both O and the factors are read
         }
         if (!ok && lane == 0) atomicOr(&g_status_rows, kStatusTimeout);
         tc_fence_before();

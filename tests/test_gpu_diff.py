@@ -281,3 +281,63 @@ def test_binding_refusals(fd):
         fd.fd_decode_dense_diff(q, k, v, lam, norm_weight=rand(g, 0, 1, 128), norm_eps=0.0)
     with pytest.raises(fd.FdError):
         fd.fd_decode_dense_diff(q, k, v, lam, scale=-1.0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("splits", [1, 3])
+@pytest.mark.parametrize("case", ["rising", "jump", "first masked", "deep"])
+def test_scores_far_above_the_first_ones(fd, case, splits, dtype):
+    """Rows whose scores rise by hundreds behind their first keys, in one map or both, fall behind by hundreds, or
+    start on a page that is left out."""
+    g = generator(16)
+    T, L, Hq, Hkv, d = 70, 700, 4, 2, 128
+    kp, vp, table, P, have = paged(g, [L], Hkv, d)
+    q, lam, w = randn(g, T, Hq, d), rand(g, 0.1, 0.6, Hq), rand(g, 0.2, 1.5, d)
+    k, v = (x.clone() for x in have[0])
+    q[..., 0] = q[..., 64] = 1.0
+    up = torch.zeros(L, device="cuda")
+    if case == "rising":
+        up = torch.arange(L, device="cuda") * 2.0
+    elif case == "jump":
+        up[650:] = 3000.0
+    elif case == "deep":
+        up[100:] = -3000.0
+    k[:, :, 0] = up.to(torch.bfloat16)[:, None]
+    if case != "jump":
+        k[:, :, 64] = up.to(torch.bfloat16)[:, None]
+    keep = torch.ones(L, dtype=torch.bool, device="cuda")
+    for j in range(-(-L // 64)):
+        part = k[64 * j:64 * j + 64]
+        kp[table[0, j], :, :part.shape[0]] = part.transpose(0, 1)
+    bad = case == "first masked"
+    if bad:
+        table[0, 0] = -1
+        keep[:64] = False
+    lim = limits(T, L)
+    out, lse = fd.fd_prefill_paged_diff(q, kp, vp, lam, table, P, ints([0, T]), ints([L]), norm_weight=w,
+                                        num_splits=splits, out_dtype=dtype)
+    assert fd.fd_device_status(clear=True) == (fd.FD_ERR_BAD_PAGE_TABLE if bad else fd.FD_OK)
+    ref = diff64(q, k[keep], v[keep], lam, lim - 64 * bad, 0.125, w,
+                 rounding=2.0 ** -8 if dtype == "bf16" else 2.0 ** -16)
+    check_diff(out, lse, ref, case)
+    one, z = fd.fd_decode_paged_diff(q[-1:].contiguous(), kp, vp, lam, table, P, ints([L]), norm_weight=w,
+                                     num_splits=splits, out_dtype=dtype)
+    fd.fd_device_status(clear=True)
+    check_diff(one, z, diff64(q[-1:], k[keep], v[keep], lam, lim[-1:] - 64 * bad, 0.125, w, rounding=2.0 ** -16))
+
+
+def test_many_pieces_once_more(fd):
+    """Every piece of a CTA and the last one too."""
+    g = generator(17)
+    B, n, Hq, Hkv, d = 40, 300, 8, 8, 64
+    T = B * n
+    q, k, v, lam = randn(g, T, Hq, d), randn(g, T, Hkv, d), randn(g, T, Hkv, d), rand(g, 0.1, 0.6, Hq)
+    q[..., 3] = 1.0
+    rise = (torch.arange(T, device="cuda") % n).float()
+    k[:, ::3, 3] = (rise * 4).to(torch.bfloat16)[:, None]  # some heads' pieces, not all
+    cu = ints([n * b for b in range(B + 1)])
+    out, lse = fd.fd_prefill_packed_diff(q, k, v, lam, cu)
+    for b in range(0, B, 7):
+        a = slice(n * b, n * b + n)
+        check_diff(out[a], lse[a], diff64(q[a], k[a], v[a], lam, limits(n, n), 1 / math.sqrt(d // 2)))
+    assert fd.fd_device_status(clear=True) == DEVICE_OK
