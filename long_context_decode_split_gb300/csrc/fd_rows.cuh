@@ -842,7 +842,8 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
                 }
                 Work later;
                 bool again = false;  // (maps) w is an earlier piece once more, `later` the one that was due
-                if (some) do {
+            [[maybe_unused]] hand_on:
+                if (some) {
                     // hand it on (or the end)
                     const int slot = wn & 1;
                     ok = warp_wait(&work_empty[slot], ((uint32_t)(wn >> 1) & 1u) ^ 1u, p.wait_limit_ns);
@@ -961,8 +962,10 @@ rows_kernel(const __grid_constant__ RowsMaps maps, const RowsParams p) {
                         }
                         if (!ok) break;
                     }
-                } while (MAPS && again);
-                if (!ok || !w.valid) break;
+                    if constexpr (MAPS) {
+                        if (again) goto hand_on;
+                    }
+                }
                 // all copies of this piece are under way: ask for the next one
                 if (lane == 0) {
                     mbar_arrive_expect_tx(next_full, 16);
