@@ -17,6 +17,8 @@
 // hi + lo for float32 results (2^-16).
 #pragma once
 
+#include <climits>
+
 #include "fd_device.cuh"
 #include "fd_internal.h"
 #include "fd_tma.h"
@@ -511,7 +513,8 @@ __device__ __forceinline__ void softmax_maps(const RowsParams& p, const Work* wo
         const int h = wk.h, c0 = wk.c0, c1 = wk.c1, rec_at = wk.rec, units = wk.nb[1];
         const bool live = tk < p.tok && it.t0 + tk < it.Lq;
         const int lim = live ? min(visible_keys(p, it, it.t0 + tk), c1) - c0 : 0;
-        const int least = __reduce_min_sync(0xffffffffu, lim);
+        // (rows that belong to no query may hold anything: they meet no other row)
+        const int least = __reduce_min_sync(0xffffffffu, live ? lim : INT_MAX);
         const int head = h * p.G + r - tk * p.G, token = it.q0 + it.t0 + tk;
         const size_t row = (size_t)token * p.Hq + head;
         float lambda = -1.f;  // (wanted at the end)
@@ -561,7 +564,7 @@ __device__ __forceinline__ void softmax_maps(const RowsParams& p, const Work* wo
             }
             const bool bad = PAGED && (bads >> (u & 31) & 1u);
             const int left = bad ? 0 : lim - u * kUnit;
-            if (bad || least < (u + 1) * kUnit) {
+            if (bad || least - u * kUnit < kUnit) {
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     const int k = min(max(left - 32 * c, 0), 32);
