@@ -590,8 +590,10 @@ FD_API int fd_append_kv_paged_rope_fp8(const void* q, const void* k, const void*
  *   out           as the calls without _diff
  *   lse           [tokens, Hq, 2] float32 or NULL: of either map
  * A query that sees no key gets out = 0 and lse = -inf.  A visible score that is NaN
- * or +inf makes its row NaN; one of -inf weighs nothing.  Values that a query sees
- * have to be finite.
+ * or +inf makes its row NaN; one of -inf weighs nothing.  Values of a query's
+ * sequence have to be finite and, in the prompt calls, below 2^80 in magnitude.
+ * (The prompt calls take a part of the keys twice where scores rise more than 28
+ * above those of its first 64 keys, or are not finite.)
  * Scores, maxima, sums, the maps' outputs, their difference and its norm are
  * binary32.  The weights of either map enter the product with V as the other calls'
  * do: in two bf16 terms in the decode (2^-16), and in the prompt calls in two

@@ -1144,7 +1144,10 @@ int rope_entry(fd::RopeArgs& a, const fd_rope* r, bool paged, bool fp8, int page
     const long long pool = (long long)a.num_pages * a.Hkv * kTile * a.D * (fp8 ? 1 : 2);
     const Strided others[] = {whole(a.k_pages, pool), whole(a.v_pages, pool),
                               whole(r->cos_sin, 4LL * r->max_pos * r->rot), whole(r->q_weight, 4LL * dh),
-                              whole(r->k_weight, 4LL * dh)};
+                              whole(r->k_weight, 4LL * dh), whole(r->positions, 4LL * a.T),
+                              whole(r->cu_seqlens, 4LL * r->B + 4), whole(r->seq_lens, 4LL * r->B),
+                              whole(a.slots, 8LL * a.T), whole(a.k_scales, 4LL * a.num_pages * a.Hkv * kTile),
+                              whole(a.v_scales, 4LL * a.num_pages * a.Hkv * kTile)};
     for (const Strided& o : others)
         if ((q && overlap(qo, o)) || (k && !paged && overlap(ko, o))) return FD_ERR_INVALID_ARG;
     a.cos_sin = r->cos_sin;

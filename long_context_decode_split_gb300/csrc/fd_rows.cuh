@@ -482,7 +482,7 @@ __device__ __forceinline__ void write_difference(const RowsParams& p, float* joi
 // and the warps' time bounds the pass.  Scores may rise above m by as much as binary32 and bf16 have room
 // for; a row whose sum passes kMostSum (or whose first unit gave it no reference) marks its piece, which the
 // copy warp hands out once more, with care: then every unit raises m to its maximum, and O is rescaled.
-constexpr float kMostSum = 18446744073709551616.f;  // 2^64
+constexpr float kMostSum = 1099511627776.f;  // 2^40: 28 above m, and values may be as large as 2^80
 
 template <int D, bool PAGED, bool FINE>
 __device__ __forceinline__ void softmax_maps(const RowsParams& p, const Work* work, volatile int* redo,

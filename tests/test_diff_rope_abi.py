@@ -67,7 +67,8 @@ ROPE_BAD = [
     (dict(qs=1016), BAD), (dict(qs=1028), BAD), (dict(ks=128), BAD), (dict(qos=8), BAD), (dict(q=None), BAD),
     (dict(k=None), BAD), (dict(qo=None), BAD), (dict(q=P(0x10008)), BAD), (dict(qo=P(0x10002)), BAD),
     (dict(qo=P(Q.value + 16)), BAD), (dict(qo=P(Q.value + 2048)), BAD), (dict(qo=Q, qos=2048), BAD), (dict(qo=K), BAD),
-    (dict(qo=P(TABLE.value + 25584)), BAD),
+    (dict(qo=P(TABLE.value + 25584)), BAD), (dict(positions=P(QO.value + 4)), BAD),
+    (dict(positions=None, cu_seqlens=P(QO.value + 16), seq_lens=A, B=2), BAD),
 ]
 
 

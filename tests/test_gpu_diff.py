@@ -217,6 +217,10 @@ def test_scores_of_minus_infinity_weigh_nothing(fd):
         assert torch.isneginf(lse[..., 1]).all()
         err = (out.double() - ref[0]).abs()
         assert (err <= ref[2] + 2.0 ** -24 * ref[0].abs()).all()
+        out, z = fd.fd_prefill_packed_diff(q, k[0].transpose(0, 1).contiguous(), v[0].transpose(0, 1).contiguous(), lam,
+                                           ints([0, 1]), ints([0, 200]), num_splits=splits, out_dtype="f32")
+        assert torch.isneginf(z[..., 1]).all() and (z[..., 0] - lse[..., 0]).abs().max() <= 2 * ref[3].max()
+        assert ((out.double() - ref[0]).abs() <= ref[2] + 2.0 ** -24 * ref[0].abs()).all()
 
 
 def test_results_repeat_and_streams_do_not_disturb_each_other(fd):

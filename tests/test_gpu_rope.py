@@ -56,6 +56,10 @@ SHAPES = [  # T, Hq, Hkv, d, rot, halves
     (257, 7, 7, 128, 32, False),
     (19, 64, 8, 128, 16, True),
     (8, 10, 5, 64, 16, False),
+    # more rows than the GPU holds at once: several heads a thread
+    (3000, 7, 3, 128, 128, False),
+    (2501, 32, 8, 64, 32, True),
+    (1777, 10, 5, 128, 64, True),
 ]
 
 
@@ -180,6 +184,10 @@ def test_append(fd, T, Hq, Hkv, d, rot, halves, interleaved, norm):
     rest = torch.ones((P, 64), dtype=torch.bool, device="cuda")
     rest[page, row] = False
     assert (codes[2].transpose(1, 2)[rest] == 9).all() and (scales[2].transpose(1, 2)[rest] == 9).all()
+    # the queries in place, in the fused rows
+    kept = torch.cat([k, v], 1)
+    fd.fd_append_kv_paged_rope(q, k, v, slots, *got, table, q_out=q, **more)
+    assert torch.equal(q, qo) and torch.equal(torch.cat([k, v], 1), kept)
     assert fd.fd_device_status(clear=True) == fd.FD_OK
 
 
