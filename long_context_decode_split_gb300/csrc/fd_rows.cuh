@@ -406,9 +406,10 @@ __device__ __forceinline__ void mark_empty(float* part_ml, int token, int tokens
 
 // The end of a row whose two maps are complete: warpgroup i knows the factor of map i and writes half of the channels
 // of factor0 O0 + factor1 O1 (1 / l0 and -lambda / l1), normalised where there is a weight.  o_at: O of map 0 in
-// tensor memory, map 1 behind it.  A thread tells the other warpgroup its factor, then its sum of squares.  This code
-// runs once a piece, and fetching it takes longer than running it: one small loop for both passes over the
-// channels (32 at a time and a loop each, 32 prompts of 512: 2800 cycles a piece, 4900 with the norm).
+// tensor memory, map 1 behind it.  A thread tells the other warpgroup its factor, then its sum of squares.  One small
+// loop for both passes over the channels (this code runs once a piece, and has to be fetched for it); the norm's
+// weights are in shared memory (8 prompts of 257 to 4095 tokens 673 -> 665 us).  A piece pays about 5000 cycles from
+// its last unit to the next one's first, half of them for the stores of 32 bytes a row.
 template <int D>
 __device__ __forceinline__ void write_difference(const RowsParams& p, float* join, int r, int i, size_t row, bool live,
                                                  float factor, bool some, uint32_t o_at) {
@@ -478,10 +479,24 @@ __device__ __forceinline__ void write_difference(const RowsParams& p, float* joi
 }
 
 // The softmax of map i, a warpgroup each, one row a thread, in units of 64 keys.  A row's reference m is the maximum
-// of its first unit, and the others are weighed by it as they come: maxima are a fifth of a unit's instructions,
-// and the warps' time bounds the pass.  Scores may rise above m by as much as binary32 and bf16 have room
-// for; a row whose sum passes kMostSum (or whose first unit gave it no reference) marks its piece, which the
-// copy warp hands out once more, with care: then every unit raises m to its maximum, and O is rescaled.
+// of its first unit, and the others are weighed by it as they come.  Scores may rise above m by as much as
+// binary32 and bf16 have room for; a row whose sum passes kMostSum (or whose first unit gave it no reference)
+// marks its piece, which the copy warp hands out once more, with care: then every unit raises m to its
+// maximum, and O is rescaled.
+//
+// What bounds it, and what each choice brought (32 query and 8 KV heads of 128, 16K tokens: 2.13-2.18 ms, 1.51-1.55
+// PFLOP/s of the 768 operations a pair; the tensor cores are busy 69% of the time, the exponentials' pipe 43%,
+// and one instruction is issued in two cycles): the time of two softmax warps a scheduler, whose steps wait for
+// one another.  A unit takes them about 1100 cycles, its products 384 a map.
+//   * blocks of 128 keys, as for the other modes: 2400 us.  A map's products and its softmax then follow each other
+//   * units of 64 in two rooms for scores, P over S, maxima throughout: 2410 us (seven waits and arrivals a unit
+//     and map took what the overlap brought)
+//   * one room for scores and the queries in tensor memory beside it (S | P | Q: the scores' products take 32
+//     cycles instead of 48, and half of the shared memory's traffic), one wait and one arrival a unit: 2470
+//   * no maxima behind the first unit: 2165; the test of each unit's sum in their place cost more than them (2600)
+//   * four warpgroups instead of two, each half of a unit's weights (2980) or every second unit (2650): registers
+//     spilled, and the chain from turn to turn stayed
+//   * weights in batches of four pairs: 2185 -> 2130
 constexpr float kMostSum = 1099511627776.f;  // 2^40: 28 above m, and values may be as large as 2^80
 
 template <int D, bool PAGED, bool FINE>
@@ -606,13 +621,21 @@ __device__ __forceinline__ void softmax_maps(const RowsParams& p, const Work* wo
             const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nb2 = make_float2(-base, -base);
             uint32_t w[32], lo[32];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-                const int c = e / 16, x = 2 * (e % 16);
-                float2 f = f2fma(make_float2(__uint_as_float(s[c][x]), __uint_as_float(s[c][x + 1])), sc2, nb2);
-                f = make_float2(exp2_approx(f.x), exp2_approx(f.y));
-                l2 = __fadd2_rn(l2, f);
-                if (FINE) split_bf16(f.x, f.y, w[e], lo[e]);
-                else w[e] = pack_bf16(f.x, f.y);
+            for (int g = 0; g < 32; g += 4) {
+                float2 f[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int c = (g + e) / 16, x = 2 * ((g + e) % 16);
+                    f[e] = f2fma(make_float2(__uint_as_float(s[c][x]), __uint_as_float(s[c][x + 1])), sc2, nb2);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) f[e] = make_float2(exp2_approx(f[e].x), exp2_approx(f[e].y));
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (FINE) split_bf16(f[e].x, f[e].y, w[g + e], lo[g + e]);
+                    else w[g + e] = pack_bf16(f[e].x, f[e].y);
+                }
+                l2 = __fadd2_rn(l2, __fadd2_rn(__fadd2_rn(f[0], f[1]), __fadd2_rn(f[2], f[3])));
             }
             ok = warp_wait(&s_full[i], n & 1u, p.wait_limit_ns);
             if (!ok) break;
