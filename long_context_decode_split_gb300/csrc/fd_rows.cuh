@@ -455,7 +455,7 @@ __device__ __forceinline__ void write_difference(const RowsParams& p, float* joi
             continue;
         }
         if (!live) continue;
-        if (weight) {
+        if (weight && (f0 != 0.f || f1 != 0.f)) {  // (a row that saw nothing is 0 whatever the weights)
 #pragma unroll
             for (int e = 0; e < STEP; e += 4) {
                 const float4 w = *reinterpret_cast<const float4*>(join + 256 + c + e);  // (the kernel's copy)

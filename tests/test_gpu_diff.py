@@ -142,6 +142,26 @@ def test_prompts_without_the_causal_mask_and_rows_that_see_nothing(fd):
     check_diff(out[20:], lse[20:], diff64(q[20:], k, v, lam, limits(50, 50), 1 / math.sqrt(32), w))
 
 
+@pytest.mark.parametrize("splits", [1, 3])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_that_see_nothing_are_0_whatever_lambda_and_weights(fd, dtype, splits):
+    Hq, Hkv, d, new, keys = 4, 2, 64, 40, 7
+    g = generator(31)
+    q, k, v = randn(g, new, Hq, d), randn(g, keys, Hkv, d), randn(g, keys, Hkv, d)
+    bad = torch.full((new, Hq), float("nan"), device="cuda")
+    w = torch.full((d,), float("inf"), device="cuda")
+    out, lse = fd.fd_prefill_packed_diff(q, k, v, bad, ints([0, new]), ints([0, keys]), norm_weight=w, out_dtype=dtype,
+                                         num_splits=splits)
+    empty = new - keys
+    assert (out[:empty] == 0).all() and (lse[:empty] == float("-inf")).all()
+    assert out[empty:].isnan().all() and lse[empty:].isfinite().all()
+    kc, vc = (x.transpose(0, 1)[None].repeat(2, 1, 1, 1).contiguous() for x in (k, v))
+    out, lse = fd.fd_decode_dense_diff(q[:2], kc, vc, bad[:2], ints([0, keys]), norm_weight=w, out_dtype=dtype,
+                                       num_splits=splits)
+    assert (out[0] == 0).all() and (lse[0] == float("-inf")).all()
+    assert out[1].isnan().all() and lse[1].isfinite().all()
+
+
 def test_prompts_from_a_fused_projection_leave_other_rows_alone(fd):
     g = generator(8)
     Hq, Hkv, d, T = 6, 2, 128, 90
