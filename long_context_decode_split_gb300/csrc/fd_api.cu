@@ -406,16 +406,21 @@ int check_rows(int B, int total_q, int Hq, int Hkv, int max_k, int d, int num_sp
 // tokens behind 8192 cached ones 95 us in one, 64 us in two, 82 us in three; 2 x 64
 // behind 32K 339 us in one, 65 us in nine, 78 us in sixteen; 16 x 8 behind 16K to 64K
 // (64 query heads) 458 us in one, 344 us in three, 332 us in seven, 346 us in sixteen.
-// per: query tokens of a piece of work.
-RowsPlan pieces_plan(int B, int total_q, int Hq, int Hkv, int max_k, int num_splits, int per) {
+// per: query tokens of a piece of work.  maps: a differential call, whose records are twice as long and
+// whose results leave the kernel without them otherwise (49K rows of short prompts 19 us in one part, 85 in
+// two, 95 in three), so that a row costs something in itself; its pieces are single tiles, so that parts pay up
+// to three rounds of the SMs: 40 x 8 tokens behind 1K to 32K 473 us in one part, 437 in four; 48 x 8 588 and 544
+// (three); 40 x 16 behind 16K 487 and 462 (two); but 20 x 64 behind 1K to 16K 214 us in one, 246 in two.
+RowsPlan pieces_plan(int B, int total_q, int Hq, int Hkv, int max_k, int num_splits, int per, bool maps) {
     RowsPlan pl;
     pl.splits = num_splits > 0 ? num_splits : 1;
     pl.chunk = num_splits > 0 ? 128 : 512;
     const int sms = num_splits > 0 ? 0 : current_sm_count();
     const long long mean = B > 0 ? (total_q + B - 1) / B : 0;  // tokens of a sequence
     const long long ctas = (long long)B * ((mean + per - 1) / per) * Hkv;
-    if (sms <= 0 || ctas <= 0 || ctas >= 2LL * sms) return pl;
-    const double kPiece = 6.0, kMerge = 4.0, kRecords = 1.6e-4;  // in blocks of time
+    if (sms <= 0 || ctas <= 0 || ctas >= (maps ? 3LL : 2LL) * sms) return pl;
+    const double kPiece = 6.0, kMerge = 4.0;  // in blocks of time
+    const double kRow = maps ? 7e-4 : 0.0, kRecords = maps ? 2.5e-4 : 1.6e-4;
     const double blocks = std::min(max_k, 1 << 15) / 128.0;
     const long long most = std::min((long long)max_k / pl.chunk, 8LL * sms / ctas + 1);
     double best = 1e300;
@@ -426,7 +431,7 @@ RowsPlan pieces_plan(int B, int total_q, int Hq, int Hkv, int max_k, int num_spl
             const double mean_piece = 0.625 * c + kPiece, longest = c + kPiece;
             cost = 0.5 * (cost + std::max(pieces * mean_piece / sms + 0.5 * longest, longest));
         }
-        if (S > 1) cost += kMerge + kRecords * (double)S * (double)total_q * Hq;
+        if (S > 1) cost += kMerge + (kRow + kRecords * (double)S) * (double)total_q * Hq;
         if (cost < best) {
             best = cost;
             pl.splits = (int)S;
@@ -436,7 +441,7 @@ RowsPlan pieces_plan(int B, int total_q, int Hq, int Hkv, int max_k, int num_spl
 }
 
 RowsPlan prefill_plan(int B, int total_q, int Hq, int Hkv, int max_k, int num_splits) {
-    return pieces_plan(B, total_q, Hq, Hkv, max_k, num_splits, fd::rows_tokens(B, total_q, Hq / Hkv, -1));
+    return pieces_plan(B, total_q, Hq, Hkv, max_k, num_splits, fd::rows_tokens(B, total_q, Hq / Hkv, -1), false);
 }
 
 // The plan of a packed call, whose sequences share total_k: no more parts than a
@@ -473,7 +478,7 @@ int check_prefill(const fd::RowsArgs& a, int num_splits, int out_dtype) {
 
 // A differential call: a piece of work has one tile, and either map its own records.
 RowsPlan prefill_diff_plan(int B, int total_q, int Hq, int Hkv, int max_k, int num_splits, bool packed) {
-    RowsPlan pl = pieces_plan(B, total_q, Hq, Hkv, max_k, num_splits, fd::rows_diff_tokens(Hq / Hkv));
+    RowsPlan pl = pieces_plan(B, total_q, Hq, Hkv, max_k, num_splits, fd::rows_diff_tokens(Hq / Hkv), true);
     if (packed && pl.splits > 1 && num_splits == 0)  // (as packed_plan)
         pl.splits = std::min(pl.splits, std::max(1, (int)(1.6 * max_k / B) / pl.chunk));
     return pl;
