@@ -128,6 +128,24 @@ def test_prompts(fd, Hq, Hkv, d, new, ctx, norm, dtype, splits):
     assert fd.fd_device_status(clear=True) == DEVICE_OK
 
 
+@pytest.mark.parametrize("lens", [[9] * 40, [(37 * b) % 2500 for b in range(40)]])
+def test_drafts_of_many_sequences_in_parts_of_their_own_choice(fd, lens):
+    Hq, Hkv, d, B = 16, 8, 64, len(lens)
+    g = generator(32)
+    kp, vp, table, P, have = paged(g, lens, Hkv, d, wide=400)  # room for many more keys than there are
+    new = [min(4, n) for n in lens]
+    T = sum(new)
+    assert fd.fd_prefill_diff_num_splits(B, T, Hq, Hkv, table.shape[1] * 64, d) > 1
+    q, lam, w = randn(g, T, Hq, d), lam_of(g, T, Hq, True), weight_of(g, d, True)
+    cu = ints([sum(new[:b]) for b in range(B + 1)])
+    out, lse = fd.fd_prefill_paged_diff(q, kp, vp, lam, table, P, cu, ints(lens), norm_weight=w)
+    for b, n in enumerate(new):
+        a = sum(new[:b])
+        ref = diff64(q[a:a + n], *have[b], lam[a:a + n], limits(n, lens[b]), 1 / math.sqrt(32), w, rounding=2.0 ** -8)
+        check_diff(out[a:a + n], lse[a:a + n], ref, str(b))
+    assert fd.fd_device_status(clear=True) == DEVICE_OK
+
+
 def test_prompts_without_the_causal_mask_and_rows_that_see_nothing(fd):
     g = generator(7)
     q, k, v, lam = randn(g, 70, 4, 64), randn(g, 50, 2, 64), randn(g, 50, 2, 64), rand(g, 0.1, 0.6, 4)
