@@ -589,6 +589,9 @@ FD_API int fd_append_kv_paged_rope_fp8(const void* q, const void* k, const void*
  *   norm_weight   [d] float32, 16-byte aligned, or NULL; norm_eps > 0 with it
  *   out           as the calls without _diff
  *   lse           [tokens, Hq, 2] float32 or NULL: of either map
+ * out, lse and the workspace share no memory with each other or another argument
+ * (FD_ERR_INVALID_ARG), but for out = q in the decode calls with FD_OUT_BF16; the
+ * prompt calls may read a query after they have written to out.
  * A query that sees no key gets out = 0 and lse = -inf.  A visible score that is NaN
  * or +inf makes its row NaN; one of -inf weighs nothing.  Values of a query's
  * sequence have to be finite and, in the prompt calls, below 2^80 in magnitude.

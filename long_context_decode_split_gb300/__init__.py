@@ -821,7 +821,7 @@ def fd_decode_dense_diff(q, k, v, lam, seq_lens=None, scale=None, norm_weight=No
     second ones, then the norm where there is a norm_weight.  q [B,Hq,d], k, v
     [B,Hkv,L_max,d] bf16, lam [Hq] or [B,Hq] float32, seq_lens [B] int32 or None,
     norm_weight [d] float32 or None; scale None = 1/sqrt(d/2).  Returns (out
-    [B,Hq,d], lse [B,Hq,2] or None)."""
+    [B,Hq,d], lse [B,Hq,2] or None); a bf16 out may be q (in place)."""
     return _binding().dense_diff(q, k, v, lam, seq_lens, scale, norm_weight, norm_eps, num_splits, out, lse,
                                  _code(out_dtype), want_lse, workspace, stream)
 
@@ -851,7 +851,7 @@ def fd_prefill_packed_diff(q, k, v, lam, cu_seqlens_q, cu_seqlens_k=None, scale=
                            workspace=None, stream=None):
     """Differential attention (fd_decode_dense_diff) of whole prompts, packed as
     for fd_prefill_packed.  lam [Hq] or [Tq,Hq] float32.  Returns (out [Tq,Hq,d],
-    lse [Tq,Hq,2] or None)."""
+    lse [Tq,Hq,2] or None); results that would overlap an argument are refused."""
     return _binding().prefill_packed_diff(q, k, v, lam, cu_seqlens_q, cu_seqlens_k, scale, norm_weight, norm_eps, causal,
                                           num_splits, out, lse, _code(out_dtype), want_lse, workspace, stream)
 

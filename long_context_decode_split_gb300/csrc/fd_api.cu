@@ -5,6 +5,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <initializer_list>
 
 #include <cuda_runtime.h>
 
@@ -461,6 +462,35 @@ bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 // A token stride covers the token's heads and keeps 16-byte rows.
 bool stride_ok(long long s, int H, int d) { return s >= (long long)H * d && s % 8 == 0 && s <= (1LL << 32); }
 
+// T rows of `bytes` bytes, `step` bytes apart.
+struct Strided {
+    const void* at;
+    long long T, bytes, step;
+};
+bool overlap(const Strided& a, const Strided& b) {
+    if (!a.at || !b.at || a.T <= 0 || b.T <= 0 || a.bytes <= 0 || b.bytes <= 0) return false;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+    if (x >= y + (uintptr_t)((b.T - 1) * b.step + b.bytes) || y >= x + (uintptr_t)((a.T - 1) * a.step + a.bytes))
+        return false;
+    if (a.step != b.step) return true;
+    // slices of the same rows (a fused projection): apart where their columns are
+    const long long d = (long long)(y - x) % a.step, shift = d < 0 ? d + a.step : d;
+    return !(a.bytes <= shift && shift + b.bytes <= a.step);
+}
+
+Strided whole(const void* at, long long bytes) { return {at, 1, bytes, bytes}; }
+
+// Whether a buffer that a call writes shares memory with another one, or with one that it reads.
+bool clash(std::initializer_list<Strided> written, std::initializer_list<Strided> read) {
+    for (const Strided* w = written.begin(); w != written.end(); ++w) {
+        for (const Strided* o = w + 1; o != written.end(); ++o)
+            if (overlap(*w, *o)) return true;
+        for (const Strided& r : read)
+            if (overlap(*w, r)) return true;
+    }
+    return false;
+}
+
 int check_prefill(const fd::RowsArgs& a, int num_splits, int out_dtype) {
     const int st = check_rows(a.B, a.total_q, a.Hq, a.Hkv, a.max_k, a.D, num_splits);
     if (st != FD_OK) return st;
@@ -499,6 +529,27 @@ int check_mix(const fd::DiffMix& m, int Hq, bool some) {
     return FD_OK;
 }
 
+long long lambda_bytes(const fd::DiffMix& m, int tokens, int Hq) {
+    return 4 * ((tokens - 1) * m.lambda_stride + Hq);
+}
+// Bytes of a row of query heads in out_dtype.
+long long out_row_bytes(int Hq, int D, int out_dtype) { return (long long)Hq * D * (out_dtype == FD_OUT_BF16 ? 2 : 4); }
+
+bool diff_rows_clash(const fd::RowsArgs& a, const fd::DiffMix& m, int out_dtype, const void* workspace, size_t need) {
+    const auto tokens = [&](const void* at, long long T, long long stride, int H) {
+        return whole(at, T > 0 ? 2 * ((T - 1) * stride + (long long)H * a.D) : 0);
+    };
+    const long long pool = (long long)a.num_pages * a.Hkv * kTile * a.D * 2;
+    const bool paged = a.page_table != nullptr;
+    return clash({whole(a.out, a.total_q * out_row_bytes(a.Hq, a.D, out_dtype)), whole(a.lse, 8LL * a.total_q * a.Hq),
+                  whole(workspace, (long long)need)},
+                 {tokens(a.q, a.total_q, a.q_stride, a.Hq), paged ? whole(a.k, pool) : tokens(a.k, a.total_k, a.k_stride, a.Hkv),
+                  paged ? whole(a.v, pool) : tokens(a.v, a.total_k, a.v_stride, a.Hkv), whole(a.cu_q, 4LL * a.B + 4),
+                  whole(a.cu_k, 4LL * a.B + 4), whole(a.seq_lens, 4LL * a.B),
+                  whole(a.page_table, 4LL * a.B * a.table_stride), whole(m.lambda, lambda_bytes(m, a.total_q, a.Hq)),
+                  whole(m.weight, 4LL * a.D)});
+}
+
 // mix: the two maps of differential attention, or null.
 int prefill_entry(fd::RowsArgs& a, const fd::DiffMix* mix, int num_splits, int out_dtype, void* workspace,
                   size_t workspace_bytes, void* stream) {
@@ -517,6 +568,8 @@ int prefill_entry(fd::RowsArgs& a, const fd::DiffMix* mix, int num_splits, int o
         if ((long long)a.total_q * a.Hq > 0x7fffffffLL) return FD_ERR_UNSUPPORTED;  // the merge's grid
     }
     if (a.B == 0 || a.total_q == 0) return FD_OK;
+    // (a piece of work whose scores rise far reads its queries again while its first results are written)
+    if (mix && diff_rows_clash(a, *mix, out_dtype, workspace, need)) return FD_ERR_INVALID_ARG;
     a.splits = pl.splits;
     a.chunk = pl.chunk;
     a.out_bf16 = out_dtype == FD_OUT_BF16;
@@ -930,6 +983,16 @@ int diff_decode_entry(fd::DecodeArgs& a, const fd::DiffMix& mix, int num_splits,
         if (!aligned16(workspace)) return FD_ERR_INVALID_ARG;
         if ((long long)a.B * a.Hq > 0x7fffffffLL) return FD_ERR_UNSUPPORTED;  // the merge's grid
     }
+    // (in place over the queries is fine: a group's rows are read before they are written, by the same CTA or in
+    // the merge)
+    const bool in_place = a.out == a.q && out_dtype == FD_OUT_BF16;
+    if (a.B > 0 && clash({whole(a.out, a.B * out_row_bytes(a.Hq, a.D, out_dtype)), whole(a.lse, 8LL * a.B * a.Hq),
+                          whole(workspace, (long long)need)},
+                         {whole(in_place ? nullptr : a.q, 2LL * a.B * a.Hq * a.D), whole(a.k, 2 * cache_rows * a.D),
+                          whole(a.v, 2 * cache_rows * a.D), whole(a.seq_lens, 4LL * a.B),
+                          whole(a.page_table, 4LL * a.B * a.max_pages), whole(mix.lambda, lambda_bytes(mix, a.B, a.Hq)),
+                          whole(mix.weight, 4LL * a.D)}))
+        return FD_ERR_INVALID_ARG;
     a.splits = pl.splits;
     a.chunk_fixed = pl.chunk_fixed;
     a.out_bf16 = out_dtype == FD_OUT_BF16;
@@ -1089,22 +1152,6 @@ int fd_append_kv_paged_fp8(const void* k, const void* v, long long k_stride, lon
 
 namespace {
 
-// T rows of `bytes` bytes, `step` bytes apart.
-struct Strided {
-    const void* at;
-    long long T, bytes, step;
-};
-bool overlap(const Strided& a, const Strided& b) {
-    if (!a.at || !b.at || a.T <= 0 || b.T <= 0 || a.bytes <= 0 || b.bytes <= 0) return false;
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
-    if (x >= y + (uintptr_t)((b.T - 1) * b.step + b.bytes) || y >= x + (uintptr_t)((a.T - 1) * a.step + a.bytes))
-        return false;
-    if (a.step != b.step) return true;
-    // slices of the same rows (a fused projection): apart where their columns are
-    const long long d = (long long)(y - x) % a.step, shift = d < 0 ? d + a.step : d;
-    return !(a.bytes <= shift && shift + b.bytes <= a.step);
-}
-
 // The arguments that norms and rotation share.  a: the tensors; paged: keys and values go to the cache.
 int rope_entry(fd::RopeArgs& a, const fd_rope* r, bool paged, bool fp8, int page_size, void* stream) {
     if (paged && page_size != kTile) return page_size > 0 ? FD_ERR_UNSUPPORTED : FD_ERR_INVALID_ARG;
@@ -1145,7 +1192,6 @@ int rope_entry(fd::RopeArgs& a, const fd_rope* r, bool paged, bool fp8, int page
     if (q && ((overlap(qo, qi) && !same(qo, qi)) || overlap(qo, ki) || overlap(qo, vi) || overlap(qo, ko)))
         return FD_ERR_INVALID_ARG;
     if (k && !paged && ((overlap(ko, ki) && !same(ko, ki)) || overlap(ko, qi))) return FD_ERR_INVALID_ARG;
-    const auto whole = [](const void* at, long long bytes) { return Strided{at, 1, bytes, bytes}; };
     const long long pool = (long long)a.num_pages * a.Hkv * kTile * a.D * (fp8 ? 1 : 2);
     const Strided others[] = {whole(a.k_pages, pool), whole(a.v_pages, pool),
                               whole(r->cos_sin, 4LL * r->max_pos * r->rot), whole(r->q_weight, 4LL * dh),
