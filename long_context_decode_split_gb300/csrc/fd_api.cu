@@ -5,7 +5,6 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
-#include <initializer_list>
 
 #include <cuda_runtime.h>
 
@@ -480,15 +479,25 @@ bool overlap(const Strided& a, const Strided& b) {
 
 Strided whole(const void* at, long long bytes) { return {at, 1, bytes, bytes}; }
 
+// The bytes [lo, hi) of a buffer.
+struct Span {
+    uintptr_t lo, hi;
+};
+Span span(const void* at, long long bytes) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(at);
+    return {x, at && bytes > 0 ? x + (uintptr_t)bytes : x};
+}
+bool meet(const Span& a, const Span& b) { return std::max(a.lo, b.lo) < std::min(a.hi, b.hi); }
+
 // Whether a buffer that a call writes shares memory with another one, or with one that it reads.
-bool clash(std::initializer_list<Strided> written, std::initializer_list<Strided> read) {
-    for (const Strided* w = written.begin(); w != written.end(); ++w) {
-        for (const Strided* o = w + 1; o != written.end(); ++o)
-            if (overlap(*w, *o)) return true;
-        for (const Strided& r : read)
-            if (overlap(*w, r)) return true;
+template <size_t W, size_t R>
+bool clash(const Span (&written)[W], const Span (&read)[R]) {
+    bool any = false;
+    for (size_t w = 0; w < W; ++w) {
+        for (size_t o = w + 1; o < W; ++o) any |= meet(written[w], written[o]);
+        for (size_t r = 0; r < R; ++r) any |= meet(written[w], read[r]);
     }
-    return false;
+    return any;
 }
 
 int check_prefill(const fd::RowsArgs& a, int num_splits, int out_dtype) {
@@ -537,17 +546,18 @@ long long out_row_bytes(int Hq, int D, int out_dtype) { return (long long)Hq * D
 
 bool diff_rows_clash(const fd::RowsArgs& a, const fd::DiffMix& m, int out_dtype, const void* workspace, size_t need) {
     const auto tokens = [&](const void* at, long long T, long long stride, int H) {
-        return whole(at, T > 0 ? 2 * ((T - 1) * stride + (long long)H * a.D) : 0);
+        return span(at, T > 0 ? 2 * ((T - 1) * stride + (long long)H * a.D) : 0);
     };
     const long long pool = (long long)a.num_pages * a.Hkv * kTile * a.D * 2;
     const bool paged = a.page_table != nullptr;
-    return clash({whole(a.out, a.total_q * out_row_bytes(a.Hq, a.D, out_dtype)), whole(a.lse, 8LL * a.total_q * a.Hq),
-                  whole(workspace, (long long)need)},
-                 {tokens(a.q, a.total_q, a.q_stride, a.Hq), paged ? whole(a.k, pool) : tokens(a.k, a.total_k, a.k_stride, a.Hkv),
-                  paged ? whole(a.v, pool) : tokens(a.v, a.total_k, a.v_stride, a.Hkv), whole(a.cu_q, 4LL * a.B + 4),
-                  whole(a.cu_k, 4LL * a.B + 4), whole(a.seq_lens, 4LL * a.B),
-                  whole(a.page_table, 4LL * a.B * a.table_stride), whole(m.lambda, lambda_bytes(m, a.total_q, a.Hq)),
-                  whole(m.weight, 4LL * a.D)});
+    const Span written[] = {span(a.out, a.total_q * out_row_bytes(a.Hq, a.D, out_dtype)), span(a.lse, 8LL * a.total_q * a.Hq),
+                            span(workspace, (long long)need)};
+    const Span read[] = {tokens(a.q, a.total_q, a.q_stride, a.Hq), paged ? span(a.k, pool) : tokens(a.k, a.total_k, a.k_stride, a.Hkv),
+                  paged ? span(a.v, pool) : tokens(a.v, a.total_k, a.v_stride, a.Hkv), span(a.cu_q, 4LL * a.B + 4),
+                  span(a.cu_k, 4LL * a.B + 4), span(a.seq_lens, 4LL * a.B),
+                  span(a.page_table, 4LL * a.B * a.table_stride), span(m.lambda, lambda_bytes(m, a.total_q, a.Hq)),
+                  span(m.weight, 4LL * a.D)};
+    return clash(written, read);
 }
 
 // mix: the two maps of differential attention, or null.
@@ -986,13 +996,14 @@ int diff_decode_entry(fd::DecodeArgs& a, const fd::DiffMix& mix, int num_splits,
     // (in place over the queries is fine: a group's rows are read before they are written, by the same CTA or in
     // the merge)
     const bool in_place = a.out == a.q && out_dtype == FD_OUT_BF16;
-    if (a.B > 0 && clash({whole(a.out, a.B * out_row_bytes(a.Hq, a.D, out_dtype)), whole(a.lse, 8LL * a.B * a.Hq),
-                          whole(workspace, (long long)need)},
-                         {whole(in_place ? nullptr : a.q, 2LL * a.B * a.Hq * a.D), whole(a.k, 2 * cache_rows * a.D),
-                          whole(a.v, 2 * cache_rows * a.D), whole(a.seq_lens, 4LL * a.B),
-                          whole(a.page_table, 4LL * a.B * a.max_pages), whole(mix.lambda, lambda_bytes(mix, a.B, a.Hq)),
-                          whole(mix.weight, 4LL * a.D)}))
-        return FD_ERR_INVALID_ARG;
+    const Span written[] = {span(a.out, a.B * out_row_bytes(a.Hq, a.D, out_dtype)), span(a.lse, 8LL * a.B * a.Hq),
+                            span(workspace, (long long)need)};
+    const Span read[] = {span(in_place ? nullptr : a.q, 2LL * a.B * a.Hq * a.D), span(a.k, 2 * cache_rows * a.D),
+                         span(a.v, 2 * cache_rows * a.D), span(a.seq_lens, 4LL * a.B),
+                         span(a.page_table, 4LL * a.B * a.max_pages),
+                         span(mix.lambda, a.B > 0 ? lambda_bytes(mix, a.B, a.Hq) : 0),
+                         span(mix.weight, a.B > 0 ? 4LL * a.D : 0)};
+    if (clash(written, read)) return FD_ERR_INVALID_ARG;
     a.splits = pl.splits;
     a.chunk_fixed = pl.chunk_fixed;
     a.out_bf16 = out_dtype == FD_OUT_BF16;
