@@ -557,7 +557,8 @@ FD_API int fd_norm_rope(const void* q, const void* k, long long q_stride, long l
  * slots, values as they are to theirs, in one launch.  slots, pools and
  * page_size as fd_append_kv_paged; a token left out, or with a negative slot,
  * leaves its cache rows as they were (with a negative slot its query is turned all the
- * same).  Hq = 0: keys and values alone. */
+ * same).  Hq = 0: keys and values alone.  The pools (and scales) overlap neither
+ * each other nor another argument (FD_ERR_INVALID_ARG). */
 FD_API int fd_append_kv_paged_rope(const void* q, const void* k, const void* v,
                                    long long q_stride, long long k_stride, long long v_stride,
                                    const int64_t* slots, int T, int Hq, int Hkv, int d, const fd_rope* rope,

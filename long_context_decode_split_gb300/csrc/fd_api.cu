@@ -477,8 +477,6 @@ bool overlap(const Strided& a, const Strided& b) {
     return !(a.bytes <= shift && shift + b.bytes <= a.step);
 }
 
-Strided whole(const void* at, long long bytes) { return {at, 1, bytes, bytes}; }
-
 // The bytes [lo, hi) of a buffer.
 struct Span {
     uintptr_t lo, hi;
@@ -1191,7 +1189,8 @@ int rope_entry(fd::RopeArgs& a, const fd_rope* r, bool paged, bool fp8, int page
         !aligned16(r->k_weight) || !aligned4(r->positions) || !aligned4(r->cu_seqlens) || !aligned4(r->seq_lens) ||
         !aligned4(a.k_scales) || !aligned4(a.v_scales) || (reinterpret_cast<uintptr_t>(a.slots) & 7u))
         return FD_ERR_INVALID_ARG;
-    // outputs share no memory with anything but, in place, the very rows that they replace
+    // rows, pools and scales that are written share no memory with anything but, in place, the very rows that they
+    // replace
     const auto rows = [&](const void* at, int H, long long stride) {
         return Strided{at, a.T, 2LL * H * a.D, 2 * stride};
     };
@@ -1203,15 +1202,18 @@ int rope_entry(fd::RopeArgs& a, const fd_rope* r, bool paged, bool fp8, int page
     if (q && ((overlap(qo, qi) && !same(qo, qi)) || overlap(qo, ki) || overlap(qo, vi) || overlap(qo, ko)))
         return FD_ERR_INVALID_ARG;
     if (k && !paged && ((overlap(ko, ki) && !same(ko, ki)) || overlap(ko, qi))) return FD_ERR_INVALID_ARG;
-    const long long pool = (long long)a.num_pages * a.Hkv * kTile * a.D * (fp8 ? 1 : 2);
-    const Strided others[] = {whole(a.k_pages, pool), whole(a.v_pages, pool),
-                              whole(r->cos_sin, 4LL * r->max_pos * r->rot), whole(r->q_weight, 4LL * dh),
-                              whole(r->k_weight, 4LL * dh), whole(r->positions, 4LL * a.T),
-                              whole(r->cu_seqlens, 4LL * r->B + 4), whole(r->seq_lens, 4LL * r->B),
-                              whole(a.slots, 8LL * a.T), whole(a.k_scales, 4LL * a.num_pages * a.Hkv * kTile),
-                              whole(a.v_scales, 4LL * a.num_pages * a.Hkv * kTile)};
-    for (const Strided& o : others)
-        if ((q && overlap(qo, o)) || (k && !paged && overlap(ko, o))) return FD_ERR_INVALID_ARG;
+    const auto extent = [](const Strided& x) { return span(x.at, x.T > 0 && x.bytes > 0 ? (x.T - 1) * x.step + x.bytes : 0); };
+    const long long slot_rows = some ? (long long)a.num_pages * a.Hkv * kTile : 0, pool = slot_rows * a.D * (fp8 ? 1 : 2);
+    const Span written[] = {span(a.k_pages, pool), span(a.v_pages, pool), span(a.k_scales, 4 * slot_rows),
+                            span(a.v_scales, 4 * slot_rows), extent(qo)};
+    const Span read[] = {span(r->cos_sin, 4LL * r->max_pos * r->rot), span(r->q_weight, 4LL * dh),
+                         span(r->k_weight, 4LL * dh), span(r->positions, 4LL * a.T), span(r->cu_seqlens, 4LL * r->B + 4),
+                         span(r->seq_lens, 4LL * r->B), span(a.slots, 8LL * a.T)};
+    const Span keys_out[] = {extent(ko)}, rows_in[] = {extent(qi), extent(ki), extent(vi)};
+    if (clash(written, read) || clash(keys_out, read)) return FD_ERR_INVALID_ARG;
+    for (int i = 0; i < 4; ++i)
+        for (const Span& in : rows_in)
+            if (meet(written[i], in)) return FD_ERR_INVALID_ARG;
     a.cos_sin = r->cos_sin;
     a.max_pos = r->max_pos;
     a.rot = r->rot;
