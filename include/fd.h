@@ -523,7 +523,7 @@ FD_API int fd_append_kv_paged_fp8(const void* k, const void* v, long long k_stri
  *   (y_a, y_b) <- (y_a cos_i - y_b sin_i, y_b cos_i + y_a sin_i)
  * for the pairs i = 0 .. rot/2 - 1 of its first `rot` channels: a = i, b = i +
  * rot/2, or with `interleaved` a = 2i, b = 2i + 1.  All of it in binary32, rounded
- * once at the end. */
+ * once at the end.  The norm holds for every finite x. */
 typedef struct fd_rope {
     const float* cos_sin;       /* [max_pos, rot]: row t holds the rot/2 cosines, then the sines; 16-byte aligned */
     int max_pos;
@@ -595,7 +595,9 @@ FD_API int fd_append_kv_paged_rope_fp8(const void* q, const void* k, const void*
  * prompt calls may read a query after they have written to out.
  * A query that sees no key gets out = 0 and lse = -inf.  A visible score that is NaN
  * or +inf makes its row NaN; one of -inf weighs nothing.  Values of a query's
- * sequence have to be finite and, in the prompt calls, below 2^80 in magnitude.
+ * sequence have to be below 2^96 in magnitude and, in the prompt calls, below 2^80
+ * (their sums over all keys stay in binary32, and the norm holds for all of them;
+ * in the prompt calls with a norm_eps below 2^-60 only up to 2^56).
  * (The prompt calls take a part of the keys twice where scores rise more than 28
  * above those of its first 64 keys, or are not finite.)
  * Scores, maxima, sums, the maps' outputs, their difference and its norm are

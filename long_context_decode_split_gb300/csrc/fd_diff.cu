@@ -49,12 +49,22 @@ __device__ __forceinline__ void store_difference(const float (&o1)[D / 32], cons
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = o1[e] - lambda * o2[e];
     if (mix.weight) {
-        float sum = 0.f;
+        const auto squares = [&] {
+            float sum = 0.f;
 #pragma unroll
-        for (int e = 0; e < E; ++e) sum = fmaf(o[e], o[e], sum);
+            for (int e = 0; e < E; ++e) sum = fmaf(o[e], o[e], sum);
 #pragma unroll
-        for (int s = 16; s >= 1; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
-        const float r = rsqrtf(sum * (1.f / D) + mix.eps);
+            for (int s = 16; s >= 1; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+            return sum;
+        };
+        float sum = squares(), eps = mix.eps;
+        if (sum == INFINITY) {  // (all lanes) from 2^60 on: o and sqrt(eps) by 2^-96 are in range, whatever o is
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] *= 0x1p-96f;
+            eps = eps * 0x1p-96f * 0x1p-96f;
+            sum = squares();
+        }
+        const float r = rsqrtf(sum * (1.f / D) + eps);
 #pragma unroll
         for (int e = 0; e < E; ++e) o[e] *= r * mix.weight[lane * E + e];
     }

@@ -76,16 +76,20 @@ __device__ __forceinline__ void encode_row(const uint32_t (&w)[8], uint8_t* code
 
 // The same for a row in binary32 (rotated and not yet rounded): one rounding,
 // from these values to the codes.  The lane's 16 channels lie in two runs of 8 at
-// `at0` and `at1` of the row.  (A NaN's code is NaN with either sign.)
-template <int C>
-__device__ __forceinline__ void encode_floats(const float (&x)[16], uint8_t* codes, float* scale, bool live, int c,
-                                              int at0, int at1) {
-    float amax = fabsf(x[0]);
+// `at0` and `at1` of the row.  (A NaN's code is NaN with either sign.)  Where a lane's x is
+// `worthless`, again(x, the row's lanes) makes them anew, in the branch that is there for rows
+// at the ends of the range.
+template <int C, typename Again>
+__device__ __forceinline__ void encode_floats(float (&x)[16], bool worthless, Again again, uint8_t* codes, float* scale,
+                                              bool live, int c, int at0, int at1) {
+    const auto largest = [&](float amax, unsigned lanes) {
 #pragma unroll
-    for (int e = 1; e < 16; ++e) amax = fmaxf(amax, fabsf(x[e]));
+        for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(x[e]));
 #pragma unroll
-    for (int o = C / 2; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    const float s = amax / 448.0f;
+        for (int o = C / 2; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(lanes, amax, o));
+        return amax;
+    };
+    float s = largest(worthless ? INFINITY : fabsf(x[0]), 0xffffffffu) / 448.0f;
     uint32_t out[4];
     if (s > 1e-30f && s < 1e30f) {
         const float r = 1.0f / s;
@@ -99,6 +103,11 @@ __device__ __forceinline__ void encode_floats(const float (&x)[16], uint8_t* cod
             out[e >> 1] = e & 1 ? (out[e >> 1] | pair << 16) ^ 0x80808080u : pair;
         }
     } else {
+        if (s == INFINITY) {
+            const unsigned lanes = ((1u << C) - 1u) << ((threadIdx.x & 31) / C * C);
+            again(x, lanes);
+            s = largest(fabsf(x[0]), lanes) / 448.0f;
+        }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const uint32_t pair = s != 0.f ? e4m3_pair(x[2 * e] / s, x[2 * e + 1] / s) : 0u;

@@ -8,6 +8,7 @@
 //   first `rot` channels, cos and sin from row t of a table
 // in binary32, rounded once: to bf16, or to the e4m3 codes.
 #include <cstdint>
+#include <type_traits>
 
 #include "fd_device.cuh"
 #include "fd_encode.cuh"
@@ -114,22 +115,37 @@ __device__ __forceinline__ void load_weights(Weights& w, const float* from, cons
     load8(w.w + 4, from + l.at1);
 }
 
-// Norm (NORM) and rotation of the head whose channels the DH / 16 lanes hold as bf16.
-template <int DH, bool NORM>
-__device__ __forceinline__ void turn(float (&x)[16], const uint4& a, const uint4& b, const RopeArgs& p, const Lane& l,
-                                     const Angles& g, const Weights& w) {
+// Norm (NORM) and rotation of the head whose channels the DH / 16 lanes hold as bf16 (all lanes together).  Whether
+// the head's squares leave binary32, as they do from 2^60 on: x is then worthless.  LARGE: such a head, and sqrt(eps) with
+// it, by 2^-96 before its norm, in range whatever it is.
+template <int DH, bool NORM, bool LARGE>
+__device__ __forceinline__ bool turn(float (&x)[16], const uint4& a, const uint4& b, const RopeArgs& p, const Lane& l,
+                                     const Angles& g, const Weights& w, unsigned lanes = 0xffffffffu) {
     const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     float2 y[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) y[e] = bf16x2_to_float2(u[e]);
+    bool large = false;
     if (NORM) {
-        float2 sum = make_float2(0.f, 0.f);
+        const auto squares = [&] {
+            float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum = f2fma(y[e], y[e], sum);
-        float all = sum.x + sum.y;
+            for (int e = 0; e < 8; ++e) sum = f2fma(y[e], y[e], sum);
+            float all = sum.x + sum.y;
 #pragma unroll
-        for (int o = DH / 32; o >= 1; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-        const float r = rsqrtf(all * (1.f / DH) + p.eps);
+            for (int o = DH / 32; o >= 1; o >>= 1) all += __shfl_xor_sync(lanes, all, o);
+            return all;
+        };
+        float all = squares(), eps = p.eps;
+        large = all == INFINITY;
+        if (LARGE) {
+            const float by = large ? 0x1p-96f : 1.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = f2mul(y[e], make_float2(by, by));
+            eps = eps * by * by;
+            all = squares();
+        }
+        const float r = rsqrtf(all * (1.f / DH) + eps);
         const float2 r2 = make_float2(r, r);
 #pragma unroll
         for (int e = 0; e < 8; ++e) y[e] = f2mul(f2mul(y[e], r2), w.w[e]);
@@ -153,24 +169,27 @@ __device__ __forceinline__ void turn(float (&x)[16], const uint4& a, const uint4
         x[2 * e] = y[e].x;
         x[2 * e + 1] = y[e].y;
     }
+    return large;
 }
 
 __device__ __forceinline__ uint4 pack8(const float* x) {
     return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
 }
 
-// Rows of one operand to rows: heads hg, hg + groups, .. of token t (all lanes together).
-template <int D, int DH, int RPT, bool NORM>
-__device__ __forceinline__ void rows_to_rows(const RopeArgs& p, const uint16_t* in, long long stride, uint16_t* out,
-                                             long long out_stride, const float* weight, int H, int groups,
-                                             unsigned block) {
+// Rows of one operand to rows: heads hg, hg + groups, .. of token t (all lanes together).  Returns which of the lane's
+// RPT rows are left, not yet written, for the LARGE form: one row, the one `from` heads on, where `wanted`.  (A branch to
+// it within the rows made the call 5% slower.)
+template <int D, int DH, int RPT, bool NORM, bool LARGE = false>
+__device__ __forceinline__ unsigned rows_to_rows(const RopeArgs& p, const uint16_t* in, long long stride, uint16_t* out,
+                                                 long long out_stride, const float* weight, int H, int groups,
+                                                 unsigned block, int from = 0, bool wanted = true) {
     constexpr int C = D / 16;  // lanes of a row
     const int c = threadIdx.x % C;
     const unsigned item = block * (kThreads / C) + threadIdx.x / C;
     const unsigned at_t = item / (unsigned)groups;
     const bool in_range = at_t < (unsigned)p.T;
     const int t = in_range ? (int)at_t : p.T - 1;
-    const int hg = (int)(item - at_t * groups);
+    const int hg = from + (int)(item - at_t * groups);
     const Lane l = lane_of<DH>(p, c % (DH / 16));
     const int part = c / (DH / 16) * DH;
     const uint16_t* row = in + (size_t)t * stride + hg * D + part;
@@ -190,29 +209,36 @@ __device__ __forceinline__ void rows_to_rows(const RopeArgs& p, const uint16_t* 
     const int at = row_of(p, t);
     Angles g = {};
     load_angles(g, p, l, at);
+    unsigned left = 0;
     uint16_t* to = out + (size_t)t * out_stride + hg * D + part;
 #pragma unroll
     for (int u = 0; u < RPT; ++u) {
         const int h = u * groups;
         float x[16];
-        turn<DH, NORM>(x, a[u], b[u], p, l, g, w);
-        if (!in_range || at < 0 || hg + h >= H) continue;
+        const bool large = turn<DH, NORM, LARGE>(x, a[u], b[u], p, l, g, w);
+        if (!wanted || !in_range || at < 0 || hg + h >= H) continue;
+        if (!LARGE && large) {
+            left |= 1u << u;
+            continue;
+        }
         *reinterpret_cast<uint4*>(to + h * D + l.at0) = pack8(x);
         *reinterpret_cast<uint4*>(to + h * D + l.at1) = pack8(x + 8);
     }
+    return left;
 }
 
 // Key rows of a token, turned, and its value rows to their slot of the pools: heads hg, hg + groups,
-// .. (all lanes together).
-template <int D, int DH, int RPT, bool FP8, bool NORM>
-__device__ __forceinline__ void rows_to_pages(const RopeArgs& p, int groups, unsigned block) {
+// .. (all lanes together).  Returns whether the LARGE form has to write over one of them (bf16; e4m3 rows are encoded
+// again where their maximum tells so: that form beside them made the call 5% slower).
+template <int D, int DH, int RPT, bool FP8, bool NORM, bool LARGE = false>
+__device__ __forceinline__ bool rows_to_pages(const RopeArgs& p, int groups, unsigned block, int from = 0) {
     constexpr int C = D / 16;
     const int c = threadIdx.x % C;
     const unsigned item = block * (kThreads / C) + threadIdx.x / C;
     const unsigned at_t = item / (unsigned)groups;
     const bool in_range = at_t < (unsigned)p.T;
     const int t = in_range ? (int)at_t : p.T - 1;
-    const int hg = (int)(item - at_t * groups);
+    const int hg = from + (int)(item - at_t * groups);
     const Lane l = lane_of<DH>(p, c % (DH / 16));
     const int part = c / (DH / 16) * DH;
     const long long slot = p.slots[t];
@@ -256,21 +282,31 @@ __device__ __forceinline__ void rows_to_pages(const RopeArgs& p, int groups, uns
             vp[1] = v1[u];
         }
     }
+    bool left = false;
 #pragma unroll
     for (int u = 0; u < RPT; ++u) {
         const bool wanted = live && hg + u * groups < p.Hkv;
         const size_t row = row0 + (size_t)u * groups * kTile;
         float x[16];
-        turn<DH, NORM>(x, a[u], b[u], p, l, g, w);
+        const bool large = turn<DH, NORM, LARGE>(x, a[u], b[u], p, l, g, w);
         if constexpr (FP8) {
-            encode_floats<C>(x, static_cast<uint8_t*>(p.k_pages) + row * D, p.k_scales + row, wanted, c, part + l.at0,
-                             part + l.at1);
-        } else if (wanted) {
+            const auto again = [&](float (&y)[16], unsigned lanes) {
+                const uint16_t* at_row = kr + u * groups * D;
+                turn<DH, NORM, true>(y, *reinterpret_cast<const uint4*>(at_row + l.at0),
+                                     *reinterpret_cast<const uint4*>(at_row + l.at1), p, l, g, w, lanes);
+            };
+            encode_floats<C>(x, large, again, static_cast<uint8_t*>(p.k_pages) + row * D, p.k_scales + row, wanted, c,
+                             part + l.at0, part + l.at1);
+            continue;
+        }
+        left |= large;
+        if (wanted) {
             uint16_t* kp = static_cast<uint16_t*>(p.k_pages) + row * D + part;
             *reinterpret_cast<uint4*>(kp + l.at0) = pack8(x);
             *reinterpret_cast<uint4*>(kp + l.at1) = pack8(x + 8);
         }
     }
+    return left;
 }
 
 enum { kToRows, kToPages, kToPagesFp8 };
@@ -281,25 +317,42 @@ template <int D, int DH, int TO, int RPT, int RPP>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSM) rope_kernel(const RopeArgs p, unsigned q_blocks, int q_groups, int k_groups) {
     pdl_wait_primary();
     pdl_launch_dependents();
+    // the rows of an operand, then those with squares that left binary32
+    const auto to_rows = [&](auto norm, const uint16_t* in, long long stride, uint16_t* out, long long out_stride,
+                             const float* weight, int H, int groups, unsigned block) {
+        constexpr bool NORM = decltype(norm)::value;
+        unsigned left = rows_to_rows<D, DH, RPT, NORM>(p, in, stride, out, out_stride, weight, H, groups, block);
+        if constexpr (NORM) {
+            if (__any_sync(0xffffffffu, left != 0u)) {
+#pragma unroll 1
+                for (int u = 0; u < RPT; ++u, left >>= 1)
+                    rows_to_rows<D, DH, 1, true, true>(p, in, stride, out, out_stride, weight, H, groups, block, u * groups,
+                                                       left & 1u);
+            }
+        }
+    };
+    const std::true_type with_norm;
+    const std::false_type without;
     if (blockIdx.x < q_blocks) {
-        if (p.q_weight)
-            rows_to_rows<D, DH, RPT, true>(p, p.q, p.q_stride, p.q_out, p.q_out_stride, p.q_weight, p.Hq, q_groups,
-                                           blockIdx.x);
-        else
-            rows_to_rows<D, DH, RPT, false>(p, p.q, p.q_stride, p.q_out, p.q_out_stride, nullptr, p.Hq, q_groups,
-                                            blockIdx.x);
+        if (p.q_weight) to_rows(with_norm, p.q, p.q_stride, p.q_out, p.q_out_stride, p.q_weight, p.Hq, q_groups, blockIdx.x);
+        else to_rows(without, p.q, p.q_stride, p.q_out, p.q_out_stride, nullptr, p.Hq, q_groups, blockIdx.x);
         return;
     }
     const unsigned block = blockIdx.x - q_blocks;
     if constexpr (TO == kToRows) {
-        if (p.k_weight)
-            rows_to_rows<D, DH, RPT, true>(p, p.k, p.k_stride, p.k_out, p.k_out_stride, p.k_weight, p.Hkv, k_groups,
-                                           block);
-        else
-            rows_to_rows<D, DH, RPT, false>(p, p.k, p.k_stride, p.k_out, p.k_out_stride, nullptr, p.Hkv, k_groups, block);
+        if (p.k_weight) to_rows(with_norm, p.k, p.k_stride, p.k_out, p.k_out_stride, p.k_weight, p.Hkv, k_groups, block);
+        else to_rows(without, p.k, p.k_stride, p.k_out, p.k_out_stride, nullptr, p.Hkv, k_groups, block);
     } else {
-        if (p.k_weight) rows_to_pages<D, DH, RPP, TO == kToPagesFp8, true>(p, k_groups, block);
-        else rows_to_pages<D, DH, RPP, TO == kToPagesFp8, false>(p, k_groups, block);
+        constexpr bool FP8 = TO == kToPagesFp8;
+        if (!p.k_weight) {
+            rows_to_pages<D, DH, RPP, FP8, false>(p, k_groups, block);
+            return;
+        }
+        const bool left = rows_to_pages<D, DH, RPP, FP8, true>(p, k_groups, block);
+        if (!FP8 && __any_sync(0xffffffffu, left)) {
+#pragma unroll 1
+            for (int u = 0; u < RPP; ++u) rows_to_pages<D, DH, 1, FP8, true, true>(p, k_groups, block, u * k_groups);
+        }
     }
 }
 

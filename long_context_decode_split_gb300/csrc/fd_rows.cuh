@@ -60,7 +60,8 @@ struct RowsParams {
     const int32_t* own_table;
     long long own_table_stride;
     int own_max, own_skip, own_splits, own_chunk, own_rec0;
-    DiffMix mix;  // differential attention
+    DiffMix mix;   // differential attention; eps as the kernel adds it
+    float shrink;  // o by this before its norm (1 without one), eps by its square: sums of large squares stay in range
 };
 
 // The tensor maps of a launch: queries, keys, values; then the same of the own keys.
@@ -416,7 +417,7 @@ template <int D>
 __device__ __forceinline__ void write_difference(const RowsParams& p, float* join, int r, int i, size_t row, bool live,
                                                  float factor, bool some, uint32_t o_at) {
     constexpr int MINE = D / 2, STEP = 16;
-    join[i * 128 + r] = factor;
+    join[i * 128 + r] = factor * p.shrink;
     tc_fence_before();
     named_barrier(1, 256);  // (both O are complete: each warpgroup has waited for its own)
     tc_fence_after();
@@ -1467,6 +1468,7 @@ inline bool rows_setup(const RowsArgs& a, RowsParams& p, RowsMaps& m) {
     p.part_o = a.part_o;
     p.part_ml = a.part_ml;
     p.mix = DiffMix{};
+    p.shrink = 1.f;
     p.rec0 = a.rec0;
     p.rec_stride = a.rec_stride;
     p.direct = a.direct;
