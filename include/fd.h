@@ -595,11 +595,14 @@ FD_API int fd_append_kv_paged_rope_fp8(const void* q, const void* k, const void*
  * prompt calls may read a query after they have written to out.
  * A query that sees no key gets out = 0 and lse = -inf.  A visible score that is NaN
  * or +inf makes its row NaN; one of -inf weighs nothing.  Values of a query's
- * sequence have to be below 2^96 in magnitude and, in the prompt calls, below 2^80
- * (their sums over all keys stay in binary32, and the norm holds for all of them;
- * in the prompt calls with a norm_eps below 2^-60 only up to 2^56).
- * (The prompt calls take a part of the keys twice where scores rise more than 28
- * above those of its first 64 keys, or are not finite.)
+ * sequence, and lambda times them, have to be below 2^96 in magnitude and, in the
+ * prompt calls, below 2^80 (their sums over all keys stay in binary32, and the norm
+ * holds for all of them; in the prompt calls with a norm_eps below 2^-60 only up to
+ * 2^56).
+ * (The prompt calls weigh a row by the maximum m of its scores on the first 64 keys
+ * of its part, in either map.  Where sum_j exp(s_j - m) over the part reaches 2^40,
+ * 27.7 above m for one key, 13.9 for a plateau of 2^20 keys, or m is not finite,
+ * the row's tile of 128 rows goes over all keys of the part once more, slower.)
  * Scores, maxima, sums, the maps' outputs, their difference and its norm are
  * binary32.  The weights of either map enter the product with V as the other calls'
  * do: in two bf16 terms in the decode (2^-16), and in the prompt calls in two

@@ -500,7 +500,9 @@ __device__ __forceinline__ void write_difference(const RowsParams& p, float* joi
 //   * four warpgroups instead of two, each half of a unit's weights (2980) or every second unit (2650): registers
 //     spilled, and the chain from turn to turn stayed
 //   * weights in batches of four pairs: 2185 -> 2130
-constexpr float kMostSum = 1099511627776.f;  // 2^40: 28 above m, and values may be as large as 2^80
+// Of a row's sum of weights: 2^40, so that values may be as large as 2^80.  One score reaches it 27.7 (natural units) above
+// m, a plateau of n keys 27.7 - ln n: 18 with 16K of them, 14 with a million.
+constexpr float kMostSum = 1099511627776.f;
 
 template <int D, bool PAGED, bool FINE>
 __device__ __forceinline__ void softmax_maps(const RowsParams& p, const Work* work, volatile int* redo,
