@@ -7,6 +7,7 @@
 //   (y_a, y_b) <- (y_a cos - y_b sin, y_b cos + y_a sin)   for the pairs (a, b) of the
 //   first `rot` channels, cos and sin from row t of a table
 // in binary32, rounded once: to bf16, or to the e4m3 codes.
+#include <algorithm>
 #include <cstdint>
 #include <type_traits>
 
@@ -59,7 +60,6 @@ __device__ __forceinline__ int row_of(const RopeArgs& p, int t) {
             if (x == t) s = found;
         }
         const int a = p.cu[s], b = p.cu[s + 1];
-        if (a < 0 || a > b || b > p.T) atomicOr(&g_status_rope, kStatusBadSeqLen);
         if (t < a || t >= b) return -1;
         pos = (long long)p.lens[s] - b + t;
     }
@@ -68,6 +68,15 @@ __device__ __forceinline__ int row_of(const RopeArgs& p, int t) {
         pos = pos < 0 ? 0 : p.max_pos - 1;
     }
     return (int)pos;
+}
+
+// Reports offsets that run backwards or out of [0, T], those between which no token lies too.  Blocks of their own: within
+// the others the test cost the e4m3 append registers (118 -> 123 us).
+__device__ __forceinline__ void check_offsets(const RopeArgs& p, unsigned block, unsigned blocks) {
+    for (long long s = (long long)block * kThreads + threadIdx.x; s < p.B; s += (long long)blocks * kThreads) {
+        const int a = p.cu[s], b = p.cu[s + 1];
+        if (a < 0 || a > b || b > p.T) atomicOr(&g_status_rope, kStatusBadSeqLen);
+    }
 }
 
 // The 16 channels of a row that a lane holds: two runs of 8, which pair with each other (halves of
@@ -311,12 +320,17 @@ __device__ __forceinline__ bool rows_to_pages(const RopeArgs& p, int groups, uns
 
 enum { kToRows, kToPages, kToPagesFp8 };
 
-// The first q_blocks blocks take the queries, the others the keys (and values); RPT rows a thread, on the
-// way to pages RPP keys and their values.
+// The first q_blocks blocks take the queries, the others of work_blocks the keys (and values), any behind them the
+// offsets; RPT rows a thread, on the way to pages RPP keys and their values.
 template <int D, int DH, int TO, int RPT, int RPP>
-__global__ void __launch_bounds__(kThreads, kBlocksPerSM) rope_kernel(const RopeArgs p, unsigned q_blocks, int q_groups, int k_groups) {
+__global__ void __launch_bounds__(kThreads, kBlocksPerSM)
+rope_kernel(const RopeArgs p, unsigned q_blocks, int q_groups, int k_groups, unsigned work_blocks) {
     pdl_wait_primary();
     pdl_launch_dependents();
+    if (blockIdx.x >= work_blocks) {
+        check_offsets(p, blockIdx.x - work_blocks, gridDim.x - work_blocks);
+        return;
+    }
     // the rows of an operand, then those with squares that left binary32
     const auto to_rows = [&](auto norm, const uint16_t* in, long long stride, uint16_t* out, long long out_stride,
                              const float* weight, int H, int groups, unsigned block) {
@@ -361,11 +375,12 @@ cudaError_t launch(const RopeArgs& p, cudaStream_t stream) {
     const int qg = (p.Hq + RPT - 1) / RPT, kr = p.slots ? RPP : RPT, kg = (p.Hkv + kr - 1) / kr;
     const auto blocks = [&](int groups) { return ((long long)p.T * groups * (D / 16) + kThreads - 1) / kThreads; };
     const unsigned qb = (unsigned)blocks(qg);
-    const dim3 grid((unsigned)(qb + blocks(kg)));
+    const unsigned work = (unsigned)(qb + blocks(kg));
+    const dim3 grid(work + (p.positions ? 0u : (unsigned)std::min(((long long)p.B + kThreads - 1) / kThreads, 32LL)));
     const auto kernel = !p.slots      ? rope_kernel<D, DH, kToRows, RPT, RPP>
                         : p.k_scales ? rope_kernel<D, DH, kToPagesFp8, RPT, RPP>
                                      : rope_kernel<D, DH, kToPages, RPT, RPP>;
-    return launch_pdl(kernel, grid, dim3(kThreads), 0, stream, p, qb, qg, kg);
+    return launch_pdl(kernel, grid, dim3(kThreads), 0, stream, p, qb, qg, kg, work);
 }
 
 // One row a thread while all of them are on the GPU at once: more rows then only make each thread's chain
