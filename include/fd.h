@@ -567,7 +567,9 @@ FD_API int fd_append_kv_paged_rope(const void* q, const void* k, const void* v,
 
 /* The same into the paged fp8 cache: value rows as fd_append_kv_paged_fp8 encodes
  * them, key rows from their turned binary32 values by the same rule, s = max |y| / 448
- * and e4m3(y / s): one rounding. */
+ * and e4m3(y / s): one rounding.  A key row of nothing but NaN (a norm makes one of any
+ * NaN) keeps it: its scale is NaN too, where the rule alone would store zeros.  No
+ * differential call reads such a cache; `halves` is for callers with a reader of their own. */
 FD_API int fd_append_kv_paged_rope_fp8(const void* q, const void* k, const void* v,
                                        long long q_stride, long long k_stride, long long v_stride,
                                        const int64_t* slots, int T, int Hq, int Hkv, int d, const fd_rope* rope,

@@ -797,7 +797,7 @@ def fd_append_kv_paged_rope_fp8(q, k, v, slots, k_pages, k_page_scales, v_pages,
                                 norm_eps=1e-6, interleaved=False, halves=False, q_out=None, stream=None):
     """fd_append_kv_paged_rope into the paged fp8 cache (as
     fd_append_kv_paged_fp8; the keys are encoded from their turned float32
-    values).  Returns (q_out, k_pages, k_page_scales, v_pages, v_page_scales)."""
+    values).  No differential call reads this cache.  Returns (q_out, k_pages, k_page_scales, v_pages, v_page_scales)."""
     return _binding().append_rope_fp8(q, k, v, slots, k_pages, k_page_scales, v_pages, v_page_scales, cos_sin,
                                       positions, cu_seqlens, seq_lens, q_weight, k_weight, norm_eps, interleaved,
                                       halves, q_out, stream)

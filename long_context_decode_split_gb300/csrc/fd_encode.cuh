@@ -76,7 +76,8 @@ __device__ __forceinline__ void encode_row(const uint32_t (&w)[8], uint8_t* code
 
 // The same for a row in binary32 (rotated and not yet rounded): one rounding,
 // from these values to the codes.  The lane's 16 channels lie in two runs of 8 at
-// `at0` and `at1` of the row.  (A NaN's code is NaN with either sign.)  Where a lane's x is
+// `at0` and `at1` of the row.  (A NaN's code is NaN with either sign; a
+// row of nothing but NaN gets the scale NaN.)  Where a lane's x is
 // `worthless`, again(x, the row's lanes) makes them anew, in the branch that is there for rows
 // at the ends of the range.
 template <int C, typename Again>
