@@ -76,23 +76,22 @@ __device__ __forceinline__ void encode_row(const uint32_t (&w)[8], uint8_t* code
 
 // The same for a row in binary32 (rotated and not yet rounded): one rounding,
 // from these values to the codes.  The lane's 16 channels lie in two runs of 8 at
-// `at0` and `at1` of the row.  (A NaN's code is NaN with either sign; a
-// row of nothing but NaN gets the scale NaN.)  Where a lane's x is
-// `worthless`, again(x, the row's lanes) makes them anew, in the branch that is there for rows
-// at the ends of the range.
-template <int C, typename Again>
-__device__ __forceinline__ void encode_floats(float (&x)[16], bool worthless, Again again, uint8_t* codes, float* scale,
+// `at0` and `at1` of the row.  (A NaN's code is NaN with either sign; a row of nothing
+// but NaN gets the scale NaN.)  Returns, the same to the row's lanes, whether the row is
+// left for the EXACT form, which divides: its scale is near the ends of the range, or
+// a lane's x is `worthless`.
+template <int C, bool EXACT>
+__device__ __forceinline__ bool encode_floats(const float (&x)[16], bool worthless, uint8_t* codes, float* scale,
                                               bool live, int c, int at0, int at1) {
-    const auto largest = [&](float amax, unsigned lanes) {
+    float amax = !EXACT && worthless ? INFINITY : fabsf(x[0]);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(x[e]));
+    for (int e = 1; e < 16; ++e) amax = fmaxf(amax, fabsf(x[e]));
 #pragma unroll
-        for (int o = C / 2; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(lanes, amax, o));
-        return amax;
-    };
-    float s = largest(worthless ? INFINITY : fabsf(x[0]), 0xffffffffu) / 448.0f;
+    for (int o = C / 2; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    const float s = amax / 448.0f;
+    if (!EXACT && !(s > 1e-30f && s < 1e30f)) return live;
     uint32_t out[4];
-    if (s > 1e-30f && s < 1e30f) {
+    if constexpr (!EXACT) {
         const float r = 1.0f / s;
         const float2 s2 = make_float2(s, s), nr2 = make_float2(-r, -r);
 #pragma unroll
@@ -104,21 +103,17 @@ __device__ __forceinline__ void encode_floats(float (&x)[16], bool worthless, Ag
             out[e >> 1] = e & 1 ? (out[e >> 1] | pair << 16) ^ 0x80808080u : pair;
         }
     } else {
-        if (s == INFINITY) {
-            const unsigned lanes = ((1u << C) - 1u) << ((threadIdx.x & 31) / C * C);
-            again(x, lanes);
-            s = largest(fabsf(x[0]), lanes) / 448.0f;
-        }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const uint32_t pair = s != 0.f ? e4m3_pair(x[2 * e] / s, x[2 * e + 1] / s) : 0u;
             out[e >> 1] = e & 1 ? out[e >> 1] | pair << 16 : pair;
         }
     }
-    if (!live) return;
+    if (!live) return false;
     *reinterpret_cast<uint2*>(codes + at0) = make_uint2(out[0], out[1]);
     *reinterpret_cast<uint2*>(codes + at1) = make_uint2(out[2], out[3]);
     if (c == 0) *scale = s;
+    return false;
 }
 
 }  // namespace fd

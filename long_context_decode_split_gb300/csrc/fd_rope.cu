@@ -129,7 +129,7 @@ __device__ __forceinline__ void load_weights(Weights& w, const float* from, cons
 // it, by 2^-96 before its norm, in range whatever it is.
 template <int DH, bool NORM, bool LARGE>
 __device__ __forceinline__ bool turn(float (&x)[16], const uint4& a, const uint4& b, const RopeArgs& p, const Lane& l,
-                                     const Angles& g, const Weights& w, unsigned lanes = 0xffffffffu) {
+                                     const Angles& g, const Weights& w) {
     const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     float2 y[8];
 #pragma unroll
@@ -142,7 +142,7 @@ __device__ __forceinline__ bool turn(float (&x)[16], const uint4& a, const uint4
             for (int e = 0; e < 8; ++e) sum = f2fma(y[e], y[e], sum);
             float all = sum.x + sum.y;
 #pragma unroll
-            for (int o = DH / 32; o >= 1; o >>= 1) all += __shfl_xor_sync(lanes, all, o);
+            for (int o = DH / 32; o >= 1; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
             return all;
         };
         float all = squares(), eps = p.eps;
@@ -237,10 +237,11 @@ __device__ __forceinline__ unsigned rows_to_rows(const RopeArgs& p, const uint16
 }
 
 // Key rows of a token, turned, and its value rows to their slot of the pools: heads hg, hg + groups,
-// .. (all lanes together).  Returns whether the LARGE form has to write over one of them (bf16; e4m3 rows are encoded
-// again where their maximum tells so: that form beside them made the call 5% slower).
+// .. (all lanes together).  Returns which of the lane's key rows are left for the LARGE form: heads as above, e4m3
+// rows that have to be divided too.  That form writes no values.
 template <int D, int DH, int RPT, bool FP8, bool NORM, bool LARGE = false>
-__device__ __forceinline__ bool rows_to_pages(const RopeArgs& p, int groups, unsigned block, int from = 0) {
+__device__ __forceinline__ unsigned rows_to_pages(const RopeArgs& p, int groups, unsigned block, int from = 0,
+                                                  bool mine = true) {
     constexpr int C = D / 16;
     const int c = threadIdx.x % C;
     const unsigned item = block * (kThreads / C) + threadIdx.x / C;
@@ -260,8 +261,10 @@ __device__ __forceinline__ bool rows_to_pages(const RopeArgs& p, int groups, uns
         if (in_range && hg + h < p.Hkv) {
             a[u] = *reinterpret_cast<const uint4*>(kr + h * D + l.at0);
             b[u] = *reinterpret_cast<const uint4*>(kr + h * D + l.at1);
-            v0[u] = reinterpret_cast<const uint4*>(vr + h * D)[0];
-            v1[u] = reinterpret_cast<const uint4*>(vr + h * D)[1];
+            if (!LARGE) {
+                v0[u] = reinterpret_cast<const uint4*>(vr + h * D)[0];
+                v1[u] = reinterpret_cast<const uint4*>(vr + h * D)[1];
+            }
         } else {
             a[u] = b[u] = v0[u] = v1[u] = make_uint4(0u, 0u, 0u, 0u);
         }
@@ -279,7 +282,7 @@ __device__ __forceinline__ bool rows_to_pages(const RopeArgs& p, int groups, uns
     const size_t row0 = live ? (size_t)((slot / kTile * p.Hkv + hg) * kTile + slot % kTile) : 0;
     // the values first: they wait for no angles
 #pragma unroll
-    for (int u = 0; u < RPT; ++u) {
+    for (int u = 0; u < (LARGE ? 0 : RPT); ++u) {
         const bool wanted = live && hg + u * groups < p.Hkv;
         const size_t row = row0 + (size_t)u * groups * kTile;
         if constexpr (FP8) {
@@ -291,29 +294,22 @@ __device__ __forceinline__ bool rows_to_pages(const RopeArgs& p, int groups, uns
             vp[1] = v1[u];
         }
     }
-    bool left = false;
+    unsigned left = 0;
 #pragma unroll
     for (int u = 0; u < RPT; ++u) {
-        const bool wanted = live && hg + u * groups < p.Hkv;
+        const bool wanted = mine && live && hg + u * groups < p.Hkv;
         const size_t row = row0 + (size_t)u * groups * kTile;
         float x[16];
-        const bool large = turn<DH, NORM, LARGE>(x, a[u], b[u], p, l, g, w);
+        bool later = turn<DH, NORM, LARGE>(x, a[u], b[u], p, l, g, w);
         if constexpr (FP8) {
-            const auto again = [&](float (&y)[16], unsigned lanes) {
-                const uint16_t* at_row = kr + u * groups * D;
-                turn<DH, NORM, true>(y, *reinterpret_cast<const uint4*>(at_row + l.at0),
-                                     *reinterpret_cast<const uint4*>(at_row + l.at1), p, l, g, w, lanes);
-            };
-            encode_floats<C>(x, large, again, static_cast<uint8_t*>(p.k_pages) + row * D, p.k_scales + row, wanted, c,
-                             part + l.at0, part + l.at1);
-            continue;
-        }
-        left |= large;
-        if (wanted) {
+            later = encode_floats<C, LARGE>(x, later, static_cast<uint8_t*>(p.k_pages) + row * D, p.k_scales + row,
+                                            wanted, c, part + l.at0, part + l.at1);
+        } else if (wanted) {  // (what a large head leaves there is written over)
             uint16_t* kp = static_cast<uint16_t*>(p.k_pages) + row * D + part;
             *reinterpret_cast<uint4*>(kp + l.at0) = pack8(x);
             *reinterpret_cast<uint4*>(kp + l.at1) = pack8(x + 8);
         }
+        if (!LARGE && later) left |= 1u << u;
     }
     return left;
 }
@@ -358,15 +354,17 @@ rope_kernel(const RopeArgs p, unsigned q_blocks, int q_groups, int k_groups, uns
         else to_rows(without, p.k, p.k_stride, p.k_out, p.k_out_stride, nullptr, p.Hkv, k_groups, block);
     } else {
         constexpr bool FP8 = TO == kToPagesFp8;
-        if (!p.k_weight) {
-            rows_to_pages<D, DH, RPP, FP8, false>(p, k_groups, block);
-            return;
-        }
-        const bool left = rows_to_pages<D, DH, RPP, FP8, true>(p, k_groups, block);
-        if (!FP8 && __any_sync(0xffffffffu, left)) {
+        const auto to_pages = [&](auto norm) {
+            constexpr bool NORM = decltype(norm)::value;
+            unsigned left = rows_to_pages<D, DH, RPP, FP8, NORM>(p, k_groups, block);
+            if ((FP8 || NORM) && __any_sync(0xffffffffu, left != 0u)) {
 #pragma unroll 1
-            for (int u = 0; u < RPP; ++u) rows_to_pages<D, DH, 1, FP8, true, true>(p, k_groups, block, u * k_groups);
-        }
+                for (int u = 0; u < RPP; ++u, left >>= 1)
+                    rows_to_pages<D, DH, 1, FP8, NORM, true>(p, k_groups, block, u * k_groups, left & 1u);
+            }
+        };
+        if (p.k_weight) to_pages(with_norm);
+        else to_pages(without);
     }
 }
 
