@@ -21,11 +21,12 @@ __device__ unsigned int g_status_rope;
 
 namespace {
 
-// HBM bounds the large calls: 20.5K tokens of 32 + 8 heads of 128 with norms in 66.5 us (6.3 TB/s, rows read
-// and written), 32K tokens of them into the e4m3 cache in 116 us (6.1 TB/s).  What counts is the bytes that
+// HBM bounds the large calls: 20.5K tokens of 32 + 8 heads of 128 with norms in 67-70 us (6.0-6.3 TB/s, rows read
+// and written), 31K tokens of them into the e4m3 cache in 116-119 us (6.0-6.1 TB/s).  What counts is the bytes that
 // an SM has on their way: the chain behind a row (position, its angles) takes longer than the row itself.
-// Four rows a thread and six blocks of 128 threads an SM (80 registers) measured best: two rows 68.5 and
-// 122 us, four in three blocks of 256 69.6 and 127 us, one in four of 256 91 and 168 us.
+// Four rows a thread and six blocks of 128 threads an SM (80 registers, of which these forms spill 40 to 76 bytes)
+// measured best, where the kept one took 66.5 and 116: two rows 68.5 and 122 us, four in three blocks of 256 69.6
+// and 127 us, one in four of 256 91 and 168 us.
 constexpr int kThreads = 128, kBlocksPerSM = 6;
 
 // The token's sequence: the last s with cu[s] <= t.  All lanes together; each round every lane
@@ -238,7 +239,8 @@ __device__ __forceinline__ unsigned rows_to_rows(const RopeArgs& p, const uint16
 
 // Key rows of a token, turned, and its value rows to their slot of the pools: heads hg, hg + groups,
 // .. (all lanes together).  Returns which of the lane's key rows are left for the LARGE form: heads as above, e4m3
-// rows that have to be divided too.  That form writes no values.
+// rows that have to be divided too.  That form writes no values.  (Its code in a branch within the rows cost nothing in
+// a loop and 3% beside cold caches: 31K tokens 153.5 us instead of 149.)
 template <int D, int DH, int RPT, bool FP8, bool NORM, bool LARGE = false>
 __device__ __forceinline__ unsigned rows_to_pages(const RopeArgs& p, int groups, unsigned block, int from = 0,
                                                   bool mine = true) {
@@ -382,7 +384,7 @@ cudaError_t launch(const RopeArgs& p, cudaStream_t stream) {
 }
 
 // One row a thread while all of them are on the GPU at once: more rows then only make each thread's chain
-// longer (30 rows of three tokens 1.65 us, 2.07 us with four a thread).
+// longer (30 rows of three tokens 1.5-1.65 us, 2.07 us with four a thread).
 template <int D, int DH>
 cudaError_t launch_for(const RopeArgs& p, cudaStream_t stream) {
     int sms = 0, dev = 0;

@@ -487,8 +487,12 @@ __device__ __forceinline__ void write_difference(const RowsParams& p, float* joi
 // marks its piece, which the copy warp hands out once more, with care: then every unit raises m to its
 // maximum, and O is rescaled.
 //
-// What bounds it, and what each choice brought (32 query and 8 KV heads of 128, 16K tokens: 2.13-2.18 ms, 1.51-1.55
-// PFLOP/s of the 768 operations a pair; the tensor cores are busy 69% of the time, the exponentials' pipe 43%,
+// What that costs: 16K tokens (32 and 8 heads) 2.17 ms in one pass, 6.5 ms where every piece goes twice, 2.7 ms where
+// those of one KV head do; 8 prompts of 257 to 4095 664 us, 1900 and 900.  (The second pass rescales all of O in every
+// unit.)
+//
+// What bounds it, and what each choice brought (32 query and 8 KV heads of 128, 16K tokens: 2.06-2.18 ms, 1.51-1.60
+// PFLOP/s of the 768 operations a pair; the tensor cores are busy 70% of the time, the exponentials' pipe 44%,
 // and one instruction is issued in two cycles): the time of two softmax warps a scheduler, whose steps wait for
 // one another.  A unit takes them about 1100 cycles, its products 384 a map.
 //   * blocks of 128 keys, as for the other modes: 2400 us.  A map's products and its softmax then follow each other
@@ -497,8 +501,8 @@ __device__ __forceinline__ void write_difference(const RowsParams& p, float* joi
 //   * one room for scores and the queries in tensor memory beside it (S | P | Q: the scores' products take 32
 //     cycles instead of 48, and half of the shared memory's traffic), one wait and one arrival a unit: 2470
 //   * no maxima behind the first unit: 2165; the test of each unit's sum in their place cost more than them (2600)
-//   * four warpgroups instead of two, each half of a unit's weights (2980) or every second unit (2650): registers
-//     spilled, and the chain from turn to turn stayed
+//   * four warpgroups instead of two, each half of a unit's weights (2980) or every second unit (2650): more registers
+//     spilled (the kept kernels spill 76 to 108 bytes a thread), and the chain from turn to turn stayed
 //   * weights in batches of four pairs: 2185 -> 2130
 // Of a row's sum of weights: 2^40, so that values may be as large as 2^80.  One score reaches it 27.7 (natural units) above
 // m, a plateau of n keys 27.7 - ln n: 18 with 16K of them, 14 with a million.
